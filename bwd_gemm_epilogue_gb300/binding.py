@@ -1,8 +1,9 @@
-"""ctypes binding of the C ABI in ``include/swiglu_mlp.h`` and ``include/swiglu_moe.h``
--- argument marshalling only.
+"""ctypes binding of the C ABI in ``include/swiglu_mlp.h``, ``include/swiglu_moe.h`` and
+``include/swiglu_ops.h`` -- argument marshalling only.
 
 Each function has the name of the C entry point it calls and takes torch CUDA
-tensors (bf16, contiguous) for the pointer arguments; torch supplies device
+tensors for the pointer arguments (bf16, contiguous; the operators of
+``swiglu_ops.h`` also take fp16 and fp32, and rows at a stride); torch supplies device
 memory and the current stream, every step of the computation runs in the
 library's kernels.  Outputs and workspaces the caller does not pass are
 allocated with torch.  A non-OK status raises ``SwigluError``; a missing
@@ -30,7 +31,8 @@ STATUS_NAMES = {
     7: "SWIGLU_ERR_CUDA",
 }
 
-# Every symbol include/swiglu_mlp.h and include/swiglu_moe.h declare: name -> (restype, argtypes)
+# Every symbol the headers under include/ declare: name -> (restype, argtypes)
+_f32 = ctypes.c_float
 _vp, _i64, _i32, _u64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64, ctypes.c_size_t
 SIGNATURES = {
     "swiglu_mlp_fwd_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
@@ -66,10 +68,18 @@ SIGNATURES = {
     "swiglu_moe_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _sz, _vp]),
     "swiglu_moe_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _sz,
                               _vp]),
+    "swiglu_mlp_layer_norm_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
+                                         _f32, _i32, _i32, _vp]),
+    "swiglu_mlp_layer_norm_bwd_workspace_size": (_sz, [_i64, _i64]),
+    "swiglu_mlp_layer_norm_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64,
+                                         _i64, _i32, _i32, _vp, _sz, _vp]),
+    "swiglu_mlp_clip_grads_workspace_size": (_sz, [_i64]),
+    "swiglu_mlp_clip_grads": (_i32, [_vp, _vp, _vp, _vp, _i64, _f32, _f32, _vp, _vp, _sz, _vp]),
 }
 
 KERNEL_KINDS = {1: "fwd_preact", 2: "fwd_down", 3: "bwd_grad_h", 4: "bwd_dW2", 5: "bwd_dx", 6: "bwd_dW1", 7: "gemm",
-                8: "bwd_gemms", 9: "elementwise"}
+                8: "bwd_gemms", 9: "elementwise", 10: "norm_fwd", 11: "norm_bwd", 12: "norm_params", 13: "grad_norm",
+                14: "grad_scale", 15: "moe_route", 16: "moe_up", 17: "moe_down"}
 
 
 class SwigluError(RuntimeError):
@@ -560,3 +570,224 @@ def swiglu_moe_bwd(x, W1, W2, preact, dy, counts, dx=None, dW1=None, dW2=None, w
                               _nbytes(workspace), _stream(x.device))
     _check(st, "swiglu_moe_bwd")
     return dx, dW1, dW2
+
+
+# ---------------------------------------------------------------------------- layer norm
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}      # swiglu_dtype
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: {t.dtype}, expected bf16, fp16 or fp32")
+    return code
+
+
+def _rows(t, name: str, shape, like: torch.Tensor):
+    """(pointer, row stride) of a [M, D] tensor whose rows are contiguous; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t is not like:
+        _expect(t, name, shape, like.dtype, like.device)
+    ld = t.stride(0) if shape[0] > 1 else shape[1]
+    if (shape[1] > 1 and t.stride(1) != 1) or ld < shape[1]:
+        raise ValueError(f"{name}: each row must be contiguous and rows must not overlap (strides {t.stride()})")
+    return t.data_ptr(), ld
+
+
+def _device_stream(device) -> ctypes.c_void_p:
+    """The current stream of `device`, refused where that is no CUDA device."""
+    if device.type != "cuda":
+        raise ValueError("tensor must live on a CUDA device")
+    return _stream(device)
+
+
+def _vector(t, name: str, n: int, dtype, like: torch.Tensor):
+    """Pointer of a contiguous vector of n elements, or None."""
+    if t is None:
+        return None
+    _expect(t, name, (n,), dtype, like.device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _norm_params(x, gamma, beta):
+    """dtype of gamma and beta (x's, where there are none)."""
+    wdtype = gamma.dtype if gamma is not None else beta.dtype if beta is not None else x.dtype
+    if wdtype not in (x.dtype, torch.float32):
+        raise TypeError(f"gamma, beta: {wdtype}, expected {x.dtype} or torch.float32")
+    return wdtype
+
+
+def swiglu_mlp_layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, y=None, s=None, mean=None,
+                              rstd=None):
+    """Layer norm of x (+ residual); returns (y, s, mean, rstd): s is x + residual, or x itself
+    without a residual; mean, rstd [M] fp32 are what the backward takes.  x, residual, y, s
+    [M, D] bf16, fp16 or fp32, rows at any stride; gamma, beta [D] of x's type or fp32."""
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected two dimensions")
+    M, D = x.shape
+    code, wdtype = _dtype(x, "x"), _norm_params(x, gamma, beta)
+    if s is not None and residual is None:
+        raise ValueError("s: only written with a residual")
+    y = torch.empty((M, D), dtype=x.dtype, device=x.device) if y is None else y
+    if residual is not None and s is None:
+        s = torch.empty((M, D), dtype=x.dtype, device=x.device)
+    if mean is None:
+        mean = torch.empty(M, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    px, ldx = _rows(x, "x", (M, D), x)
+    pr, ldr = _rows(residual, "residual", (M, D), x)
+    py, ldy = _rows(y, "y", (M, D), x)
+    ps, lds = _rows(s, "s", (M, D), x)
+    st = lib().swiglu_mlp_layer_norm_fwd(px, ldx, pr, ldr, _vector(gamma, "gamma", D, wdtype, x),
+                                         _vector(beta, "beta", D, wdtype, x), py, ldy, ps, lds,
+                                         _vector(mean, "mean", M, torch.float32, x),
+                                         _vector(rstd, "rstd", M, torch.float32, x), M, D, eps, code, _DTYPES[wdtype],
+                                         _device_stream(x.device))
+    _check(st, "swiglu_mlp_layer_norm_fwd")
+    return y, (x if s is None else s), mean, rstd
+
+
+def swiglu_mlp_layer_norm_bwd_workspace_size(M: int, D: int) -> int:
+    return int(lib().swiglu_mlp_layer_norm_bwd_workspace_size(M, D))
+
+
+def swiglu_mlp_layer_norm_bwd(dy, s, gamma, mean, rstd, dskip=None, dx=None, dgamma=None, dbeta=None, workspace=None,
+                              param_grads: bool = True):
+    """Backward of the layer norm; returns (dx, dgamma, dbeta).  s: the forward's normalised
+    input; dskip: a gradient added to dx (the residual stream's).  gamma None (= 1): dgamma
+    and dbeta have the type of the dbeta passed in, or s's.  param_grads False: neither is computed and both are None."""
+    if s.dim() != 2:
+        raise ValueError(f"s: shape {tuple(s.shape)}, expected two dimensions")
+    M, D = s.shape
+    code, wdtype = _dtype(s, "s"), _norm_params(s, gamma, dbeta)
+    dx = torch.empty((M, D), dtype=s.dtype, device=s.device) if dx is None else dx
+    if param_grads:
+        dgamma = _out(dgamma, "dgamma", (D,), s, wdtype)
+        dbeta = _out(dbeta, "dbeta", (D,), s, wdtype)
+    elif dgamma is not None or dbeta is not None:
+        raise ValueError("dgamma, dbeta: not computed with param_grads=False")
+    _same_device(s, workspace=workspace)
+    if workspace is None:
+        workspace = torch.empty(max(16, swiglu_mlp_layer_norm_bwd_workspace_size(M, D)), dtype=torch.uint8,
+                                device=s.device)
+    pdy, lddy = _rows(dy, "dy", (M, D), s)
+    ps, lds = _rows(s, "s", (M, D), s)
+    pk, ldk = _rows(dskip, "dskip", (M, D), s)
+    pdx, lddx = _rows(dx, "dx", (M, D), s)
+    st = lib().swiglu_mlp_layer_norm_bwd(pdy, lddy, ps, lds, _vector(gamma, "gamma", D, wdtype, s),
+                                         _vector(mean, "mean", M, torch.float32, s),
+                                         _vector(rstd, "rstd", M, torch.float32, s), pk, ldk, pdx, lddx,
+                                         _vector(dgamma, "dgamma", D, wdtype, s),
+                                         _vector(dbeta, "dbeta", D, wdtype, s), M, D, code, _DTYPES[wdtype],
+                                         _ptr(workspace), _nbytes(workspace), _device_stream(s.device))
+    _check(st, "swiglu_mlp_layer_norm_bwd")
+    return dx, dgamma, dbeta
+
+
+class LayerNorm(torch.autograd.Function):
+    """autograd wrapper: y without a residual, (y, s) with one; the gradient reaching s past
+    the norm is then added to dx in the backward kernel.  Leading dimensions are flattened."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, beta, eps, residual):
+        y, s, mean, rstd = swiglu_mlp_layer_norm_fwd(_flat_rows(x), gamma, beta, eps,
+                                                     None if residual is None else _flat_rows(residual))
+        ctx.save_for_backward(s, gamma, mean, rstd)
+        ctx.beta_dtype = None if beta is None else beta.dtype
+        ctx.residual = residual is not None
+        ctx.set_materialize_grads(False)
+        return (y.reshape(x.shape), s.reshape(x.shape)) if ctx.residual else y.reshape(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy, ds=None):
+        s, gamma, mean, rstd = ctx.saved_tensors
+        if dy is None:
+            return ds, None, None, None, ds
+        dbeta = None if ctx.beta_dtype is None else torch.empty(s.shape[1], dtype=ctx.beta_dtype, device=s.device)
+        want = gamma is not None or dbeta is not None
+        dx, dgamma, _ = swiglu_mlp_layer_norm_bwd(_flat_rows(dy), s, gamma, mean, rstd,
+                                                  None if ds is None else _flat_rows(ds), dbeta=dbeta,
+                                                  param_grads=want)
+        dx = dx.reshape(dy.shape)
+        return dx, None if gamma is None else dgamma, dbeta, None, dx if ctx.residual else None
+
+
+def _flat_rows(t):
+    """[..., D] as [M, D] with contiguous, non-overlapping rows (a copy where the strides forbid it)."""
+    t = t.reshape(-1, t.shape[-1])
+    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+
+
+def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, residual=None):
+    """(y, s): the layer norm of s = x + residual, and s (x itself without a residual)."""
+    out = LayerNorm.apply(x, gamma, beta, eps, residual)
+    return out if residual is not None else (out, x)
+
+
+# ---------------------------------------------------------------------------- gradient clipping
+
+def swiglu_mlp_clip_grads_workspace_size(n: int) -> int:
+    return int(lib().swiglu_mlp_clip_grads_workspace_size(n))
+
+
+def _grad_arrays(tensors, name: str):
+    """Host arrays (pointers, counts, types) of dense CUDA tensors."""
+    n = len(tensors)
+    ptrs, counts, types = (ctypes.c_void_p * n)(), (_i64 * n)(), (_i32 * n)()
+    device = None
+    for i, t in enumerate(tensors):
+        if t.device != device:
+            if device is not None:
+                raise ValueError(f"{name}[{i}]: on {t.device}, the call's other tensors are on {device}")
+            device = t.device
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}]: tensor must be contiguous")
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name}[{i}]: {t.dtype}, expected bf16, fp16 or fp32")
+        ptrs[i], counts[i], types[i] = t.data_ptr(), t.numel(), code
+    return ptrs, counts, types, device
+
+
+def _clip_call(grads, max_norm, eps, out, norm, workspace):
+    if not grads:
+        raise ValueError("grads: empty")
+    ptrs, counts, types, device = _grad_arrays(grads, "grads")
+    outs = None
+    if out is grads:
+        outs = ptrs
+    elif out is not None:
+        outs, ocounts, otypes, odevice = _grad_arrays(out, "out")
+        if len(out) != len(grads) or odevice != device or ocounts[:] != counts[:] or otypes[:] != types[:]:
+            raise ValueError("out: one tensor of the same type, element count and device for each gradient")
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=device)
+    else:
+        _expect(norm, "norm", (), torch.float32, device)
+    if workspace is None:
+        workspace = torch.empty(swiglu_mlp_clip_grads_workspace_size(len(grads)), dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace: on {workspace.device}, the call's other tensors are on {device}")
+    st = lib().swiglu_mlp_clip_grads(ptrs, outs, counts, types, len(grads), max_norm, eps, norm.data_ptr(),
+                                     _ptr(workspace), _nbytes(workspace), _device_stream(device))
+    _check(st, "swiglu_mlp_clip_grads")
+    return norm
+
+
+def swiglu_mlp_clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm=None, workspace=None):
+    """Clip gradients by their global norm; returns (norm, clipped gradients).  The result
+    goes to `out` (a list like grads), or into grads themselves when out is None.  norm: fp32
+    scalar on the device, of the gradients before clipping (no host synchronisation)."""
+    grads = list(grads)
+    dst = grads if out is None else list(out)
+    return _clip_call(grads, float(max_norm), float(eps), dst, norm, workspace), dst
+
+
+def swiglu_mlp_grad_norm(grads, norm=None, workspace=None):
+    """Global norm of gradients alone (swiglu_mlp_clip_grads without outputs)."""
+    return _clip_call(list(grads), 0.0, 0.0, None, norm, workspace)

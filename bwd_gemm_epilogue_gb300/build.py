@@ -1,6 +1,6 @@
 """Compile the CUDA library (``libswiglu_mlp.so``) in-tree for sm_103a with nvcc.
 
-One translation unit per file of ``csrc/*.cu``, compiled in parallel and linked
+One translation unit per file of ``csrc/*.cu`` and ``csrc/ops/*.cu``, compiled in parallel and linked
 into one shared library with the CUDA runtime linked statically.  Rebuilds only
 when a source or header is newer than the library.
 """
@@ -33,7 +33,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    deps = glob.glob(os.path.join(CSRC, "*.*")) + glob.glob(os.path.join(CSRC, "ops", "*.*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -42,7 +42,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     nvcc = _nvcc()
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "ops", "*.cu")))
 
     def compile_one(src):
         obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")

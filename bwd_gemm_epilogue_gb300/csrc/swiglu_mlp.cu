@@ -17,11 +17,28 @@
 #include <mutex>
 
 #include "gemm_kernel.cuh"
+#include "host.h"
 #include "skinny_kernel.cuh"
 #include "swiglu_mlp.h"
 #include "swiglu_moe.h"
 
 namespace swiglu {
+
+thread_local Trace g_trace;
+
+namespace {
+// Last failure on this thread, for swiglu_mlp_last_error_detail.
+thread_local char g_detail[256];
+}  // namespace
+
+swiglu_status fail(swiglu_status st, const char* what, cudaError_t err) {
+    if (err != cudaSuccess)
+        std::snprintf(g_detail, sizeof g_detail, "%s: %s (%s)", what, cudaGetErrorName(err), cudaGetErrorString(err));
+    else
+        std::snprintf(g_detail, sizeof g_detail, "%s", what);
+    return st;
+}
+
 namespace {
 
 constexpr int kMaxDevices = 64;
@@ -42,25 +59,6 @@ struct DeviceState {
     int num_sms = 0;
     int* err_word = nullptr;
 };
-
-struct Trace {
-    cudaEvent_t* events = nullptr;
-    int* kinds = nullptr;
-    int capacity = 0;
-    int count = 0;
-};
-thread_local Trace g_trace;
-
-// Last failure on this thread, for swiglu_mlp_last_error_detail.
-thread_local char g_detail[256];
-
-swiglu_status fail(swiglu_status st, const char* what, cudaError_t err = cudaSuccess) {
-    if (err != cudaSuccess)
-        std::snprintf(g_detail, sizeof g_detail, "%s: %s (%s)", what, cudaGetErrorName(err), cudaGetErrorString(err));
-    else
-        std::snprintf(g_detail, sizeof g_detail, "%s", what);
-    return st;
-}
 
 std::mutex g_mutex;
 EncodeTiledFn g_encode = nullptr;
@@ -95,8 +93,6 @@ swiglu_status get_device_state(DeviceState** out) {
     *out = &st;
     return SWIGLU_OK;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // 2-D bf16 tensor map: `inner` contiguous elements per row, `outer` rows, row
 // pitch `row_bytes`.
@@ -354,26 +350,6 @@ constexpr int DEBUG_NO_SKINNY = 8;
 
 bool use_skinny(int64_t M) { return M >= 1 && M <= SK_MAX_M && !(g_debug_flags.load() & DEBUG_NO_SKINNY); }
 int64_t skinny_ld(int64_t M) { return (M + 15) / 16 * 16; }
-
-template <class F>
-swiglu_status launch_traced(int kind, cudaStream_t stream, F&& do_launch) {
-    Trace& tr = g_trace;
-    const int slot = tr.events ? tr.count++ : -1;
-    const bool traced = slot >= 0 && slot < tr.capacity;
-    cudaError_t e;
-    if (traced) {
-        tr.kinds[slot] = kind;
-        e = cudaEventRecord(tr.events[2 * slot], stream);
-        if (e != cudaSuccess) return fail(SWIGLU_ERR_CUDA, "cudaEventRecord(trace)", e);
-    }
-    e = do_launch();
-    if (e != cudaSuccess) return fail(SWIGLU_ERR_LAUNCH, "kernel launch", e);
-    if (traced) {
-        e = cudaEventRecord(tr.events[2 * slot + 1], stream);
-        if (e != cudaSuccess) return fail(SWIGLU_ERR_CUDA, "cudaEventRecord(trace)", e);
-    }
-    return SWIGLU_OK;
-}
 
 // Split-K plan of one small-M product with N weight rows and reduction length K: the
 // fewest splits whose makespan ceil(tiles * s / SMs) / s (in whole-K tiles) is within 2 %
@@ -891,6 +867,15 @@ swiglu_status run_gemm_group(DeviceState* st, int kind, const GemmSpec* g, int n
 }  // namespace swiglu
 
 using namespace swiglu;
+
+namespace swiglu {
+swiglu_status device_sms(int* num_sms) {
+    DeviceState* st;
+    swiglu_status rc = get_device_state(&st);
+    if (rc == SWIGLU_OK) *num_sms = st->num_sms;
+    return rc;
+}
+}  // namespace swiglu
 
 extern "C" {
 

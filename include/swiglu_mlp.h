@@ -329,7 +329,15 @@ typedef enum {
     SWIGLU_KERNEL_BWD_DW1 = 6,      /* dW1 = grad_preact^T @ x */
     SWIGLU_KERNEL_GEMM = 7,         /* swiglu_mlp_gemm_bf16 */
     SWIGLU_KERNEL_BWD_GEMMS = 8,    /* dW2, dx and dW1 in one launch (the backward's default) */
-    SWIGLU_KERNEL_ELEMENTWISE = 9   /* small-M path: SwiGLU forward/backward or cast of fp32 sums */
+    SWIGLU_KERNEL_ELEMENTWISE = 9,  /* small-M path: SwiGLU forward/backward or cast of fp32 sums */
+    SWIGLU_KERNEL_NORM_FWD = 10,    /* layer norm forward (swiglu_ops.h) */
+    SWIGLU_KERNEL_NORM_BWD = 11,    /* layer norm backward: dx and partial sums of dgamma, dbeta */
+    SWIGLU_KERNEL_NORM_PARAMS = 12, /* layer norm backward: dgamma and dbeta from the partial sums */
+    SWIGLU_KERNEL_GRAD_NORM = 13,   /* partial sums of squares of gradients */
+    SWIGLU_KERNEL_GRAD_SCALE = 14,  /* global norm and clipped gradients */
+    SWIGLU_KERNEL_MOE_ROUTE = 15,   /* routed MoE layer (swiglu_moe.h): router and choice of experts */
+    SWIGLU_KERNEL_MOE_UP = 16,      /* routed MoE layer: x @ W1^T and SwiGLU of the chosen experts */
+    SWIGLU_KERNEL_MOE_DOWN = 17     /* routed MoE layer: h @ W2^T, weighted and added per token */
 } swiglu_kernel_kind;
 
 /*
