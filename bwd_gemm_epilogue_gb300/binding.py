@@ -68,6 +68,9 @@ SIGNATURES = {
     "swiglu_moe_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _sz, _vp]),
     "swiglu_moe_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _sz,
                               _vp]),
+    "swiglu_moe_routed_fwd_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "swiglu_moe_routed_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _i32,
+                                     _i32, _vp, _sz, _vp]),
     "swiglu_mlp_layer_norm_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
                                          _f32, _i32, _i32, _vp]),
     "swiglu_mlp_layer_norm_bwd_workspace_size": (_sz, [_i64, _i64]),
@@ -570,6 +573,40 @@ def swiglu_moe_bwd(x, W1, W2, preact, dy, counts, dx=None, dW1=None, dW2=None, w
                               _nbytes(workspace), _stream(x.device))
     _check(st, "swiglu_moe_bwd")
     return dx, dW1, dW2
+
+
+def swiglu_moe_routed_fwd_workspace_size(T: int, H: int, top_k: int) -> int:
+    return int(lib().swiglu_moe_routed_fwd_workspace_size(T, H, top_k))
+
+
+def swiglu_moe_routed_fwd(x, Wr, W1, W2, top_k: int, renormalize: bool = True, residual=None, y=None, ids=None,
+                          gates=None, workspace=None):
+    """A whole MoE layer for up to 64 tokens, routed on the device: returns (y [T,Dout] bf16,
+    ids [T,top_k] int32, gates [T,top_k] fp32).  Wr [E,D] bf16 or fp32; residual [T,Dout] is
+    added to y; renormalize: the chosen gates sum to one."""
+    T, E, D, H, Dout = _moe_dims(x, W1, W2)
+    if Wr.dtype != torch.float32:
+        _expect(Wr, "Wr", (E, D), torch.bfloat16, x.device)
+    else:
+        _expect(Wr, "Wr", (E, D), torch.float32, x.device)
+    if residual is not None:
+        _expect(residual, "residual", (T, Dout), torch.bfloat16, x.device)
+    y = _out(y, "y", (T, Dout), x)
+    ids = _out(ids, "ids", (T, top_k), x, torch.int32)
+    gates = _out(gates, "gates", (T, top_k), x, torch.float32)
+    _same_device(x, workspace=workspace)
+    if workspace is None:
+        workspace = torch.empty(max(16, swiglu_moe_routed_fwd_workspace_size(T, H, top_k)), dtype=torch.uint8,
+                                device=x.device)
+    for name, t in (("Wr", Wr), ("ids", ids), ("gates", gates)):
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+    st = lib().swiglu_moe_routed_fwd(_ptr(x), Wr.data_ptr(), _ptr(W1), _ptr(W2), _ptr(residual), _ptr(y),
+                                     ids.data_ptr(), gates.data_ptr(), T, E, D, H, Dout, top_k, int(renormalize),
+                                     int(Wr.dtype == torch.float32), _ptr(workspace), _nbytes(workspace),
+                                     _stream(x.device))
+    _check(st, "swiglu_moe_routed_fwd")
+    return y, ids, gates
 
 
 # ---------------------------------------------------------------------------- layer norm

@@ -65,6 +65,40 @@ swiglu_status swiglu_moe_bwd(const void* x, const void* W1, const void* W2, cons
                              const int64_t* counts, int64_t E, int64_t D, int64_t H, int64_t Dout,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * A whole MoE layer for a few tokens (T <= 64, the decode regime): router, choice of
+ * experts, the chosen experts' SwiGLU blocks and the weighted sum, with the routing on the
+ * device.  No host arrays, no host synchronisation, fit for stream capture.
+ *
+ *   x [T, D]                       tokens, in any order
+ *   Wr [E, D]                      router weights: bf16, or fp32 when router_fp32 is not 0
+ *   W1 [E, 2H, D], W2 [E, Dout, H] stacked expert weights (bf16, as above)
+ *   residual [T, Dout]             bf16, added to y; NULL: none
+ *   y [T, Dout]                    bf16 output
+ *   ids, gates [T, top_k]          int32 and fp32 outputs: the chosen experts and their
+ *                                  weights, by falling logit
+ *
+ *   l = x @ Wr^T,  p = softmax(l) over the E experts;  the top_k largest p are chosen, ties
+ *   going to the lowest index (NaN logits rank lowest), gate = p, divided by the sum of the
+ *   chosen p when renormalize is not 0
+ *   y_t = (residual_t) + sum_j gate_tj * W2[e] (left * silu(gate')),
+ *         [left | gate'] = W1[e] x_t,  e = ids_tj
+ *
+ * Products accumulate in fp32; left, gate' and silu stay fp32, h = left * silu(gate') is
+ * rounded to bf16 once (it is the down product's operand), y once.  (The block's forward
+ * also rounds preact, which it saves.)  Only the chosen experts' weights are read, each
+ * once however many tokens chose it.  Sums have a fixed order: the same call returns the
+ * same bits on every run.
+ *   Needs T in 0..64, E in 1..682, top_k in 1..min(E, 16), widths as above (below 2^24).
+ *   workspace >= swiglu_moe_routed_fwd_workspace_size bytes (h [T * top_k, H] bf16).
+ */
+size_t swiglu_moe_routed_fwd_workspace_size(int64_t T, int64_t H, int64_t top_k);
+
+swiglu_status swiglu_moe_routed_fwd(const void* x, const void* Wr, const void* W1, const void* W2,
+                                    const void* residual, void* y, int32_t* ids, float* gates, int64_t T, int64_t E,
+                                    int64_t D, int64_t H, int64_t Dout, int64_t top_k, int renormalize,
+                                    int router_fp32, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

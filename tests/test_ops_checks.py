@@ -136,3 +136,39 @@ def test_clip_argument_errors(b):
     assert clip(ptrs=(A + 1, A)) == MISALIGNED and clip(ptrs=(A, A + 2)) == MISALIGNED
     assert clip(max_norm=-1.0) == INVALID and clip(max_norm=float("nan")) == INVALID and clip(eps=-1.0) == INVALID
     assert clip(norm=A + 2) == MISALIGNED
+
+
+def test_routed_layer_refusals(b):
+    E, H, Do, k = 5, 24, 32, 2
+    x, Wr, W1, W2 = z(M, D), z(E, D), z(E, 2 * H, D), z(E, Do, H)
+    f = b.swiglu_moe_routed_fwd
+    for call, err, match in [
+        (lambda: f(x, Wr, W1, W2, k), ValueError, CUDA),
+        (lambda: f(x, Wr.float(), W1, W2, k, residual=z(M, Do)), ValueError, CUDA),
+        (lambda: f(x, z(E + 1, D), W1, W2, k), ValueError, "Wr: shape"),
+        (lambda: f(x, Wr.half(), W1, W2, k), TypeError, "Wr: torch.float16"),
+        (lambda: f(x.float(), Wr, W1, W2, k), TypeError, "x: torch.float32"),
+        (lambda: f(x, Wr, W1, z(E, Do, H + 8), k), ValueError, "shape mismatch"),
+        (lambda: f(x, Wr, W1, W2, k, residual=z(M, D)), ValueError, "residual: shape"),
+        (lambda: f(x, Wr, W1, W2, k, y=z(M, D)), ValueError, "y: shape"),
+        (lambda: f(x, Wr, W1, W2, k, ids=z(M, k, dtype=torch.int64)), TypeError, "ids: torch.int64"),
+        (lambda: f(x, Wr, W1, W2, k, gates=z(M, k)), TypeError, "gates: torch.bfloat16"),
+        (lambda: f(x, z(D, E).T, W1, W2, k), ValueError, "Wr: must be contiguous"),
+    ]:
+        with pytest.raises(err, match=match):
+            call()
+
+    L = b.lib()
+
+    def call(x=A, wr=A, r=None, y=A, ids=A, gates=A, T=4, E=8, D=64, H=64, Do=64, k=2, ws=A, wsb=1 << 30):
+        return L.swiglu_moe_routed_fwd(x, wr, A, A, r, y, ids, gates, T, E, D, H, Do, k, 1, 0, ws, wsb, None)
+
+    assert call(T=0) == 0
+    assert call(T=-1) == INVALID and call(k=0) == INVALID and call(k=9) == INVALID and call(E=0) == INVALID
+    assert call(T=65) == SHAPE and call(E=683) == SHAPE and call(E=64, k=17) == SHAPE and call(D=60) == SHAPE
+    assert call(H=1 << 24) == SHAPE
+    assert call(x=None) == INVALID and call(gates=None) == INVALID and call(ws=None) == INVALID
+    assert call(wr=A + 8) == MISALIGNED and call(r=A + 2) == MISALIGNED and call(ids=A + 2) == MISALIGNED
+    need = b.swiglu_moe_routed_fwd_workspace_size(4, 64, 2)
+    assert need == 4 * 2 * 64 * 2 and call(wsb=need - 1) == WS
+    assert b.swiglu_moe_routed_fwd_workspace_size(0, 64, 2) == 0
