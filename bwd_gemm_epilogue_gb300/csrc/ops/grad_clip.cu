@@ -71,10 +71,11 @@ __device__ __forceinline__ Acc squares(const T* p, int64_t n) {
     const int packs = (int)((n - head) / V);
 #pragma unroll 4
     for (int i = threadIdx.x; i < packs; i += kThreads) {
-        const Pack<T, V> k = load_pack<T, V>(q + (int64_t)i * V);
+        float v[V];
+        load_pack<T, V>(q + (int64_t)i * V).unpack(v);
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
-            const Acc a = to_f32(k.v[j]), b = to_f32(k.v[j + 1]);
+            const Acc a = v[j], b = v[j + 1];
             s0 += a * a;
             s1 += b * b;
         }
@@ -141,10 +142,10 @@ __device__ __forceinline__ void scale_chunk(const T* p, T* o, int64_t n, float f
     const int packs = (int)((n - head) / V);
 #pragma unroll 4
     for (int i = threadIdx.x; i < packs; i += kThreads) {
-        const Pack<T, V> k = load_pack<T, V>(p + head + (int64_t)i * V);
         float v[V];
+        load_pack<T, V>(p + head + (int64_t)i * V).unpack(v);
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = to_f32(k.v[j]) * f;
+        for (int j = 0; j < V; ++j) v[j] *= f;
         store_pack<T, V>(o + head + (int64_t)i * V, v);
     }
     const int64_t tail = head + (int64_t)packs * V;

@@ -1,11 +1,18 @@
 // layer_norm.cu -- layer norm forward and backward (include/swiglu_ops.h).
 //
 // Both directions are bound by HBM: a row is read once into registers, its statistics are
-// reduced there, and the result is written once.  A row belongs to `lanes` threads, each
-// holding CPT of its columns as packs of VEC elements (pack i of lane l is columns
-// (i * lanes + l) * VEC ...), and a CTA walks rows blockIdx, blockIdx + gridDim, ...,
-// loading its next row before it reduces the current one, so that loads stay in flight
-// through the reductions.
+// reduced there, and the result is written once.  At the HBM rate an SM has about 40
+// instructions a column for all of it, so what a row costs besides its columns has to be
+// spread over many of them, and the columns' arithmetic runs in packed pairs: a row belongs
+// to a group of `lanes` threads with NV packs of 16 bytes each (pack k = q * lanes + lane of
+// the row, q < NV), and a group walks its own rows, with the next two in flight to shared
+// memory (registers could hold one, and its latency showed: 92 us backward instead of
+// the ring's for 11136 x 3584 bf16).
+//
+// Rows that do not start on 16-byte boundaries (odd widths, strides, bases) move in aligned
+// 16-byte pieces all the same: each lane copies the aligned piece its pack starts in, takes
+// the rest from its neighbour's and shifts the two together; stores likewise, with single
+// elements at the ends of a warp's span.
 #include "../host.h"
 #include "convert.cuh"
 #include "swiglu_ops.h"
@@ -14,9 +21,8 @@ namespace swiglu {
 namespace {
 
 constexpr int kPlanSms = 152;      // grids are planned for the GB300, so that the workspace query sees no device
-constexpr int kMaxThreads = 1024;
-constexpr int kMaxWidthFwd = 16384;   // widest rows held in registers: 1024 threads x 16 columns forward,
-constexpr int kMaxWidthBwd = 8192;    // 8 backward, whose threads also hold two column sums for each column
+constexpr int kMaxThreads = 512;   // the forms for rows too wide for registers
+constexpr int kBwdThreads = 512;
 
 struct NormFwd {
     const void *x, *r, *gamma, *beta;
@@ -36,7 +42,462 @@ struct NormBwd {
     int D, lanes, gf32;
 };
 
-// gamma or beta at column `col`, in the row's type or in fp32.
+// ---------------------------------------------------------------- 16-byte packs of a row
+
+template <class T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// The first `n` elements of a partial pack, the others zero.
+template <class T>
+__device__ __forceinline__ void keep_first(F2* v, int n) {
+#pragma unroll
+    for (int i = 0; i < kVec<T> / 2; ++i) {
+        const float2 f = split(v[i]);
+        v[i] = f2(2 * i < n ? f.x : 0.f, 2 * i + 1 < n ? f.y : 0.f);
+    }
+}
+
+// 16 bytes from byte s (0 < s < 16, a multiple of the element) of the 32 bytes a, b.
+__device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, int s) {
+    uint32_t c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const bool two = s & 8, one = s & 4;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) c[i] = two ? c[i + 2] : c[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) c[i] = one ? c[i + 1] : c[i];
+    const int bits = (s & 2) * 8;
+    return make_uint4(__funnelshift_r(c[0], c[1], bits), __funnelshift_r(c[1], c[2], bits),
+                      __funnelshift_r(c[2], c[3], bits), __funnelshift_r(c[3], c[4], bits));
+}
+
+// The aligned 16 bytes at p, of which only [lo, hi) may be read; what lies outside is zero.
+template <class T>
+__device__ __noinline__ uint4 load_edge(uintptr_t p, uintptr_t lo, uintptr_t hi) {
+    uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kVec<T>; ++i) {
+        const uintptr_t at = p + i * sizeof(T);
+        if (at >= lo && at < hi) {
+            if constexpr (sizeof(T) == 4) u[i] = *reinterpret_cast<const uint32_t*>(at);
+            else u[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(at) << (i % 2 * 16);
+        }
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+__device__ __forceinline__ void copy_async(uint32_t dst, uintptr_t src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint4 load_smem(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_smem(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_async() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A row read and the next one in flight, in shared memory, filled by asynchronous copies.  A
+// thread copies and reads its own packs, so this needs no barrier; of an unaligned row it
+// copies the aligned pieces its packs start in, and finds the next piece in its neighbour's
+// slot (the last lane of a warp copies one piece more).  Layout: [stage][pack][slot].
+constexpr int kStages = 2;
+
+__host__ __device__ constexpr int ring_slots(int threads) { return threads / 32 * 33; }
+
+// One tensor's share of the ring, and the group's next row of it.
+template <class T, int NV, bool SHIFT>
+struct Rows {
+    const char *next = nullptr, *now = nullptr;   // this lane's pack 0 of the row to copy; of the row to read
+    int64_t hop = 0;                       // bytes from a group's row to its next
+    uint32_t slot;                         // shared address of this thread's slot, stage 0, pack 0
+    uint32_t per;                          // bytes from a pack's slots to the next pack's
+    uintptr_t lo, hi;                      // SHIFT: the tensor's bytes
+    __device__ __forceinline__ void init(const T* base, int64_t ld, int64_t row, int64_t step, int lane, int64_t M,
+                                         int D, uint32_t smem, int tensor) {
+        next = now = reinterpret_cast<const char*>(base + row * ld) + lane * 16;
+        hop = step * ld * (int64_t)sizeof(T);
+        per = ring_slots(blockDim.x) * 16;
+        slot = smem + tensor * kStages * NV * per + (threadIdx.x / 32 * 33 + threadIdx.x % 32) * 16;
+        lo = reinterpret_cast<uintptr_t>(base);
+        hi = lo + (uintptr_t)((M - 1) * ld + D) * sizeof(T);
+    }
+    // Copies the group's next row into a stage; `lane16`: 16 x lane, `pitch`: 16 x lanes.
+    __device__ __forceinline__ void issue(int stage, int lane16, int pitch, int row_bytes) {
+        const uint32_t to = slot + stage * NV * per;
+        if constexpr (!SHIFT) {
+#pragma unroll
+            for (int q = 0; q < NV; ++q)
+                if (q < NV - 1 || q * pitch + lane16 < row_bytes)
+                    copy_async(to + q * per, reinterpret_cast<uintptr_t>(next) + q * pitch, 16);
+        } else {
+            const int m = (int)(reinterpret_cast<uintptr_t>(next) & 15);
+            auto piece = [&](int at, uint32_t dst) {       // the aligned piece at byte `at` - m of the row
+                if (at - m >= row_bytes) return;
+                const uintptr_t p = reinterpret_cast<uintptr_t>(next) - lane16 + at - m;
+                if (p >= lo) copy_async(dst, p, p + 16 <= hi ? 16 : (int)(hi - p));
+                else store_smem(dst, load_edge<T>(p, lo, hi));
+            };
+#pragma unroll
+            for (int q = 0; q < NV; ++q) {
+                piece(q * pitch + lane16, to + q * per);
+                if ((threadIdx.x & 31) == 31) piece(q * pitch + lane16 + 16, to + q * per + 16);
+            }
+        }
+        next += hop;
+    }
+    // Pack q of the row to read, once its copies have landed.
+    __device__ __forceinline__ uint4 get(int stage, int q) const {
+        const uint32_t from = slot + (stage * NV + q) * per;
+        const uint4 a = load_smem(from);
+        if constexpr (SHIFT) {
+            const int m = (int)(reinterpret_cast<uintptr_t>(now) & 15);
+            if (m) return shift_bytes(a, load_smem(from + 16), m);
+        }
+        return a;
+    }
+    __device__ __forceinline__ void advance() {
+        if (SHIFT) now += hop;
+    }
+};
+
+// Stores pack k, of which `n` elements (0 .. VEC) are the row's: an aligned piece is stored
+// by the lane whose pack it ends in where both its parts are the row's and the warp's, all
+// else element by element.
+template <class T>
+__device__ __forceinline__ void store_shifted(T* row, int k, int n, const uint4& v) {
+    constexpr int V = kVec<T>;
+    T* p = row + (int64_t)k * V;
+    const int m = (int)(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x & 31;
+    const int split_at = (16 - m) / (int)sizeof(T);        // elements of the pack before the aligned boundary
+    uint4 prev;
+    prev.x = __shfl_up_sync(0xffffffffu, v.x, 1);
+    prev.y = __shfl_up_sync(0xffffffffu, v.y, 1);
+    prev.z = __shfl_up_sync(0xffffffffu, v.z, 1);
+    prev.w = __shfl_up_sync(0xffffffffu, v.w, 1);
+    const bool piece = n >= split_at && (m == 0 || lane > 0);
+    bool next = __shfl_down_sync(0xffffffffu, piece, 1);
+    if (lane == 31) next = false;
+    if (piece) *reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(p) - m) = m == 0 ? v : shift_bytes(prev, v, 16 - m);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (i < n && (i < split_at ? !piece : !next)) {
+            if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[i] = u[i];
+            else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(u[i / 2] >> (i % 2 * 16));
+        }
+    }
+}
+
+// gamma or beta as fp32 in shared memory: the first 16 bytes of every pack's values, then
+// (16-bit rows) the second 16 bytes of every pack's, so that a warp's 16-byte reads touch
+// every bank once.
+__host__ __device__ constexpr int padded(int D) { return (D + 7) / 8 * 8; }
+
+template <class T>
+__device__ __forceinline__ void stage_param(float* to, const void* p, int gf32, int D, float none) {
+    const int half = padded(D) / 2;
+    auto put = [&](int c, float v) { to[sizeof(T) == 4 ? c : (c & 4 ? half : 0) + (c >> 3) * 4 + (c & 3)] = v; };
+    if (gf32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && p != nullptr && D % 4 == 0) {
+#pragma unroll 4
+        for (int c = threadIdx.x * 4; c < D; c += blockDim.x * 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + c);
+            *reinterpret_cast<uint4*>(&to[sizeof(T) == 4 ? c : (c & 4 ? half : 0) + (c >> 3) * 4]) = v;
+        }
+        for (int c = D + threadIdx.x; c < padded(D); c += blockDim.x) put(c, 0.f);
+        return;
+    }
+#pragma unroll 8
+    for (int c = threadIdx.x; c < padded(D); c += blockDim.x)
+        put(c, c >= D ? 0.f : p == nullptr ? none : gf32 ? static_cast<const float*>(p)[c] : to_f32(static_cast<const T*>(p)[c]));
+}
+
+// Pack k of one, as pairs.
+template <class T>
+__device__ __forceinline__ void load_staged(F2* o, uint32_t p, int k, int D) {
+    unpack16<float>(load_smem(p + k * 16), o);
+    if constexpr (sizeof(T) == 2) unpack16<float>(load_smem(p + padded(D) * 2 + k * 16), o + 2);
+}
+
+// The same from global memory (`n` elements are the row's; !SHIFT: whole packs, aligned).
+template <class T, bool SHIFT>
+__device__ __forceinline__ void load_param16(F2* o, const void* p, int gf32, int k, int n, float none) {
+    constexpr int V = kVec<T>;
+    const bool whole = !SHIFT || (n == V && (reinterpret_cast<uintptr_t>(p) & 15) == 0);
+    if (p == nullptr) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) o[i] = f2(none);
+    } else if (!whole) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int at = k * V + 2 * i + j;
+                f[j] = 2 * i + j >= n ? 0.f : gf32 ? static_cast<const float*>(p)[at] : to_f32(static_cast<const T*>(p)[at]);
+            }
+            o[i] = f2(f[0], f[1]);
+        }
+    } else if (sizeof(T) == 2 && gf32) {
+        const uint4* q = reinterpret_cast<const uint4*>(p) + 2 * k;
+        unpack16<float>(q[0], o);
+        unpack16<float>(q[1], o + 2);
+    } else {
+        unpack16<T>(reinterpret_cast<const uint4*>(p)[k], o);
+    }
+}
+
+// ---------------------------------------------------------------- sums over a row
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Barrier of a group of threads (barrier 0 is __syncthreads').
+__device__ __forceinline__ void group_sync(int group, int lanes) {
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
+}
+
+// Sums over the group's `lanes` threads.  One warp: shuffles.  More: shuffles, then every
+// thread adds the warps' sums from shared memory in warp order.  `red`: kRed entries for each
+// of two buffers, which the caller alternates, so that one barrier a reduction is enough: a
+// buffer is rewritten only after the other one's barrier, which every reader of the first
+// has passed.  The entries past the group's warps hold zeros.
+constexpr int kRed = 24;
+
+__device__ __forceinline__ float row_sum(float v, int group, int lanes, float* red, int buf) {
+    v = warp_sum(v);
+    if (lanes == 32) return v;
+    red += buf * kRed;
+    if ((threadIdx.x & 31) == 0) red[(threadIdx.x - group * lanes) >> 5] = v;
+    group_sync(group, lanes);
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRed; w += 4) {
+        if (w * 32 >= lanes) break;
+        const float4 f = *reinterpret_cast<const float4*>(red + w);
+        v += (f.x + f.y) + (f.z + f.w);
+    }
+    return v;
+}
+
+// Two sums at once.  The first exchange leaves the low half-warp with x and the high half
+// with y, so that the two take 5 or 6 shuffles instead of 10.
+__device__ __forceinline__ float2 row_sum2(float2 v, int group, int lanes, float2* red, int buf) {
+    const bool high = threadIdx.x & 16;
+    float t = (high ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, high ? v.x : v.y, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lanes == 32) {
+        const float u = __shfl_xor_sync(0xffffffffu, t, 16);
+        return high ? make_float2(u, t) : make_float2(t, u);
+    }
+    red += buf * kRed;
+    if ((threadIdx.x & 15) == 0) reinterpret_cast<float*>(&red[(threadIdx.x - group * lanes) >> 5])[high] = t;
+    group_sync(group, lanes);
+    v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kRed; w += 2) {
+        if (w * 32 >= lanes) break;
+        const float4 f = *reinterpret_cast<const float4*>(red + w);
+        v.x += f.x + f.z;
+        v.y += f.y + f.w;
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------- forward
+
+// What of pack k = q * lanes + lane is the row's: the plan gives a row ceil(packs / lanes)
+// packs a thread, so only the last one can end past it.
+template <class T, int NV, bool SHIFT>
+__device__ __forceinline__ int pack_elements(int q, int k, int D) {
+    constexpr int V = kVec<T>;
+    if (q < NV - 1 && !SHIFT) return V;
+    const int left = D - k * V;
+    return left >= V ? V : left > 0 ? left : 0;
+}
+
+// The packs of an unaligned row that a warp holds, as the aligned pieces they start in: lane
+// l's of pack q, and in lane q the piece that follows pack q of the last lane.
+template <class T, int NV>
+struct Pieces {
+    uint4 a[NV], after;
+    int m;                                 // bytes of the first piece before the row
+    __device__ __forceinline__ void load(const T* row, int lane16, int pitch, int row_bytes, uintptr_t lo, uintptr_t hi) {
+        const uintptr_t start = reinterpret_cast<uintptr_t>(row);
+        const int l = threadIdx.x & 31;
+        m = (int)(start & 15);
+        auto piece = [&](int at) {
+            const uintptr_t p = start - m + at;
+            if (at - m >= row_bytes) return make_uint4(0, 0, 0, 0);
+            if (p >= lo && p + 16 <= hi) return *reinterpret_cast<const uint4*>(p);
+            return load_edge<T>(p, lo, hi);
+        };
+#pragma unroll
+        for (int q = 0; q < NV; ++q) a[q] = piece(q * pitch + lane16);
+        after = l < NV ? piece(l * pitch + lane16 - l * 16 + 512) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ uint4 pack(int q) const {
+        if (m == 0) return a[q];
+        uint4 b;
+        const bool last = (threadIdx.x & 31) == 31;
+        const uint32_t own[4] = {a[q].x, a[q].y, a[q].z, a[q].w}, end[4] = {after.x, after.y, after.z, after.w};
+        uint32_t next[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t n = __shfl_down_sync(0xffffffffu, own[i], 1), e = __shfl_sync(0xffffffffu, end[i], q);
+            next[i] = last ? e : n;
+        }
+        b = make_uint4(next[0], next[1], next[2], next[3]);
+        return shift_bytes(a[q], b, m);
+    }
+};
+
+// One row for each group of `lanes` threads: a CTA is one row of more than a warp, or four
+// rows of one.  Many small CTAs take turns at loading, reducing and storing; a persistent
+// form with the next row in flight in shared memory took 57 us where this takes 53
+// (11136 x 3584 bf16).  The statistics need one barrier: a warp centres its columns on its
+// own mean, and the warps' (mean, sum of squares about it) are joined exactly.
+template <class T, int NV, bool SHIFT, bool RES, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) layer_norm_fwd_kernel(const NormFwd a) {
+    constexpr int V = kVec<T>, P = V / 2;
+    __shared__ float2 red[THREADS / 32];
+    const int lanes = a.lanes, lane = threadIdx.x % lanes, D = a.D;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / lanes) + threadIdx.x / lanes;
+    if (row >= a.M) return;                // whole warps; with more than one warp a row, no thread
+    const int lane16 = lane * 16, pitch = lanes * 16, row_bytes = D * (int)sizeof(T);
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* r = static_cast<const T*>(a.r) + row * a.ldr;
+    F2 v[NV * P];
+    if constexpr (SHIFT) {
+        const uintptr_t x0 = reinterpret_cast<uintptr_t>(a.x), r0 = reinterpret_cast<uintptr_t>(a.r);
+        Pieces<T, NV> px, pr;
+        px.load(x, lane16, pitch, row_bytes, x0, x0 + ((a.M - 1) * a.ldx + D) * sizeof(T));
+        if (RES) pr.load(r, lane16, pitch, row_bytes, r0, r0 + ((a.M - 1) * a.ldr + D) * sizeof(T));
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int n = pack_elements<T, NV, SHIFT>(q, q * lanes + lane, D);
+            F2* w = v + q * P;
+            unpack16<T>(px.pack(q), w);
+            if (RES) {
+                F2 f[P];
+                unpack16<T>(pr.pack(q), f);
+#pragma unroll
+                for (int i = 0; i < P; ++i) w[i] = w[i] + f[i];
+            }
+            if (n < V) keep_first<T>(w, n);
+        }
+    } else {
+        uint4 px[NV], pr[NV];
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int k = q * lanes + lane;
+            px[q] = pr[q] = make_uint4(0, 0, 0, 0);
+            if (pack_elements<T, NV, SHIFT>(q, k, D)) {
+                px[q] = __ldcs(reinterpret_cast<const uint4*>(x) + k);
+                if (RES) pr[q] = __ldcs(reinterpret_cast<const uint4*>(r) + k);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            F2* w = v + q * P;
+            unpack16<T>(px[q], w);
+            if (RES) {
+                F2 f[P];
+                unpack16<T>(pr[q], f);
+#pragma unroll
+                for (int i = 0; i < P; ++i) w[i] = w[i] + f[i];
+            }
+        }
+    }
+    if (RES) {
+        T* si = static_cast<T*>(a.s) + row * a.lds;
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int k = q * lanes + lane, n = pack_elements<T, NV, SHIFT>(q, k, D);
+            const uint4 o = pack16<T>(v + q * P);
+            if (SHIFT) store_shifted<T>(si, k, n, o);
+            else if (n) reinterpret_cast<uint4*>(si)[k] = o;
+        }
+    }
+    F2 sum2 = f2(0.f);
+#pragma unroll
+    for (int i = 0; i < NV * P; ++i) sum2 = sum2 + v[i];
+    // columns of warp w: of every pack its 32 * V from (q * lanes + 32 w) * V
+    auto columns = [&](int w) {
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int left = D - (q * lanes + 32 * w) * V;
+            n += left >= 32 * V ? 32 * V : left > 0 ? left : 0;
+        }
+        return (float)n;
+    };
+    const float2 ss = split(sum2);
+    const int warp = (threadIdx.x % lanes) >> 5, warps = lanes >> 5;
+    const float mine = columns(warp);
+    float mean = warp_sum(ss.x + ss.y) / fmaxf(mine, 1.f);
+    const F2 mu = f2(-mean);
+    F2 sq2 = f2(0.f);
+#pragma unroll
+    for (int q = 0; q < NV; ++q) {
+        const int n = pack_elements<T, NV, SHIFT>(q, q * lanes + lane, D);
+        if (n > 0) {
+            F2 c[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) c[i] = v[q * P + i] + mu;
+            if (SHIFT && n < V) keep_first<T>(c, n);
+#pragma unroll
+            for (int i = 0; i < P; ++i) sq2 = fma(c[i], c[i], sq2);
+        }
+    }
+    const float2 qq = split(sq2);
+    float sq = warp_sum(qq.x + qq.y);
+    if (warps > 1) {
+        if ((threadIdx.x & 31) == 0) red[warp] = make_float2(mean, sq);
+        __syncthreads();
+        float total = 0.f;
+        for (int w = 0; w < warps; ++w) total += columns(w) * red[w].x;
+        mean = total / (float)D;
+        sq = 0.f;
+        for (int w = 0; w < warps; ++w) {
+            const float d = red[w].x - mean;
+            sq += red[w].y + columns(w) * d * d;
+        }
+    }
+    const float rstd = __frsqrt_rn(sq / (float)D + a.eps);
+    const F2 rs = f2(rstd), m2 = f2(-mean);
+    T* yi = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+    for (int q = 0; q < NV; ++q) {
+        const int k = q * lanes + lane, n = pack_elements<T, NV, SHIFT>(q, k, D);
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (n > 0) {
+            F2 g[P], b[P];
+            load_param16<T, SHIFT>(g, a.gamma, a.gf32, k, n, 1.f);
+            load_param16<T, SHIFT>(b, a.beta, a.gf32, k, n, 0.f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) g[i] = fma((v[q * P + i] + m2) * rs, g[i], b[i]);
+            o = pack16<T>(g);
+            if (!SHIFT) __stcs(reinterpret_cast<uint4*>(yi) + k, o);
+        }
+        if (SHIFT) store_shifted<T>(yi, k, n, o);
+    }
+    if (lane == 0 && a.mean) {
+        a.mean[row] = mean;
+        a.rstd[row] = rstd;
+    }
+}
+
+// gamma or beta at column `col`, in the row's type or in fp32 (the forms for wide rows).
 template <class T, int VEC>
 __device__ __forceinline__ void load_param(float* o, const void* p, int gf32, int col, float none) {
     if (p == nullptr) {
@@ -45,166 +506,30 @@ __device__ __forceinline__ void load_param(float* o, const void* p, int gf32, in
     } else if (gf32) {
         constexpr int V4 = VEC >= 4 ? 4 : 1;
 #pragma unroll
-        for (int q = 0; q < VEC / V4; ++q) {
-            const Pack<float, V4> w = load_pack<float, V4>(static_cast<const float*>(p) + col + q * V4);
-#pragma unroll
-            for (int j = 0; j < V4; ++j) o[q * V4 + j] = w.v[j];
-        }
+        for (int q = 0; q < VEC / V4; ++q)
+            load_pack<float, V4>(static_cast<const float*>(p) + col + q * V4).unpack(o + q * V4);
     } else {
-        const Pack<T, VEC> w = load_pack<T, VEC>(static_cast<const T*>(p) + col);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = to_f32(w.v[j]);
-    }
-}
-
-// Sums over the `lanes` threads of a row.  One warp: shuffles.  The whole CTA: shuffles,
-// then every thread adds the warps' sums from shared memory in warp order.  The caller
-// alternates `buf`, so one barrier per reduction is enough: a buffer is rewritten only
-// after the other one's barrier, which every reader of the first has passed.
-constexpr int kWarps = kMaxThreads / 32;
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-__device__ __forceinline__ float row_sum(float v, int lanes, float (*red)[kWarps], int buf) {
-    v = warp_sum(v);
-    if (lanes == 32) return v;
-    if ((threadIdx.x & 31) == 0) red[buf][threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; w += 4) {
-        if (w * 32 < lanes) {
-            const float4 q = *reinterpret_cast<const float4*>(&red[buf][w]);
-            t += (q.x + q.y) + (q.z + q.w);
-        }
-    }
-    return t;
-}
-
-__device__ __forceinline__ float2 row_sum2(float2 v, int lanes, float2 (*red)[kWarps], int buf) {
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if (lanes == 32) return v;
-    if ((threadIdx.x & 31) == 0) red[buf][threadIdx.x >> 5] = v;
-    __syncthreads();
-    float2 t = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; w += 2) {
-        if (w * 32 < lanes) {
-            const float4 q = *reinterpret_cast<const float4*>(&red[buf][w]);
-            t.x += q.x + q.z;
-            t.y += q.y + q.w;
-        }
-    }
-    return t;
-}
-
-template <class T, int VEC, int CPT>
-__global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_kernel(const NormFwd a) {
-    constexpr int NV = CPT / VEC;
-    __shared__ __align__(16) float red[2][kWarps];
-    const int lanes = a.lanes, lane = threadIdx.x % lanes, hop = lanes * VEC;
-    const int rows = blockDim.x / lanes;                   // 1 unless a row is one warp
-    if (threadIdx.x < 2 * kWarps) red[0][threadIdx.x] = 0.f;
-    __syncthreads();
-    const int64_t step = (int64_t)gridDim.x * rows;
-    int64_t row = (int64_t)blockIdx.x * rows + threadIdx.x / lanes;
-    const int col = lane * VEC;                            // columns col + q * hop + j
-    const T* x = static_cast<const T*>(a.x) + col;
-    const T* r = static_cast<const T*>(a.r) + col;
-    Pack<T, VEC> px[NV], pr[NV];
-    auto load_row = [&](int64_t i) {
-        const T* xi = x + i * a.ldx;
-        const T* ri = r + i * a.ldr;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            if (col + q * hop < a.D) {
-                px[q] = load_pack<T, VEC>(xi + q * hop);
-                if (a.r) pr[q] = load_pack<T, VEC>(ri + q * hop);
-            }
-        }
-    };
-    if (row < a.M) load_row(row);
-    const float inv = 1.f / (float)a.D;
-    for (; row < a.M; row += step) {
-        float v[CPT];
-        float sum = 0.f;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float f = 0.f;
-                if (col + q * hop < a.D) {
-                    f = to_f32(px[q].v[j]);
-                    if (a.r) f += to_f32(pr[q].v[j]);
-                }
-                v[q * VEC + j] = f;
-                sum += f;
-            }
-        }
-        if (row + step < a.M) load_row(row + step);
-        if (a.r) {
-            T* si = static_cast<T*>(a.s) + row * a.lds + col;
-#pragma unroll
-            for (int q = 0; q < NV; ++q)
-                if (col + q * hop < a.D) store_pack<T, VEC>(si + q * hop, v + q * VEC);
-        }
-        const float mean = row_sum(sum, lanes, red, 0) * inv;
-        float sq = 0.f;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            if (col + q * hop < a.D) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float c = v[q * VEC + j] - mean;
-                    v[q * VEC + j] = c;
-                    sq += c * c;
-                }
-            }
-        }
-        const float var = row_sum(sq, lanes, red, 1) * inv;
-        const float rstd = __frsqrt_rn(var + a.eps);
-        T* yi = static_cast<T*>(a.y) + row * a.ldy + col;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            if (col + q * hop < a.D) {
-                float g[VEC], b[VEC];
-                load_param<T, VEC>(g, a.gamma, a.gf32, col + q * hop, 1.f);
-                load_param<T, VEC>(b, a.beta, a.gf32, col + q * hop, 0.f);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) g[j] = v[q * VEC + j] * rstd * g[j] + b[j];
-                store_pack<T, VEC>(yi + q * hop, g);
-            }
-        }
-        if (lane == 0 && a.mean) {
-            a.mean[row] = mean;
-            a.rstd[row] = rstd;
-        }
+        load_pack<T, VEC>(static_cast<const T*>(p) + col).unpack(o);
     }
 }
 
 // A row wider than the registers hold: three passes over it, the last two from L2.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_wide_kernel(const NormFwd a) {
-    __shared__ __align__(16) float red[2][kWarps];
-    if (threadIdx.x < 2 * kWarps) red[0][threadIdx.x] = 0.f;
+    __shared__ __align__(16) float red[2 * kRed];
+    if (threadIdx.x < 2 * kRed) red[threadIdx.x] = 0.f;
     __syncthreads();
     const float inv = 1.f / (float)a.D;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
         const T* x = static_cast<const T*>(a.x) + row * a.ldx;
         const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ldr : nullptr;
         auto load = [&](int col, float* v) {
-            const Pack<T, VEC> p = load_pack<T, VEC>(x + col);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) v[j] = to_f32(p.v[j]);
+            load_pack<T, VEC>(x + col).unpack(v);
             if (r) {
-                const Pack<T, VEC> e = load_pack<T, VEC>(r + col);
+                float e[VEC];
+                load_pack<T, VEC>(r + col).unpack(e);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) v[j] += to_f32(e.v[j]);
+                for (int j = 0; j < VEC; ++j) v[j] += e[j];
             }
         };
         const int first = threadIdx.x * VEC, hop = blockDim.x * VEC;
@@ -215,13 +540,13 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_wide_kernel(const 
             for (int j = 0; j < VEC; ++j) sum += v[j];
             if (r) store_pack<T, VEC>(static_cast<T*>(a.s) + row * a.lds + c, v);
         }
-        const float mean = row_sum(sum, blockDim.x, red, 0) * inv;
+        const float mean = row_sum(sum, 0, blockDim.x, red, 0) * inv;
         for (int64_t c = first; c < a.D; c += hop) {
             load((int)c, v);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) sq += (v[j] - mean) * (v[j] - mean);
         }
-        const float rstd = __frsqrt_rn(row_sum(sq, blockDim.x, red, 1) * inv + a.eps);
+        const float rstd = __frsqrt_rn(row_sum(sq, 0, blockDim.x, red, 1) * inv + a.eps);
         for (int64_t c = first; c < a.D; c += hop) {
             float g[VEC], b[VEC];
             load((int)c, v);
@@ -238,121 +563,134 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_wide_kernel(const 
     }
 }
 
-// Backward: the row's two sums, dx, and fp32 column sums of dy * xh and dy over the CTA's
-// rows, kept in registers and written once as this CTA's partial plane.  A row stays in
-// registers as it was loaded; xh and g are computed from it twice, before and after the
-// reduction, which costs less than keeping them beside the column sums.
-template <class T, int VEC, int CPT>
-__global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormBwd a) {
-    constexpr int NV = CPT / VEC;
-    __shared__ __align__(16) float2 red[2][kWarps];
-    extern __shared__ float acc[];                         // rows > 1: [2][D] sums of the CTA's warps
-    const int lanes = a.lanes, lane = threadIdx.x % lanes, group = threadIdx.x / lanes, hop = lanes * VEC;
+// ---------------------------------------------------------------- backward
+
+// The row's two sums, dx, and fp32 column sums of dy * xh and dy over the group's rows, kept
+// in registers; the CTA's groups are added in shared memory at the end and written once, as
+// this CTA's partial planes.  A row is read from the ring twice, before and after the
+// reduction, which costs less than keeping xh and g beside the column sums.  xh = s * rstd - mean * rstd, and
+// dx = g * rstd + s * A + B with A = -c2 * rstd^2, B = c2 * mean * rstd^2 - c1 * rstd.
+// Shared memory: red [groups][2][kRed] pairs, gamma (whole packs, fp32), then the rows in
+// flight, and after them the groups' column sums in their place.
+template <class T, int NV, bool SHIFT, bool SKIP>
+__global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormBwd a) {
+    constexpr int V = kVec<T>, P = V / 2;
+    extern __shared__ uint4 smem[];
+    const int lanes = a.lanes, lane = threadIdx.x % lanes, group = threadIdx.x / lanes, D = a.D;
     const int rows = blockDim.x / lanes;
-    if (threadIdx.x < 2 * kWarps) red[0][threadIdx.x] = make_float2(0.f, 0.f);
-    __syncthreads();
+    float2* red = reinterpret_cast<float2*>(smem) + group * 2 * kRed;
+    float* gamma = reinterpret_cast<float*>(smem) + rows * 4 * kRed;
+    float* acc = gamma + padded(D);
     const int64_t step = (int64_t)gridDim.x * rows;
     int64_t row = (int64_t)blockIdx.x * rows + group;
-    const int col = lane * VEC;                            // columns col + q * hop + j
-    const T* dy = static_cast<const T*>(a.dy) + col;
-    const T* s = static_cast<const T*>(a.s) + col;
-    Pack<T, VEC> py[NV], ps[NV];
-    float mean = 0.f, rstd = 0.f;
-    auto load_row = [&](int64_t i) {
-        mean = a.mean[i];
-        rstd = a.rstd[i];
-        const T* yi = dy + i * a.lddy;
-        const T* si = s + i * a.lds;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            if (col + q * hop < a.D) {
-                py[q] = load_pack<T, VEC>(yi + q * hop);
-                ps[q] = load_pack<T, VEC>(si + q * hop);
-            }
+    const int lane16 = lane * 16, pitch = lanes * 16, row_bytes = D * (int)sizeof(T);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(acc);
+    Rows<T, NV, SHIFT> dy, s, skip;
+    dy.init(static_cast<const T*>(a.dy), a.lddy, row, step, lane, a.M, D, ring, 0);
+    s.init(static_cast<const T*>(a.s), a.lds, row, step, lane, a.M, D, ring, 1);
+    if (SKIP) skip.init(static_cast<const T*>(a.skip), a.ldk, row, step, lane, a.M, D, ring, 2);
+    auto issue = [&](int stage, int64_t i) {
+        if (i < a.M) {
+            dy.issue(stage, lane16, pitch, row_bytes);
+            s.issue(stage, lane16, pitch, row_bytes);
+            if (SKIP) skip.issue(stage, lane16, pitch, row_bytes);
         }
+        commit_async();
     };
-    float dg[CPT], db[CPT];
+    cudaTriggerProgrammaticLaunchCompletion();             // the parameters' kernel may come up meanwhile
+    issue(0, row);
+    for (int i = threadIdx.x; i < rows * 4 * kRed; i += blockDim.x) reinterpret_cast<float*>(smem)[i] = 0.f;
+    stage_param<T>(gamma, a.gamma, a.gf32, D, 1.f);
+    const uint32_t gamma_at = (uint32_t)__cvta_generic_to_shared(gamma);
+    __syncthreads();
+    F2 dg[NV * P], db[NV * P];
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) dg[j] = db[j] = 0.f;
-    if (row < a.M) load_row(row);
-    const float inv = 1.f / (float)a.D;
-    int buf = 0;
-    for (; row < a.M; row += step, buf ^= 1) {
-        Pack<T, VEC> cy[NV], cs[NV], pk[NV];
+    for (int i = 0; i < NV * P; ++i) dg[i] = db[i] = f2(0.f);
+    float mean = 0.f, rstd = 0.f;
+    if (row < a.M) mean = a.mean[row], rstd = a.rstd[row];
+    const float inv = 1.f / (float)D;
+    for (int stage = 0; row < a.M; row += step, stage ^= 1, dy.advance(), s.advance(), skip.advance()) {
+        if (SHIFT) __syncwarp();           // the neighbours have read the stage that is filled next
+        issue(stage ^ 1, row + step);
         const float mu = mean, rs = rstd;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) cy[q] = py[q], cs[q] = ps[q];
-        if (a.skip) {
-            const T* ki = static_cast<const T*>(a.skip) + row * a.ldk + col;
-#pragma unroll
-            for (int q = 0; q < NV; ++q)
-                if (col + q * hop < a.D) pk[q] = load_pack<T, VEC>(ki + q * hop);
-        }
-        if (row + step < a.M) load_row(row + step);
-        float2 c = make_float2(0.f, 0.f);
+        if (row + step < a.M) mean = a.mean[row + step], rstd = a.rstd[row + step];
+        wait_async<1>();
+        if (SHIFT) __syncwarp();
+        const F2 rs2 = f2(rs), shift = f2(-mu * rs);
+        F2 c1 = f2(0.f), c2 = f2(0.f);
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            if (col + q * hop < a.D) {
-                float w[VEC];
-                load_param<T, VEC>(w, a.gamma, a.gf32, col + q * hop, 1.f);
+            const int k = q * lanes + lane, n = pack_elements<T, NV, SHIFT>(q, k, D);
+            if (n > 0) {
+                F2 w[P], d[P], xs[P];
+                load_staged<T>(w, gamma_at, k, D);
+                unpack16<T>(dy.get(stage, q), d);
+                unpack16<T>(s.get(stage, q), xs);
+                if (SHIFT && n < V) keep_first<T>(d, n), keep_first<T>(xs, n);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float d = to_f32(cy[q].v[j]), xh = (to_f32(cs[q].v[j]) - mu) * rs, g = d * w[j];
-                    dg[q * VEC + j] += d * xh;
-                    db[q * VEC + j] += d;
-                    c.x += g;
-                    c.y += g * xh;
+                for (int i = 0; i < P; ++i) {
+                    const F2 xh = fma(xs[i], rs2, shift), g = d[i] * w[i];
+                    dg[q * P + i] = fma(d[i], xh, dg[q * P + i]);
+                    db[q * P + i] = db[q * P + i] + d[i];
+                    c1 = c1 + g;
+                    c2 = fma(g, xh, c2);
                 }
             }
         }
-        c = row_sum2(c, lanes, red, buf);
-        c.x *= inv;
-        c.y *= inv;
-        T* oi = static_cast<T*>(a.dx) + row * a.lddx + col;
+        const float2 p1 = split(c1), p2 = split(c2);
+        float2 c = row_sum2(make_float2(p1.x + p1.y, p2.x + p2.y), group, lanes, red, stage);
+        c.x *= inv * rs;
+        c.y *= inv * rs;
+        const F2 A = f2(-c.y * rs), B = f2(c.y * mu * rs - c.x);
+        T* oi = static_cast<T*>(a.dx) + row * a.lddx;
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            if (col + q * hop < a.D) {
-                float w[VEC];
-                load_param<T, VEC>(w, a.gamma, a.gf32, col + q * hop, 1.f);
+            const int k = q * lanes + lane, n = pack_elements<T, NV, SHIFT>(q, k, D);
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (n > 0) {
+                F2 w[P], d[P], xs[P];
+                load_staged<T>(w, gamma_at, k, D);
+                unpack16<T>(dy.get(stage, q), d);
+                unpack16<T>(s.get(stage, q), xs);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float xh = (to_f32(cs[q].v[j]) - mu) * rs;
-                    w[j] = rs * (to_f32(cy[q].v[j]) * w[j] - c.x - xh * c.y);
-                    if (a.skip) w[j] += to_f32(pk[q].v[j]);
+                for (int i = 0; i < P; ++i) w[i] = fma(d[i] * w[i], rs2, fma(xs[i], A, B));
+                if (SKIP) {
+                    unpack16<T>(skip.get(stage, q), d);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) w[i] = w[i] + d[i];
                 }
-                store_pack<T, VEC>(oi + q * hop, w);
+                o = pack16<T>(w);
+                if (!SHIFT) reinterpret_cast<uint4*>(oi)[k] = o;
             }
+            if (SHIFT) store_shifted<T>(oi, k, n, o);
         }
     }
     if (a.pg == nullptr && a.pb == nullptr) return;
-    if (rows > 1) {
-        // one warp per row: add the warps' sums in warp order, through shared memory
-        for (int w = 0; w < rows; ++w) {
-            if (group == w) {
+    // the groups' sums meet in the ring's place: [group][2][columns, 16-byte pieces of packs apart]
+    wait_async<0>();
+    __syncthreads();
+    const int width = padded(D), half = sizeof(T) == 2 ? width / 2 : 0;
+    float* mine = acc + group * 2 * width;
 #pragma unroll
-                for (int k = 0; k < CPT; ++k) {
-                    const int at = col + k / VEC * hop + k % VEC;
-                    if (at < a.D) {
-                        if (w > 0) {
-                            dg[k] += acc[at];
-                            db[k] += acc[a.D + at];
-                        }
-                        acc[at] = dg[k];
-                        acc[a.D + at] = db[k];
-                    }
-                }
+    for (int q = 0; q < NV; ++q) {
+        const int k = q * lanes + lane;
+        if (pack_elements<T, NV, true>(q, k, D) > 0) {
+#pragma unroll
+            for (int h = 0; h < P / 2; ++h) {
+                const float2 g0 = split(dg[q * P + 2 * h]), g1 = split(dg[q * P + 2 * h + 1]);
+                const float2 b0 = split(db[q * P + 2 * h]), b1 = split(db[q * P + 2 * h + 1]);
+                reinterpret_cast<float4*>(mine + h * half)[k] = make_float4(g0.x, g0.y, g1.x, g1.y);
+                reinterpret_cast<float4*>(mine + width + h * half)[k] = make_float4(b0.x, b0.y, b1.x, b1.y);
             }
-            __syncthreads();
         }
-        if (group != rows - 1) return;
     }
-#pragma unroll
-    for (int k = 0; k < CPT; ++k) {
-        const int at = col + k / VEC * hop + k % VEC;
-        if (at < a.D) {
-            if (a.pg) a.pg[(int64_t)blockIdx.x * a.D + at] = dg[k];
-            if (a.pb) a.pb[(int64_t)blockIdx.x * a.D + at] = db[k];
-        }
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += blockDim.x) {
+        const float* p = acc + (sizeof(T) == 4 ? c : (c & 4 ? half : 0) + (c >> 3) * 4 + (c & 3));
+        float g = 0.f, b = 0.f;
+        for (int w = 0; w < rows; ++w, p += 2 * width) g += p[0], b += p[width];
+        if (a.pg) a.pg[(int64_t)blockIdx.x * D + c] = g;
+        if (a.pb) a.pb[(int64_t)blockIdx.x * D + c] = b;
     }
 }
 
@@ -360,8 +698,8 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_kernel(const NormB
 // and the column sums of a block of columns over a range of rows.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_wide_sums_kernel(const NormBwd a, float2* sums) {
-    __shared__ __align__(16) float2 red[2][kWarps];
-    if (threadIdx.x < 2 * kWarps) red[0][threadIdx.x] = make_float2(0.f, 0.f);
+    __shared__ __align__(16) float2 red[2 * kRed];
+    if (threadIdx.x < 2 * kRed) red[threadIdx.x] = make_float2(0.f, 0.f);
     __syncthreads();
     int buf = 0;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, buf ^= 1) {
@@ -370,17 +708,18 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_wide_sums_kernel(c
         const float mean = a.mean[row], rstd = a.rstd[row];
         float2 c = make_float2(0.f, 0.f);
         for (int64_t col = threadIdx.x * VEC; col < a.D; col += blockDim.x * VEC) {
-            float w[VEC];
-            const Pack<T, VEC> py = load_pack<T, VEC>(dy + col), ps = load_pack<T, VEC>(s + col);
+            float w[VEC], d[VEC], xs[VEC];
+            load_pack<T, VEC>(dy + col).unpack(d);
+            load_pack<T, VEC>(s + col).unpack(xs);
             load_param<T, VEC>(w, a.gamma, a.gf32, (int)col, 1.f);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const float g = to_f32(py.v[j]) * w[j];
+                const float g = d[j] * w[j];
                 c.x += g;
-                c.y += g * ((to_f32(ps.v[j]) - mean) * rstd);
+                c.y += g * ((xs[j] - mean) * rstd);
             }
         }
-        c = row_sum2(c, blockDim.x, red, buf);
+        c = row_sum2(c, 0, blockDim.x, red, buf);
         if (threadIdx.x == 0) sums[row] = make_float2(c.x / (float)a.D, c.y / (float)a.D);
     }
 }
@@ -389,6 +728,7 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_wide_sums_kernel(c
 // y, y + gridDim.y, ...; its column sums are partial plane y.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_wide_kernel(const NormBwd a, const float2* sums) {
+    cudaTriggerProgrammaticLaunchCompletion();
     const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * VEC;
     if (col >= a.D) return;
     float w[VEC], dg[VEC], db[VEC];
@@ -396,22 +736,23 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_wide_kernel(const 
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dg[j] = db[j] = 0.f;
     for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
-        const Pack<T, VEC> py = load_pack<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy + col);
-        const Pack<T, VEC> ps = load_pack<T, VEC>(static_cast<const T*>(a.s) + row * a.lds + col);
+        float d[VEC], xs[VEC];
+        load_pack<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy + col).unpack(d);
+        load_pack<T, VEC>(static_cast<const T*>(a.s) + row * a.lds + col).unpack(xs);
         const float mean = a.mean[row], rstd = a.rstd[row];
         const float2 c = sums[row];
         float o[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            const float d = to_f32(py.v[j]), xh = (to_f32(ps.v[j]) - mean) * rstd;
-            dg[j] += d * xh;
-            db[j] += d;
-            o[j] = rstd * (d * w[j] - c.x - xh * c.y);
+            const float xh = (xs[j] - mean) * rstd;
+            dg[j] += d[j] * xh;
+            db[j] += d[j];
+            o[j] = rstd * (d[j] * w[j] - c.x - xh * c.y);
         }
         if (a.skip) {
-            const Pack<T, VEC> pk = load_pack<T, VEC>(static_cast<const T*>(a.skip) + row * a.ldk + col);
+            load_pack<T, VEC>(static_cast<const T*>(a.skip) + row * a.ldk + col).unpack(d);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) o[j] += to_f32(pk.v[j]);
+            for (int j = 0; j < VEC; ++j) o[j] += d[j];
         }
         store_pack<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx + col, o);
     }
@@ -432,7 +773,9 @@ __global__ void __launch_bounds__(512) layer_norm_params_kernel(const float* pg,
     if (out == nullptr) return;
     const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float t = 0.f;
+    cudaGridDependencySynchronize();       // launched beside the kernel that writes the planes
     if (col < D) {
+#pragma unroll 10
         for (int i = threadIdx.y; i < planes; i += 16) t += p[(int64_t)i * D + col];
     }
     part[threadIdx.y][threadIdx.x] = t;
@@ -447,27 +790,58 @@ __global__ void __launch_bounds__(512) layer_norm_params_kernel(const float* pg,
 
 // ---------------------------------------------------------------- host side
 
-// How a launch covers its rows.  Up to 256 columns a row is one warp (no barriers) and a
-// CTA holds four rows; wider rows get one CTA with 8 columns a thread, 16 above 8192.
+// How a launch covers its rows: `nv` packs a thread, `lanes` threads a row, `groups` rows a
+// CTA at a time.
 struct NormPlan {
-    int cpt, lanes, threads;
-    int rows() const { return threads / lanes; }
+    int nv, lanes, groups;
+    int threads() const { return lanes * groups; }
 };
 
-NormPlan norm_plan(int64_t D) {
+// Packs a thread holds at most.  Backward: 16 columns (fp32: 8), whose two sums take 32
+// registers.
+constexpr int kFwdPacks = 4, kBwdPacks = 4;
+constexpr size_t kSmem = 227 * 1024;
+
+size_t row_smem(const NormPlan& p, int tensors) { return (size_t)kStages * tensors * p.nv * ring_slots(p.threads()) * 16; }
+size_t bwd_smem(const NormPlan& p, int64_t D, bool skip) {
+    const size_t rows = row_smem(p, skip ? 3 : 2), sums = (size_t)p.groups * 2 * padded((int)D) * 4;
+    return (size_t)p.groups * 4 * kRed * 4 + (size_t)padded((int)D) * 4 + (rows > sums ? rows : sums);
+}
+
+NormPlan norm_plan(int64_t D, int size, int packs, int threads) {
     NormPlan p;
-    p.cpt = D <= 8192 ? 8 : 16;
-    p.lanes = (int)(D > kMaxWidthFwd ? kMaxThreads : ((D + p.cpt - 1) / p.cpt + 31) / 32 * 32);
-    p.threads = p.lanes == 32 ? 128 : p.lanes;
+    const int64_t all = (D * size + 15) / 16;
+    p.lanes = (int)((all + packs * 32 - 1) / (packs * 32) * 32);
+    p.nv = (int)((all + p.lanes - 1) / p.lanes);
+    p.groups = threads / p.lanes > 1 ? threads / p.lanes : 1;
     return p;
 }
 
-// CTAs of the backward = partial planes.  About 1024 threads an SM keep two rows of loads in flight.
-int64_t bwd_ctas(int64_t M, const NormPlan& p) {
-    const int64_t want = (M + p.rows() - 1) / p.rows();
-    const int64_t most = (int64_t)kPlanSms * (1024 / p.threads < 8 ? 1024 / p.threads : 8);
-    return want < most ? want : most;
+// Forward: CTAs of one row of more than a warp, or of four rows of one.
+NormPlan fwd_plan(int64_t D, int size) {
+    NormPlan p = norm_plan(D, size, kFwdPacks, 128);
+    if (p.lanes > 32) p.groups = 1;
+    return p;
 }
+
+// Backward: one CTA on each SM, of as many groups as threads, named barriers and shared
+// memory allow, but one row for each SM before two for one.
+NormPlan bwd_plan(int64_t M, int64_t D, int size, bool skip) {
+    NormPlan p = norm_plan(D, size, kBwdPacks, kBwdThreads);
+    if (p.groups > 15) p.groups = 15;                      // barriers 1 .. 15
+    const int64_t spread = (M + kPlanSms - 1) / kPlanSms;
+    if (spread < p.groups) p.groups = spread > 0 ? (int)spread : 1;
+    while (p.groups > 1 && bwd_smem(p, D, skip) > kSmem) --p.groups;
+    return p;
+}
+int bwd_ctas(int64_t M, const NormPlan& p) {
+    const int64_t want = (M + p.groups - 1) / p.groups;
+    return (int)(want < kPlanSms ? want : kPlanSms);
+}
+
+// Widest rows these forms take, by the backward's shared memory: 24 KB, that is 12288 columns
+// of 16 bits.
+constexpr int64_t kMaxRowBytes = 384 * kBwdPacks * 16;
 
 int64_t wide_row_ranges(int64_t M, int64_t D, int vec) {
     const int64_t blocks = (D + 256 * vec - 1) / (256 * vec);
@@ -483,71 +857,102 @@ int type_bytes(int type) { return type == SWIGLU_FP32 ? 4 : type == SWIGLU_BF16 
 
 bool misaligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
-// Elements moved at a time: 16 bytes where every base, row stride and the width allow it,
-// 4 bytes (two 16-bit elements) where those are even, else one.
-struct Vec {
+// Whether every base, row stride and the width allow 16-byte accesses.
+struct Aligned {
     int size, bits = 0;
     void add(const void* p, int64_t ld) {
         if (p) bits |= (int)(reinterpret_cast<uintptr_t>(p) & 15) | (int)((ld * size) & 15);
     }
-    int elements() const { return (bits & 15) == 0 ? 16 / size : size == 2 && (bits & 3) == 0 ? 2 : 1; }
+    bool ok() const { return bits == 0; }
 };
 
-// f.run<T, VEC>() for the run-time type and pack width.
+// f.run<T>() for the run-time type.
 template <class F>
-cudaError_t with_types(int type, int vec, const F& f) {
-    if (type == SWIGLU_FP32) return vec == 4 ? f.template run<float, 4>() : f.template run<float, 1>();
-    if (type == SWIGLU_FP16)
-        return vec == 8 ? f.template run<__half, 8>() : vec == 2 ? f.template run<__half, 2>() : f.template run<__half, 1>();
-    return vec == 8   ? f.template run<__nv_bfloat16, 8>()
-           : vec == 2 ? f.template run<__nv_bfloat16, 2>()
-                      : f.template run<__nv_bfloat16, 1>();
+cudaError_t with_type(int type, const F& f) {
+    if (type == SWIGLU_FP32) return f.template run<float>();
+    if (type == SWIGLU_FP16) return f.template run<__half>();
+    return f.template run<__nv_bfloat16>();
+}
+
+template <class K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+    return bytes <= 48 * 1024 ? cudaSuccess
+                              : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 struct LaunchFwd {
     const NormFwd& a;
     const NormPlan& p;
+    bool shift;
     cudaStream_t s;
-    template <class T, int VEC>
-    cudaError_t run() const {
-        const int64_t want = (a.M + p.rows() - 1) / p.rows();
-        const int64_t most = (int64_t)kPlanSms * (2048 / p.threads < 16 ? 2048 / p.threads : 16);
-        const unsigned grid = (unsigned)(want < most ? want : most);
-        if (a.D > kMaxWidthFwd)
-            layer_norm_fwd_wide_kernel<T, VEC><<<grid, kMaxThreads, 0, s>>>(a);
-        else if (p.cpt == 16)
-            layer_norm_fwd_kernel<T, VEC, 16><<<grid, p.threads, 0, s>>>(a);
-        else
-            layer_norm_fwd_kernel<T, VEC, 8><<<grid, p.threads, 0, s>>>(a);
+    template <class T, int NV, bool SHIFT, bool RES>
+    cudaError_t go() const {
+        // 64 (unaligned rows: 80) registers for the small CTAs, whose number hides the latencies;
+        // the larger ones all hold 4 packs a thread
+        auto kern = layer_norm_fwd_kernel<T, NV, SHIFT, RES, 128, SHIFT ? 6 : 8>;
+        if constexpr (NV == 4) {
+            if (p.threads() > 128) kern = layer_norm_fwd_kernel<T, NV, SHIFT, RES, 384, 2>;
+        }
+        kern<<<(unsigned)((a.M + p.groups - 1) / p.groups), p.threads(), 0, s>>>(a);
         return cudaGetLastError();
+    }
+    template <class T, int NV>
+    cudaError_t forms() const {
+        if (shift) return a.r ? go<T, NV, true, true>() : go<T, NV, true, false>();
+        return a.r ? go<T, NV, false, true>() : go<T, NV, false, false>();
+    }
+    template <class T>
+    cudaError_t run() const {
+        if ((int64_t)a.D * (int)sizeof(T) > kMaxRowBytes) {
+            const unsigned grid = (unsigned)(a.M < kPlanSms * 4 ? a.M : kPlanSms * 4);
+            if (shift) layer_norm_fwd_wide_kernel<T, 1><<<grid, kMaxThreads, 0, s>>>(a);
+            else layer_norm_fwd_wide_kernel<T, kVec<T>><<<grid, kMaxThreads, 0, s>>>(a);
+            return cudaGetLastError();
+        }
+        return p.nv == 1 ? forms<T, 1>() : p.nv == 2 ? forms<T, 2>() : p.nv == 3 ? forms<T, 3>() : forms<T, 4>();
     }
 };
 
 struct LaunchBwd {
     const NormBwd& a;
     const NormPlan& p;
+    bool shift;
     float2* sums;
     int planes;
     cudaStream_t s;
-    template <class T, int VEC>
-    cudaError_t run() const {
-        if (a.D > kMaxWidthBwd) {
-            const int64_t grid = a.M < kPlanSms * 2 ? a.M : kPlanSms * 2;
-            layer_norm_bwd_wide_sums_kernel<T, VEC><<<(unsigned)grid, kMaxThreads, 0, s>>>(a, sums);
-            const dim3 tiles((unsigned)((a.D + 256 * VEC - 1) / (256 * VEC)), (unsigned)planes);
-            layer_norm_bwd_wide_kernel<T, VEC><<<tiles, 256, 0, s>>>(a, sums);
-        } else {
-            const size_t smem = p.rows() > 1 ? 2 * (size_t)a.D * sizeof(float) : 0;
-            layer_norm_bwd_kernel<T, VEC, 8><<<(unsigned)planes, p.threads, smem, s>>>(a);
-        }
+    template <class T, int NV, bool SHIFT, bool SKIP>
+    cudaError_t go() const {
+        auto kern = layer_norm_bwd_kernel<T, NV, SHIFT, SKIP>;
+        const size_t smem = bwd_smem(p, a.D, SKIP);
+        cudaError_t e = allow_smem(kern, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)planes, p.threads(), smem, s>>>(a);
         return cudaGetLastError();
+    }
+    template <class T, int NV>
+    cudaError_t forms() const {
+        if (shift) return a.skip ? go<T, NV, true, true>() : go<T, NV, true, false>();
+        return a.skip ? go<T, NV, false, true>() : go<T, NV, false, false>();
+    }
+    template <class T, int VEC>
+    cudaError_t wide() const {
+        const int64_t grid = a.M < kPlanSms * 4 ? a.M : kPlanSms * 4;
+        layer_norm_bwd_wide_sums_kernel<T, VEC><<<(unsigned)grid, kMaxThreads, 0, s>>>(a, sums);
+        const dim3 tiles((unsigned)((a.D + 256 * VEC - 1) / (256 * VEC)), (unsigned)planes);
+        layer_norm_bwd_wide_kernel<T, VEC><<<tiles, 256, 0, s>>>(a, sums);
+        return cudaGetLastError();
+    }
+    template <class T>
+    cudaError_t run() const {
+        if ((int64_t)a.D * (int)sizeof(T) > kMaxRowBytes) return shift ? wide<T, 1>() : wide<T, kVec<T>>();
+        return p.nv == 1 ? forms<T, 1>() : p.nv == 2 ? forms<T, 2>() : p.nv == 3 ? forms<T, 3>() : forms<T, 4>();
     }
 };
 
 swiglu_status norm_check(int64_t M, int64_t D, int type, int param_type) {
     if (M < 0 || D <= 0) return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: a size is negative or zero");
-    if (M >= (int64_t(1) << 31) || D >= (int64_t(1) << 30))
-        return fail(SWIGLU_ERR_UNSUPPORTED_SHAPE, "layer norm: M must stay below 2^31 and D below 2^30");
+    if (M >= (int64_t(1) << 31) || D >= (int64_t(1) << 28))
+        return fail(SWIGLU_ERR_UNSUPPORTED_SHAPE, "layer norm: M must stay below 2^31 and D below 2^28");
     if (type_bytes(type) == 0 || (param_type != type && param_type != SWIGLU_FP32))
         return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: unknown type, or parameters of neither the rows' type nor fp32");
     return SWIGLU_OK;
@@ -580,22 +985,24 @@ swiglu_status swiglu_mlp_layer_norm_fwd(const void* x, int64_t ldx, const void* 
     int sms;
     rc = device_sms(&sms);
     if (rc != SWIGLU_OK) return rc;
-    Vec v{(int)n};
+    Aligned v{(int)n};
     v.add(x, ldx), v.add(residual, ldr), v.add(y, ldy), v.add(s, lds), v.add(x, D);
     v.add(gamma, 0), v.add(beta, 0);
-    const NormFwd a{x, residual, gamma, beta, y, s, mean, rstd, ldx, ldr, ldy, lds, M, (int)D, norm_plan(D).lanes,
+    const NormPlan p = fwd_plan(D, (int)n);
+    const NormFwd a{x, residual, gamma, beta, y, s, mean, rstd, ldx, ldr, ldy, lds, M, (int)D, p.lanes,
                     param_type == SWIGLU_FP32, eps};
-    const NormPlan p = norm_plan(D);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return launch_traced(SWIGLU_KERNEL_NORM_FWD, st,
-                         [&] { return with_types(type, v.elements(), LaunchFwd{a, p, st}); });
+    return launch_traced(SWIGLU_KERNEL_NORM_FWD, st, [&] { return with_type(type, LaunchFwd{a, p, !v.ok(), st}); });
 }
 
 size_t swiglu_mlp_layer_norm_bwd_workspace_size(int64_t M, int64_t D) {
     if (M <= 0 || D <= 0) return 0;
-    if (D > kMaxWidthBwd)   // row sums, then the planes of the narrowest packs (the most row ranges of any vec)
-        return round256((size_t)M * sizeof(float2)) + 2 * round256((size_t)wide_row_ranges(M, D, 8) * D * 4);
-    return 2 * round256((size_t)bwd_ctas(M, norm_plan(D)) * D * 4);
+    // whatever the type and the alignment: one plane an SM, or the two-pass form's row sums and
+    // the planes of its widest packs, which have the most row ranges
+    const size_t narrow = 2 * round256((size_t)(M < kPlanSms ? M : kPlanSms) * D * 4);
+    if (D * 4 <= kMaxRowBytes) return narrow;
+    const size_t wide = round256((size_t)M * sizeof(float2)) + 2 * round256((size_t)wide_row_ranges(M, D, 8) * D * 4);
+    return narrow > wide ? narrow : wide;
 }
 
 swiglu_status swiglu_mlp_layer_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const void* gamma,
@@ -630,12 +1037,12 @@ swiglu_status swiglu_mlp_layer_norm_bwd(const void* dy, int64_t lddy, const void
         return fail(SWIGLU_ERR_WORKSPACE_TOO_SMALL, "layer norm: workspace smaller than the size query returns");
     rc = device_sms(&sms);
     if (rc != SWIGLU_OK) return rc;
-    Vec v{(int)n};
-    v.add(dy, lddy), v.add(s, lds), v.add(dskip, ldskip), v.add(dx, lddx), v.add(dy, D), v.add(gamma, 0);
-    const NormPlan p = norm_plan(D);
-    const bool wide = D > kMaxWidthBwd;
-    const int vec = v.elements();
-    const int planes = (int)(wide ? wide_row_ranges(M, D, vec) : bwd_ctas(M, p));
+    Aligned v{(int)n};
+    v.add(dy, lddy), v.add(s, lds), v.add(dskip, ldskip), v.add(dx, lddx), v.add(dy, D);
+    if (D * (int64_t)n > kMaxRowBytes) v.add(gamma, 0);
+    const NormPlan p = bwd_plan(M, D, (int)n, dskip != nullptr);
+    const bool wide = D * (int64_t)n > kMaxRowBytes, shift = !v.ok();
+    const int planes = (int)(wide ? wide_row_ranges(M, D, shift ? 1 : 16 / (int)n) : bwd_ctas(M, p));
     uint8_t* w = static_cast<uint8_t*>(workspace);
     float2* sums = reinterpret_cast<float2*>(w);
     if (wide) w += round256((size_t)M * sizeof(float2));
@@ -644,18 +1051,26 @@ swiglu_status swiglu_mlp_layer_norm_bwd(const void* dy, int64_t lddy, const void
     const NormBwd a{dy, s, gamma, dskip, mean, rstd, dx, dgamma ? pg : nullptr, dbeta ? pb : nullptr,
                     lddy, lds, ldskip, lddx, M, (int)D, p.lanes, param_type == SWIGLU_FP32};
     rc = launch_traced(SWIGLU_KERNEL_NORM_BWD, st,
-                       [&] { return with_types(type, vec, LaunchBwd{a, p, sums, planes, st}); });
+                       [&] { return with_type(type, LaunchBwd{a, p, shift, sums, planes, st}); });
     if (rc != SWIGLU_OK || (!dgamma && !dbeta)) return rc;
     return launch_traced(SWIGLU_KERNEL_NORM_PARAMS, st, [&] {
-        const dim3 grid((unsigned)((D + 31) / 32), 2), block(32, 16);
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3((unsigned)((D + 31) / 32), 2);
+        cfg.blockDim = dim3(32, 16);
+        cfg.stream = st;
+        const float *g = pg, *b = pb;
+        const int d = (int)D;
         if (param_type == SWIGLU_FP32)
-            layer_norm_params_kernel<float><<<grid, block, 0, st>>>(pg, pb, (float*)dgamma, (float*)dbeta, planes, (int)D);
-        else if (param_type == SWIGLU_FP16)
-            layer_norm_params_kernel<__half><<<grid, block, 0, st>>>(pg, pb, (__half*)dgamma, (__half*)dbeta, planes, (int)D);
-        else
-            layer_norm_params_kernel<__nv_bfloat16>
-                <<<grid, block, 0, st>>>(pg, pb, (__nv_bfloat16*)dgamma, (__nv_bfloat16*)dbeta, planes, (int)D);
-        return cudaGetLastError();
+            return cudaLaunchKernelEx(&cfg, layer_norm_params_kernel<float>, g, b, (float*)dgamma, (float*)dbeta, planes, d);
+        if (param_type == SWIGLU_FP16)
+            return cudaLaunchKernelEx(&cfg, layer_norm_params_kernel<__half>, g, b, (__half*)dgamma, (__half*)dbeta, planes, d);
+        return cudaLaunchKernelEx(&cfg, layer_norm_params_kernel<__nv_bfloat16>, g, b, (__nv_bfloat16*)dgamma,
+                                  (__nv_bfloat16*)dbeta, planes, d);
     });
 }
 

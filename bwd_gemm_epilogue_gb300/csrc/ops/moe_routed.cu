@@ -50,17 +50,11 @@ struct Routed {
 
 // 8 values of a row at p as fp32.
 __device__ __forceinline__ void load8(float* o, const __nv_bfloat16* p) {
-    const Pack<__nv_bfloat16, 8> v = load_pack<__nv_bfloat16, 8>(p);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = to_f32(v.v[j]);
+    load_pack<__nv_bfloat16, 8>(p).unpack(o);
 }
 __device__ __forceinline__ void load8(float* o, const float* p) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const Pack<float, 4> v = load_pack<float, 4>(p + 4 * q);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[4 * q + j] = v.v[j];
-    }
+    load_pack<float, 4>(p).unpack(o);
+    load_pack<float, 4>(p + 4).unpack(o + 4);
 }
 
 // Order-preserving key of a logit: larger logit, larger key; NaN lowest.

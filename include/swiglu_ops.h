@@ -30,7 +30,7 @@ typedef enum { SWIGLU_BF16 = 0, SWIGLU_FP16 = 1, SWIGLU_FP32 = 2 } swiglu_dtype;
  *   gamma, beta [D]            `param_type`: `type` or SWIGLU_FP32; NULL = 1 and 0
  *   mean, rstd [M] fp32        saved for the backward; both may be NULL
  * The statistics and y are taken from the unrounded fp32 sum, in two passes over the row
- * held in registers; each output is rounded once.  D >= 1, M >= 0, eps >= 0.
+ * held in registers; each output is rounded once.  1 <= D < 2^28, 0 <= M < 2^31, eps >= 0.
  */
 swiglu_status swiglu_mlp_layer_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                         const void* gamma, const void* beta, void* y, int64_t ldy, void* s,
@@ -38,7 +38,7 @@ swiglu_status swiglu_mlp_layer_norm_fwd(const void* x, int64_t ldx, const void* 
                                         int type, int param_type, void* stream);
 
 /* Bytes of workspace swiglu_mlp_layer_norm_bwd needs: fp32 partial sums of dgamma and
- * dbeta, one plane per CTA, and for D > 8192 two fp32 sums per row.  0 when M or D is
+ * dbeta, one plane per CTA, and for D > 6144 two fp32 sums per row.  0 when M or D is
  * not positive. */
 size_t swiglu_mlp_layer_norm_bwd_workspace_size(int64_t M, int64_t D);
 

@@ -92,7 +92,8 @@ def check_bwd(b, dy, s, gamma, mean, rstd, skip, **kw):
 # widths: one column; fewer than a warp; a pack's tail; one warp; ragged multi-warp; the widest
 # rows of each register form and one past it; rows and widths both odd
 SHAPES = [(1, 1), (3, 7), (5, 8), (130, 100), (33, 256), (7, 257), (19, 1000), (4, 1023), (300, 1032), (9, 3584),
-          (3, 8192), (5, 8193), (2, 8200), (3, 16384), (2, 16390), (3, 20001), (1300, 64)]
+          (3, 8192), (5, 8193), (2, 8200), (3, 16384), (2, 16390), (3, 20001), (1300, 64),
+          (2, 6144), (3, 6148), (2, 12288), (3, 12289), (700, 515), (5000, 24)]
 TYPES = [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32), (torch.float16, torch.float16),
          (torch.float32, torch.float32)]
 
