@@ -9,10 +9,9 @@
 // memory (registers could hold one, and its latency showed: 92 us backward instead of
 // the ring's for 11136 x 3584 bf16).
 //
-// Rows that do not start on 16-byte boundaries (odd widths, strides, bases) move in aligned
-// 16-byte pieces all the same: each lane copies the aligned piece its pack starts in, takes
-// the rest from its neighbour's and shifts the two together; stores likewise, with single
-// elements at the ends of a warp's span.
+// Rows that do not start on 16-byte boundaries (odd widths, strides, bases) go element by
+// element with constant offsets.  Moving them in aligned 16-byte pieces, shifted together in
+// registers, was tried: its shifting, edges and bounds took 66 instructions a column.
 #include "../host.h"
 #include "convert.cuh"
 #include "swiglu_ops.h"
@@ -47,54 +46,14 @@ struct NormBwd {
 template <class T>
 constexpr int kVec = 16 / (int)sizeof(T);
 
-// The first `n` elements of a partial pack, the others zero.
-template <class T>
-__device__ __forceinline__ void keep_first(F2* v, int n) {
-#pragma unroll
-    for (int i = 0; i < kVec<T> / 2; ++i) {
-        const float2 f = split(v[i]);
-        v[i] = f2(2 * i < n ? f.x : 0.f, 2 * i + 1 < n ? f.y : 0.f);
-    }
-}
-
-// 16 bytes from byte s (0 < s < 16, a multiple of the element) of the 32 bytes a, b.
-__device__ __forceinline__ uint4 shift_bytes(const uint4& a, const uint4& b, int s) {
-    uint32_t c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const bool two = s & 8, one = s & 4;
-#pragma unroll
-    for (int i = 0; i < 6; ++i) c[i] = two ? c[i + 2] : c[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) c[i] = one ? c[i + 1] : c[i];
-    const int bits = (s & 2) * 8;
-    return make_uint4(__funnelshift_r(c[0], c[1], bits), __funnelshift_r(c[1], c[2], bits),
-                      __funnelshift_r(c[2], c[3], bits), __funnelshift_r(c[3], c[4], bits));
-}
-
-// The aligned 16 bytes at p, of which only [lo, hi) may be read; what lies outside is zero.
-template <class T>
-__device__ __noinline__ uint4 load_edge(uintptr_t p, uintptr_t lo, uintptr_t hi) {
-    uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < kVec<T>; ++i) {
-        const uintptr_t at = p + i * sizeof(T);
-        if (at >= lo && at < hi) {
-            if constexpr (sizeof(T) == 4) u[i] = *reinterpret_cast<const uint32_t*>(at);
-            else u[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(at) << (i % 2 * 16);
-        }
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
-}
-
-__device__ __forceinline__ void copy_async(uint32_t dst, uintptr_t src, int bytes) {
+// 16 bytes, of which `bytes` are read and the rest are zero.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int bytes = 16) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint4 load_smem(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
-}
-__device__ __forceinline__ void store_smem(uint32_t at, const uint4& v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -103,96 +62,34 @@ __device__ __forceinline__ void wait_async() {
 }
 
 // A row read and the next one in flight, in shared memory, filled by asynchronous copies.  A
-// thread copies and reads its own packs, so this needs no barrier; of an unaligned row it
-// copies the aligned pieces its packs start in, and finds the next piece in its neighbour's
-// slot (the last lane of a warp copies one piece more).  Layout: [stage][pack][slot].
+// thread copies and reads its own packs, so this needs no barrier.  Layout:
+// [tensor][stage][pack][thread].
 constexpr int kStages = 2;
 
-__host__ __device__ constexpr int ring_slots(int threads) { return threads / 32 * 33; }
-
-// One tensor's share of the ring, and the group's next row of it.
-template <class T, int NV, bool SHIFT>
+template <class T, int NV>
 struct Rows {
-    const char *next = nullptr, *now = nullptr;   // this lane's pack 0 of the row to copy; of the row to read
+    const char* next = nullptr;            // this lane's pack 0 of the row to copy
     int64_t hop = 0;                       // bytes from a group's row to its next
-    uint32_t slot;                         // shared address of this thread's slot, stage 0, pack 0
-    uint32_t per;                          // bytes from a pack's slots to the next pack's
-    uintptr_t lo, hi;                      // SHIFT: the tensor's bytes
-    __device__ __forceinline__ void init(const T* base, int64_t ld, int64_t row, int64_t step, int lane, int64_t M,
-                                         int D, uint32_t smem, int tensor) {
-        next = now = reinterpret_cast<const char*>(base + row * ld) + lane * 16;
+    uint32_t slot = 0;                     // shared address of this thread's slot, stage 0, pack 0
+    uint32_t per = 0;                      // bytes from a pack's slots to the next pack's
+    __device__ __forceinline__ void init(const T* base, int64_t ld, int64_t row, int64_t step, int lane, uint32_t smem,
+                                         int tensor) {
+        next = reinterpret_cast<const char*>(base + row * ld) + lane * 16;
         hop = step * ld * (int64_t)sizeof(T);
-        per = ring_slots(blockDim.x) * 16;
-        slot = smem + tensor * kStages * NV * per + (threadIdx.x / 32 * 33 + threadIdx.x % 32) * 16;
-        lo = reinterpret_cast<uintptr_t>(base);
-        hi = lo + (uintptr_t)((M - 1) * ld + D) * sizeof(T);
+        per = blockDim.x * 16;
+        slot = smem + tensor * kStages * NV * per + threadIdx.x * 16;
     }
     // Copies the group's next row into a stage; `lane16`: 16 x lane, `pitch`: 16 x lanes.
     __device__ __forceinline__ void issue(int stage, int lane16, int pitch, int row_bytes) {
         const uint32_t to = slot + stage * NV * per;
-        if constexpr (!SHIFT) {
 #pragma unroll
-            for (int q = 0; q < NV; ++q)
-                if (q < NV - 1 || q * pitch + lane16 < row_bytes)
-                    copy_async(to + q * per, reinterpret_cast<uintptr_t>(next) + q * pitch, 16);
-        } else {
-            const int m = (int)(reinterpret_cast<uintptr_t>(next) & 15);
-            auto piece = [&](int at, uint32_t dst) {       // the aligned piece at byte `at` - m of the row
-                if (at - m >= row_bytes) return;
-                const uintptr_t p = reinterpret_cast<uintptr_t>(next) - lane16 + at - m;
-                if (p >= lo) copy_async(dst, p, p + 16 <= hi ? 16 : (int)(hi - p));
-                else store_smem(dst, load_edge<T>(p, lo, hi));
-            };
-#pragma unroll
-            for (int q = 0; q < NV; ++q) {
-                piece(q * pitch + lane16, to + q * per);
-                if ((threadIdx.x & 31) == 31) piece(q * pitch + lane16 + 16, to + q * per + 16);
-            }
-        }
+        for (int q = 0; q < NV; ++q)
+            if (q < NV - 1 || q * pitch + lane16 < row_bytes) copy_async(to + q * per, next + q * pitch);
         next += hop;
     }
-    // Pack q of the row to read, once its copies have landed.
-    __device__ __forceinline__ uint4 get(int stage, int q) const {
-        const uint32_t from = slot + (stage * NV + q) * per;
-        const uint4 a = load_smem(from);
-        if constexpr (SHIFT) {
-            const int m = (int)(reinterpret_cast<uintptr_t>(now) & 15);
-            if (m) return shift_bytes(a, load_smem(from + 16), m);
-        }
-        return a;
-    }
-    __device__ __forceinline__ void advance() {
-        if (SHIFT) now += hop;
-    }
+    // Pack q of a stage, once its copies have landed.
+    __device__ __forceinline__ uint4 get(int stage, int q) const { return load_smem(slot + (stage * NV + q) * per); }
 };
-
-// Stores pack k, of which `n` elements (0 .. VEC) are the row's: an aligned piece is stored
-// by the lane whose pack it ends in where both its parts are the row's and the warp's, all
-// else element by element.
-template <class T>
-__device__ __forceinline__ void store_shifted(T* row, int k, int n, const uint4& v) {
-    constexpr int V = kVec<T>;
-    T* p = row + (int64_t)k * V;
-    const int m = (int)(reinterpret_cast<uintptr_t>(row) & 15), lane = threadIdx.x & 31;
-    const int split_at = (16 - m) / (int)sizeof(T);        // elements of the pack before the aligned boundary
-    uint4 prev;
-    prev.x = __shfl_up_sync(0xffffffffu, v.x, 1);
-    prev.y = __shfl_up_sync(0xffffffffu, v.y, 1);
-    prev.z = __shfl_up_sync(0xffffffffu, v.z, 1);
-    prev.w = __shfl_up_sync(0xffffffffu, v.w, 1);
-    const bool piece = n >= split_at && (m == 0 || lane > 0);
-    bool next = __shfl_down_sync(0xffffffffu, piece, 1);
-    if (lane == 31) next = false;
-    if (piece) *reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(p) - m) = m == 0 ? v : shift_bytes(prev, v, 16 - m);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (i < n && (i < split_at ? !piece : !next)) {
-            if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[i] = u[i];
-            else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(u[i / 2] >> (i % 2 * 16));
-        }
-    }
-}
 
 // gamma or beta as fp32 in shared memory: the first 16 bytes of every pack's values, then
 // (16-bit rows) the second 16 bytes of every pack's, so that a warp's 16-byte reads touch
@@ -224,25 +121,18 @@ __device__ __forceinline__ void load_staged(F2* o, uint32_t p, int k, int D) {
     if constexpr (sizeof(T) == 2) unpack16<float>(load_smem(p + padded(D) * 2 + k * 16), o + 2);
 }
 
-// The same from global memory (`n` elements are the row's; !SHIFT: whole packs, aligned).
-template <class T, bool SHIFT>
-__device__ __forceinline__ void load_param16(F2* o, const void* p, int gf32, int k, int n, float none) {
-    constexpr int V = kVec<T>;
-    const bool whole = !SHIFT || (n == V && (reinterpret_cast<uintptr_t>(p) & 15) == 0);
+// One value of gamma or beta.
+template <class T>
+__device__ __forceinline__ float param(const void* p, int gf32, int col, float none, T*) {
+    return p == nullptr ? none : gf32 ? static_cast<const float*>(p)[col] : to_f32(static_cast<const T*>(p)[col]);
+}
+
+// Pack k of one from global memory.
+template <class T>
+__device__ __forceinline__ void load_param16(F2* o, const void* p, int gf32, int k, float none) {
     if (p == nullptr) {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) o[i] = f2(none);
-    } else if (!whole) {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            float f[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int at = k * V + 2 * i + j;
-                f[j] = 2 * i + j >= n ? 0.f : gf32 ? static_cast<const float*>(p)[at] : to_f32(static_cast<const T*>(p)[at]);
-            }
-            o[i] = f2(f[0], f[1]);
-        }
+        for (int i = 0; i < kVec<T> / 2; ++i) o[i] = f2(none);
     } else if (sizeof(T) == 2 && gf32) {
         const uint4* q = reinterpret_cast<const uint4*>(p) + 2 * k;
         unpack16<float>(q[0], o);
@@ -315,95 +205,37 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int group, int lanes, float
 
 // ---------------------------------------------------------------- forward
 
-// What of pack k = q * lanes + lane is the row's: the plan gives a row ceil(packs / lanes)
-// packs a thread, so only the last one can end past it.
-template <class T, int NV, bool SHIFT>
-__device__ __forceinline__ int pack_elements(int q, int k, int D) {
-    constexpr int V = kVec<T>;
-    if (q < NV - 1 && !SHIFT) return V;
-    const int left = D - k * V;
-    return left >= V ? V : left > 0 ? left : 0;
-}
-
-// The packs of an unaligned row that a warp holds, as the aligned pieces they start in: lane
-// l's of pack q, and in lane q the piece that follows pack q of the last lane.
+// Whether pack k = q * lanes + lane is the row's: the plan gives a row ceil(packs / lanes)
+// packs a thread, so only the last one can be past it.
 template <class T, int NV>
-struct Pieces {
-    uint4 a[NV], after;
-    int m;                                 // bytes of the first piece before the row
-    __device__ __forceinline__ void load(const T* row, int lane16, int pitch, int row_bytes, uintptr_t lo, uintptr_t hi) {
-        const uintptr_t start = reinterpret_cast<uintptr_t>(row);
-        const int l = threadIdx.x & 31;
-        m = (int)(start & 15);
-        auto piece = [&](int at) {
-            const uintptr_t p = start - m + at;
-            if (at - m >= row_bytes) return make_uint4(0, 0, 0, 0);
-            if (p >= lo && p + 16 <= hi) return *reinterpret_cast<const uint4*>(p);
-            return load_edge<T>(p, lo, hi);
-        };
-#pragma unroll
-        for (int q = 0; q < NV; ++q) a[q] = piece(q * pitch + lane16);
-        after = l < NV ? piece(l * pitch + lane16 - l * 16 + 512) : make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ uint4 pack(int q) const {
-        if (m == 0) return a[q];
-        uint4 b;
-        const bool last = (threadIdx.x & 31) == 31;
-        const uint32_t own[4] = {a[q].x, a[q].y, a[q].z, a[q].w}, end[4] = {after.x, after.y, after.z, after.w};
-        uint32_t next[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t n = __shfl_down_sync(0xffffffffu, own[i], 1), e = __shfl_sync(0xffffffffu, end[i], q);
-            next[i] = last ? e : n;
-        }
-        b = make_uint4(next[0], next[1], next[2], next[3]);
-        return shift_bytes(a[q], b, m);
-    }
-};
+__device__ __forceinline__ bool in_row(int q, int k, int D) {
+    return q < NV - 1 || k * kVec<T> < D;
+}
 
 // One row for each group of `lanes` threads: a CTA is one row of more than a warp, or four
 // rows of one.  Many small CTAs take turns at loading, reducing and storing; a persistent
 // form with the next row in flight in shared memory took 57 us where this takes 53
 // (11136 x 3584 bf16).  The statistics need one barrier: a warp centres its columns on its
 // own mean, and the warps' (mean, sum of squares about it) are joined exactly.
-template <class T, int NV, bool SHIFT, bool RES, int THREADS, int CTAS>
+template <class T, int NV, bool RES, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) layer_norm_fwd_kernel(const NormFwd a) {
     constexpr int V = kVec<T>, P = V / 2;
     __shared__ float2 red[THREADS / 32];
     const int lanes = a.lanes, lane = threadIdx.x % lanes, D = a.D;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / lanes) + threadIdx.x / lanes;
     if (row >= a.M) return;                // whole warps; with more than one warp a row, no thread
-    const int lane16 = lane * 16, pitch = lanes * 16, row_bytes = D * (int)sizeof(T);
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    const T* r = static_cast<const T*>(a.r) + row * a.ldr;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + row * a.ldx);
+    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const T*>(a.r) + row * a.ldr);
     F2 v[NV * P];
-    if constexpr (SHIFT) {
-        const uintptr_t x0 = reinterpret_cast<uintptr_t>(a.x), r0 = reinterpret_cast<uintptr_t>(a.r);
-        Pieces<T, NV> px, pr;
-        px.load(x, lane16, pitch, row_bytes, x0, x0 + ((a.M - 1) * a.ldx + D) * sizeof(T));
-        if (RES) pr.load(r, lane16, pitch, row_bytes, r0, r0 + ((a.M - 1) * a.ldr + D) * sizeof(T));
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            const int n = pack_elements<T, NV, SHIFT>(q, q * lanes + lane, D);
-            F2* w = v + q * P;
-            unpack16<T>(px.pack(q), w);
-            if (RES) {
-                F2 f[P];
-                unpack16<T>(pr.pack(q), f);
-#pragma unroll
-                for (int i = 0; i < P; ++i) w[i] = w[i] + f[i];
-            }
-            if (n < V) keep_first<T>(w, n);
-        }
-    } else {
+    {
         uint4 px[NV], pr[NV];
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
             const int k = q * lanes + lane;
             px[q] = pr[q] = make_uint4(0, 0, 0, 0);
-            if (pack_elements<T, NV, SHIFT>(q, k, D)) {
-                px[q] = __ldcs(reinterpret_cast<const uint4*>(x) + k);
-                if (RES) pr[q] = __ldcs(reinterpret_cast<const uint4*>(r) + k);
+            if (in_row<T, NV>(q, k, D)) {
+                px[q] = __ldcs(x + k);
+                if (RES) pr[q] = __ldcs(r + k);
             }
         }
 #pragma unroll
@@ -419,14 +251,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) layer_norm_fwd_kernel(const Nor
         }
     }
     if (RES) {
-        T* si = static_cast<T*>(a.s) + row * a.lds;
+        uint4* s = reinterpret_cast<uint4*>(static_cast<T*>(a.s) + row * a.lds);
 #pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            const int k = q * lanes + lane, n = pack_elements<T, NV, SHIFT>(q, k, D);
-            const uint4 o = pack16<T>(v + q * P);
-            if (SHIFT) store_shifted<T>(si, k, n, o);
-            else if (n) reinterpret_cast<uint4*>(si)[k] = o;
-        }
+        for (int q = 0; q < NV; ++q)
+            if (in_row<T, NV>(q, q * lanes + lane, D)) s[q * lanes + lane] = pack16<T>(v + q * P);
     }
     F2 sum2 = f2(0.f);
 #pragma unroll
@@ -443,20 +271,17 @@ __global__ void __launch_bounds__(THREADS, CTAS) layer_norm_fwd_kernel(const Nor
     };
     const float2 ss = split(sum2);
     const int warp = (threadIdx.x % lanes) >> 5, warps = lanes >> 5;
-    const float mine = columns(warp);
-    float mean = warp_sum(ss.x + ss.y) / fmaxf(mine, 1.f);
+    float mean = warp_sum(ss.x + ss.y) / columns(warp);
     const F2 mu = f2(-mean);
     F2 sq2 = f2(0.f);
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
-        const int n = pack_elements<T, NV, SHIFT>(q, q * lanes + lane, D);
-        if (n > 0) {
-            F2 c[P];
+        if (in_row<T, NV>(q, q * lanes + lane, D)) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) c[i] = v[q * P + i] + mu;
-            if (SHIFT && n < V) keep_first<T>(c, n);
-#pragma unroll
-            for (int i = 0; i < P; ++i) sq2 = fma(c[i], c[i], sq2);
+            for (int i = 0; i < P; ++i) {
+                const F2 c = v[q * P + i] + mu;
+                sq2 = fma(c, c, sq2);
+            }
         }
     }
     const float2 qq = split(sq2);
@@ -475,23 +300,78 @@ __global__ void __launch_bounds__(THREADS, CTAS) layer_norm_fwd_kernel(const Nor
     }
     const float rstd = __frsqrt_rn(sq / (float)D + a.eps);
     const F2 rs = f2(rstd), m2 = f2(-mean);
-    T* yi = static_cast<T*>(a.y) + row * a.ldy;
+    uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.ldy);
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
-        const int k = q * lanes + lane, n = pack_elements<T, NV, SHIFT>(q, k, D);
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (n > 0) {
+        const int k = q * lanes + lane;
+        if (in_row<T, NV>(q, k, D)) {
             F2 g[P], b[P];
-            load_param16<T, SHIFT>(g, a.gamma, a.gf32, k, n, 1.f);
-            load_param16<T, SHIFT>(b, a.beta, a.gf32, k, n, 0.f);
+            load_param16<T>(g, a.gamma, a.gf32, k, 1.f);
+            load_param16<T>(b, a.beta, a.gf32, k, 0.f);
 #pragma unroll
             for (int i = 0; i < P; ++i) g[i] = fma((v[q * P + i] + m2) * rs, g[i], b[i]);
-            o = pack16<T>(g);
-            if (!SHIFT) __stcs(reinterpret_cast<uint4*>(yi) + k, o);
+            __stcs(y + k, pack16<T>(g));
         }
-        if (SHIFT) store_shifted<T>(yi, k, n, o);
     }
     if (lane == 0 && a.mean) {
+        a.mean[row] = mean;
+        a.rstd[row] = rstd;
+    }
+}
+
+// Rows off 16-byte boundaries (odd widths, strides, bases), element by element: thread t of a
+// row's THREADS has columns t + i * THREADS, i < kCols, whose offsets are constants; kCols
+// loads a thread keep enough bytes in flight, and a warp still reads 64 or 128 bytes in a row.
+constexpr int kCols = 16;
+
+template <class T, bool RES, int THREADS>
+__global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS, THREADS > 128 ? 2 : 8)
+    layer_norm_fwd_narrow_kernel(const NormFwd a) {
+    __shared__ __align__(16) float red[2 * kRed];
+    const int t = threadIdx.x % THREADS, D = a.D;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / THREADS) + threadIdx.x / THREADS;
+    if (THREADS > 32) {
+        if (threadIdx.x < 2 * kRed) red[threadIdx.x] = 0.f;
+        __syncthreads();
+    }
+    if (row >= a.M) return;
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx + t;
+    const T* r = static_cast<const T*>(a.r) + row * a.ldr + t;
+    float v[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+        v[i] = 0.f;
+        if (t + i * THREADS < D) v[i] = to_f32(x[i * THREADS]);
+    }
+    if (RES) {
+        T* s = static_cast<T*>(a.s) + row * a.lds + t;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+            if (t + i * THREADS < D) v[i] += to_f32(r[i * THREADS]);
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+            if (t + i * THREADS < D) s[i * THREADS] = from_f32<T>(v[i]);
+    }
+    float sum = 0.f, sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) sum += v[i];
+    const float mean = row_sum(sum, 0, THREADS, red, 0) / (float)D;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+        v[i] -= mean;
+        if (t + i * THREADS < D) sq += v[i] * v[i];
+    }
+    const float rstd = __frsqrt_rn(row_sum(sq, 0, THREADS, red, 1) / (float)D + a.eps);
+    T* y = static_cast<T*>(a.y) + row * a.ldy + t;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+        if (t + i * THREADS < D) {
+            const float g = param(a.gamma, a.gf32, t + i * THREADS, 1.f, (T*)nullptr);
+            const float b = param(a.beta, a.gf32, t + i * THREADS, 0.f, (T*)nullptr);
+            y[i * THREADS] = from_f32<T>(v[i] * rstd * g + b);
+        }
+    }
+    if (t == 0 && a.mean) {
         a.mean[row] = mean;
         a.rstd[row] = rstd;
     }
@@ -572,7 +452,7 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_wide_kernel(const 
 // dx = g * rstd + s * A + B with A = -c2 * rstd^2, B = c2 * mean * rstd^2 - c1 * rstd.
 // Shared memory: red [groups][2][kRed] pairs, gamma (whole packs, fp32), then the rows in
 // flight, and after them the groups' column sums in their place.
-template <class T, int NV, bool SHIFT, bool SKIP>
+template <class T, int NV, bool SKIP>
 __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormBwd a) {
     constexpr int V = kVec<T>, P = V / 2;
     extern __shared__ uint4 smem[];
@@ -585,10 +465,10 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
     int64_t row = (int64_t)blockIdx.x * rows + group;
     const int lane16 = lane * 16, pitch = lanes * 16, row_bytes = D * (int)sizeof(T);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(acc);
-    Rows<T, NV, SHIFT> dy, s, skip;
-    dy.init(static_cast<const T*>(a.dy), a.lddy, row, step, lane, a.M, D, ring, 0);
-    s.init(static_cast<const T*>(a.s), a.lds, row, step, lane, a.M, D, ring, 1);
-    if (SKIP) skip.init(static_cast<const T*>(a.skip), a.ldk, row, step, lane, a.M, D, ring, 2);
+    Rows<T, NV> dy, s, skip;
+    dy.init(static_cast<const T*>(a.dy), a.lddy, row, step, lane, ring, 0);
+    s.init(static_cast<const T*>(a.s), a.lds, row, step, lane, ring, 1);
+    if (SKIP) skip.init(static_cast<const T*>(a.skip), a.ldk, row, step, lane, ring, 2);
     auto issue = [&](int stage, int64_t i) {
         if (i < a.M) {
             dy.issue(stage, lane16, pitch, row_bytes);
@@ -609,24 +489,21 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
     float mean = 0.f, rstd = 0.f;
     if (row < a.M) mean = a.mean[row], rstd = a.rstd[row];
     const float inv = 1.f / (float)D;
-    for (int stage = 0; row < a.M; row += step, stage ^= 1, dy.advance(), s.advance(), skip.advance()) {
-        if (SHIFT) __syncwarp();           // the neighbours have read the stage that is filled next
+    for (int stage = 0; row < a.M; row += step, stage ^= 1) {
         issue(stage ^ 1, row + step);
         const float mu = mean, rs = rstd;
         if (row + step < a.M) mean = a.mean[row + step], rstd = a.rstd[row + step];
         wait_async<1>();
-        if (SHIFT) __syncwarp();
         const F2 rs2 = f2(rs), shift = f2(-mu * rs);
         F2 c1 = f2(0.f), c2 = f2(0.f);
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int k = q * lanes + lane, n = pack_elements<T, NV, SHIFT>(q, k, D);
-            if (n > 0) {
+            const int k = q * lanes + lane;
+            if (in_row<T, NV>(q, k, D)) {
                 F2 w[P], d[P], xs[P];
                 load_staged<T>(w, gamma_at, k, D);
                 unpack16<T>(dy.get(stage, q), d);
                 unpack16<T>(s.get(stage, q), xs);
-                if (SHIFT && n < V) keep_first<T>(d, n), keep_first<T>(xs, n);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     const F2 xh = fma(xs[i], rs2, shift), g = d[i] * w[i];
@@ -642,12 +519,11 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
         c.x *= inv * rs;
         c.y *= inv * rs;
         const F2 A = f2(-c.y * rs), B = f2(c.y * mu * rs - c.x);
-        T* oi = static_cast<T*>(a.dx) + row * a.lddx;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.lddx);
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int k = q * lanes + lane, n = pack_elements<T, NV, SHIFT>(q, k, D);
-            uint4 o = make_uint4(0, 0, 0, 0);
-            if (n > 0) {
+            const int k = q * lanes + lane;
+            if (in_row<T, NV>(q, k, D)) {
                 F2 w[P], d[P], xs[P];
                 load_staged<T>(w, gamma_at, k, D);
                 unpack16<T>(dy.get(stage, q), d);
@@ -659,10 +535,8 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
 #pragma unroll
                     for (int i = 0; i < P; ++i) w[i] = w[i] + d[i];
                 }
-                o = pack16<T>(w);
-                if (!SHIFT) reinterpret_cast<uint4*>(oi)[k] = o;
+                o[k] = pack16<T>(w);
             }
-            if (SHIFT) store_shifted<T>(oi, k, n, o);
         }
     }
     if (a.pg == nullptr && a.pb == nullptr) return;
@@ -674,7 +548,7 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
 #pragma unroll
     for (int q = 0; q < NV; ++q) {
         const int k = q * lanes + lane;
-        if (pack_elements<T, NV, true>(q, k, D) > 0) {
+        if (in_row<T, NV>(q, k, D)) {
 #pragma unroll
             for (int h = 0; h < P / 2; ++h) {
                 const float2 g0 = split(dg[q * P + 2 * h]), g1 = split(dg[q * P + 2 * h + 1]);
@@ -691,6 +565,110 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
         for (int w = 0; w < rows; ++w, p += 2 * width) g += p[0], b += p[width];
         if (a.pg) a.pg[(int64_t)blockIdx.x * D + c] = g;
         if (a.pb) a.pb[(int64_t)blockIdx.x * D + c] = b;
+    }
+}
+
+// Rows off 16-byte boundaries: THREADS threads walk the rows of a worker (a warp, or the CTA),
+// whose column sums are its own partial plane.  A row comes to shared memory in the aligned
+// 16-byte pieces that cover it, one row ahead, and is read there element by element (loaded
+// to registers instead, 2 bytes at a time, it took 200 us where this takes @@ for
+// 4864 x 5003 bf16).  Shared memory: [worker][stage][tensor][pitch bytes].
+__host__ __device__ constexpr int narrow_pitch(int row_bytes) { return (row_bytes + 14) / 16 * 16 + 16; }
+
+template <class T>
+__device__ __forceinline__ void copy_row(char* to, const T* base, int64_t ld, int64_t i, int64_t M, int D, int t, int threads) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(base), hi = lo + (uintptr_t)((M - 1) * ld + D) * sizeof(T);
+    const uintptr_t start = lo + (uintptr_t)(i * ld) * sizeof(T), first = start & ~uintptr_t(15);
+    const int pieces = (int)((start + (uintptr_t)D * sizeof(T) - first + 15) / 16);
+    for (int p = t; p < pieces; p += threads) {
+        const uintptr_t from = first + (uintptr_t)p * 16;
+        char* dst = to + p * 16;
+        if (from >= lo) {
+            copy_async((uint32_t)__cvta_generic_to_shared(dst), reinterpret_cast<const void*>(from),
+                       from + 16 <= hi ? 16 : (int)(hi - from));
+        } else {                           // the tensor starts inside this piece
+            for (uintptr_t e = lo; e < from + 16 && e < hi; e += sizeof(T))
+                *reinterpret_cast<T*>(dst + (e - from)) = *reinterpret_cast<const T*>(e);
+        }
+    }
+}
+
+template <class T, bool SKIP, int THREADS>
+__global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS, THREADS > 128 ? 1 : 4)
+    layer_norm_bwd_narrow_kernel(const NormBwd a) {
+    constexpr int TENSORS = SKIP ? 3 : 2;
+    __shared__ __align__(16) float2 red[2 * kRed];
+    extern __shared__ uint4 smem[];
+    const int t = threadIdx.x % THREADS, D = a.D, pitch = narrow_pitch(D * (int)sizeof(T));
+    const int64_t worker = (int64_t)blockIdx.x * (blockDim.x / THREADS) + threadIdx.x / THREADS;
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x / THREADS);
+    char* rows = reinterpret_cast<char*>(smem) + threadIdx.x / THREADS * 2 * TENSORS * pitch;
+    cudaTriggerProgrammaticLaunchCompletion();
+    if (THREADS > 32) {
+        if (threadIdx.x < 2 * kRed) red[threadIdx.x] = make_float2(0.f, 0.f);
+    }
+    const T* src[3] = {static_cast<const T*>(a.dy), static_cast<const T*>(a.s), static_cast<const T*>(a.skip)};
+    const int64_t ld[3] = {a.lddy, a.lds, a.ldk};
+    auto issue = [&](int stage, int64_t i) {
+        if (i < a.M) {
+#pragma unroll
+            for (int k = 0; k < TENSORS; ++k)
+                copy_row<T>(rows + (stage * TENSORS + k) * pitch, src[k], ld[k], i, a.M, D, t, THREADS);
+        }
+        commit_async();
+    };
+    // this thread's first element of a tensor's row in a stage
+    auto at = [&](int stage, int k, int64_t i) {
+        const int m = (int)(reinterpret_cast<uintptr_t>(src[k] + i * ld[k]) & 15);
+        return reinterpret_cast<const T*>(rows + (stage * TENSORS + k) * pitch + m) + t;
+    };
+    float dg[kCols], db[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) dg[j] = db[j] = 0.f;
+    int64_t row = worker;
+    issue(0, row);
+    const float inv = 1.f / (float)D;
+    for (int stage = 0; row < a.M; row += step, stage ^= 1) {
+        const float mu = a.mean[row], rs = a.rstd[row];
+        wait_async<0>();
+        if (THREADS > 32) group_sync(0, THREADS);          // all pieces are here, and the other stage has been read
+        else __syncwarp();
+        issue(stage ^ 1, row + step);
+        const T *y = at(stage, 0, row), *s = at(stage, 1, row);
+        float g[kCols], xh[kCols];
+        float2 c = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+            if (t + j * THREADS < D) {
+                const float d = to_f32(y[j * THREADS]);
+                xh[j] = (to_f32(s[j * THREADS]) - mu) * rs;
+                g[j] = d * param(a.gamma, a.gf32, t + j * THREADS, 1.f, (T*)nullptr);
+                dg[j] += d * xh[j];
+                db[j] += d;
+                c.x += g[j];
+                c.y += g[j] * xh[j];
+            }
+        }
+        c = row_sum2(c, 0, THREADS, red, stage);
+        c.x *= inv;
+        c.y *= inv;
+        T* o = static_cast<T*>(a.dx) + row * a.lddx + t;
+        const T* k = at(stage, SKIP ? 2 : 0, row);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+            if (t + j * THREADS < D) {
+                float v = rs * (g[j] - c.x - xh[j] * c.y);
+                if (SKIP) v += to_f32(k[j * THREADS]);
+                o[j * THREADS] = from_f32<T>(v);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+        if (t + j * THREADS < D) {
+            if (a.pg) a.pg[worker * D + t + j * THREADS] = dg[j];
+            if (a.pb) a.pb[worker * D + t + j * THREADS] = db[j];
+        }
     }
 }
 
@@ -802,7 +780,7 @@ struct NormPlan {
 constexpr int kFwdPacks = 4, kBwdPacks = 4;
 constexpr size_t kSmem = 227 * 1024;
 
-size_t row_smem(const NormPlan& p, int tensors) { return (size_t)kStages * tensors * p.nv * ring_slots(p.threads()) * 16; }
+size_t row_smem(const NormPlan& p, int tensors) { return (size_t)kStages * tensors * p.nv * p.threads() * 16; }
 size_t bwd_smem(const NormPlan& p, int64_t D, bool skip) {
     const size_t rows = row_smem(p, skip ? 3 : 2), sums = (size_t)p.groups * 2 * padded((int)D) * 4;
     return (size_t)p.groups * 4 * kRed * 4 + (size_t)padded((int)D) * 4 + (rows > sums ? rows : sums);
@@ -842,6 +820,15 @@ int bwd_ctas(int64_t M, const NormPlan& p) {
 // Widest rows these forms take, by the backward's shared memory: 24 KB, that is 12288 columns
 // of 16 bits.
 constexpr int64_t kMaxRowBytes = 384 * kBwdPacks * 16;
+
+// Rows element by element: THREADS of a row, and (backward) workers that share the rows; each
+// worker has a partial plane, so the wider the row, the fewer.  Wider than 8192: two passes.
+int narrow_threads(int64_t D) { return D <= 32 * kCols ? 32 : D <= 128 * kCols ? 128 : 512; }
+constexpr int64_t kNarrowWidth = 512 * kCols;
+int64_t narrow_workers(int64_t M, int64_t D) {
+    const int64_t most = kPlanSms * (int64_t)(narrow_threads(D) == 32 ? 16 : narrow_threads(D) == 128 ? 4 : 1);
+    return M < most ? M : most;
+}
 
 int64_t wide_row_ranges(int64_t M, int64_t D, int vec) {
     const int64_t blocks = (D + 256 * vec - 1) / (256 * vec);
@@ -883,46 +870,56 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 struct LaunchFwd {
     const NormFwd& a;
     const NormPlan& p;
-    bool shift;
+    bool shift;                            // rows off 16-byte boundaries
     cudaStream_t s;
-    template <class T, int NV, bool SHIFT, bool RES>
+    template <class T, int NV, bool RES>
     cudaError_t go() const {
-        // 64 (unaligned rows: 80) registers for the small CTAs, whose number hides the latencies;
-        // the larger ones all hold 4 packs a thread
-        auto kern = layer_norm_fwd_kernel<T, NV, SHIFT, RES, 128, SHIFT ? 6 : 8>;
+        // 64 registers for the small CTAs, whose number hides the latencies; the larger ones
+        // all hold 4 packs a thread
+        auto kern = layer_norm_fwd_kernel<T, NV, RES, 128, 8>;
         if constexpr (NV == 4) {
-            if (p.threads() > 128) kern = layer_norm_fwd_kernel<T, NV, SHIFT, RES, 384, 2>;
+            if (p.threads() > 128) kern = layer_norm_fwd_kernel<T, NV, RES, 384, 2>;
         }
         kern<<<(unsigned)((a.M + p.groups - 1) / p.groups), p.threads(), 0, s>>>(a);
         return cudaGetLastError();
     }
     template <class T, int NV>
-    cudaError_t forms() const {
-        if (shift) return a.r ? go<T, NV, true, true>() : go<T, NV, true, false>();
-        return a.r ? go<T, NV, false, true>() : go<T, NV, false, false>();
+    cudaError_t res() const {
+        return a.r ? go<T, NV, true>() : go<T, NV, false>();
+    }
+    template <class T, int THREADS>
+    cudaError_t narrow() const {
+        constexpr int rows = THREADS == 32 ? 4 : 1;
+        auto kern = a.r ? layer_norm_fwd_narrow_kernel<T, true, THREADS> : layer_norm_fwd_narrow_kernel<T, false, THREADS>;
+        kern<<<(unsigned)((a.M + rows - 1) / rows), THREADS * rows, 0, s>>>(a);
+        return cudaGetLastError();
     }
     template <class T>
     cudaError_t run() const {
-        if ((int64_t)a.D * (int)sizeof(T) > kMaxRowBytes) {
+        if (shift ? a.D > kNarrowWidth : (int64_t)a.D * (int)sizeof(T) > kMaxRowBytes) {
             const unsigned grid = (unsigned)(a.M < kPlanSms * 4 ? a.M : kPlanSms * 4);
             if (shift) layer_norm_fwd_wide_kernel<T, 1><<<grid, kMaxThreads, 0, s>>>(a);
             else layer_norm_fwd_wide_kernel<T, kVec<T>><<<grid, kMaxThreads, 0, s>>>(a);
             return cudaGetLastError();
         }
-        return p.nv == 1 ? forms<T, 1>() : p.nv == 2 ? forms<T, 2>() : p.nv == 3 ? forms<T, 3>() : forms<T, 4>();
+        if (shift) {
+            const int n = narrow_threads(a.D);
+            return n == 32 ? narrow<T, 32>() : n == 128 ? narrow<T, 128>() : narrow<T, 512>();
+        }
+        return p.nv == 1 ? res<T, 1>() : p.nv == 2 ? res<T, 2>() : p.nv == 3 ? res<T, 3>() : res<T, 4>();
     }
 };
 
 struct LaunchBwd {
     const NormBwd& a;
     const NormPlan& p;
-    bool shift;
+    bool shift;                            // rows off 16-byte boundaries
     float2* sums;
     int planes;
     cudaStream_t s;
-    template <class T, int NV, bool SHIFT, bool SKIP>
+    template <class T, int NV, bool SKIP>
     cudaError_t go() const {
-        auto kern = layer_norm_bwd_kernel<T, NV, SHIFT, SKIP>;
+        auto kern = layer_norm_bwd_kernel<T, NV, SKIP>;
         const size_t smem = bwd_smem(p, a.D, SKIP);
         cudaError_t e = allow_smem(kern, smem);
         if (e != cudaSuccess) return e;
@@ -930,9 +927,18 @@ struct LaunchBwd {
         return cudaGetLastError();
     }
     template <class T, int NV>
-    cudaError_t forms() const {
-        if (shift) return a.skip ? go<T, NV, true, true>() : go<T, NV, true, false>();
-        return a.skip ? go<T, NV, false, true>() : go<T, NV, false, false>();
+    cudaError_t res() const {
+        return a.skip ? go<T, NV, true>() : go<T, NV, false>();
+    }
+    template <class T, int THREADS>
+    cudaError_t narrow() const {
+        constexpr int rows = THREADS == 32 ? 4 : 1;
+        auto kern = a.skip ? layer_norm_bwd_narrow_kernel<T, true, THREADS> : layer_norm_bwd_narrow_kernel<T, false, THREADS>;
+        const size_t smem = (size_t)rows * 2 * (a.skip ? 3 : 2) * narrow_pitch(a.D * (int)sizeof(T));
+        cudaError_t e = allow_smem(kern, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)(planes / rows), THREADS * rows, smem, s>>>(a);
+        return cudaGetLastError();
     }
     template <class T, int VEC>
     cudaError_t wide() const {
@@ -944,8 +950,13 @@ struct LaunchBwd {
     }
     template <class T>
     cudaError_t run() const {
-        if ((int64_t)a.D * (int)sizeof(T) > kMaxRowBytes) return shift ? wide<T, 1>() : wide<T, kVec<T>>();
-        return p.nv == 1 ? forms<T, 1>() : p.nv == 2 ? forms<T, 2>() : p.nv == 3 ? forms<T, 3>() : forms<T, 4>();
+        if (shift && a.D > kNarrowWidth) return wide<T, 1>();
+        if (!shift && (int64_t)a.D * (int)sizeof(T) > kMaxRowBytes) return wide<T, kVec<T>>();
+        if (shift) {
+            const int n = narrow_threads(a.D);
+            return n == 32 ? narrow<T, 32>() : n == 128 ? narrow<T, 128>() : narrow<T, 512>();
+        }
+        return p.nv == 1 ? res<T, 1>() : p.nv == 2 ? res<T, 2>() : p.nv == 3 ? res<T, 3>() : res<T, 4>();
     }
 };
 
@@ -997,12 +1008,16 @@ swiglu_status swiglu_mlp_layer_norm_fwd(const void* x, int64_t ldx, const void* 
 
 size_t swiglu_mlp_layer_norm_bwd_workspace_size(int64_t M, int64_t D) {
     if (M <= 0 || D <= 0) return 0;
-    // whatever the type and the alignment: one plane an SM, or the two-pass form's row sums and
-    // the planes of its widest packs, which have the most row ranges
-    const size_t narrow = 2 * round256((size_t)(M < kPlanSms ? M : kPlanSms) * D * 4);
-    if (D * 4 <= kMaxRowBytes) return narrow;
-    const size_t wide = round256((size_t)M * sizeof(float2)) + 2 * round256((size_t)wide_row_ranges(M, D, 8) * D * 4);
-    return narrow > wide ? narrow : wide;
+    // whatever the type and the alignment: the most planes of the forms that take rows of this
+    // width (the two-pass form: row sums too, and the widest packs have the most row ranges)
+    int64_t planes = M < kPlanSms ? M : kPlanSms;
+    if (D <= kNarrowWidth && (narrow_workers(M, D) + 3) / 4 * 4 > planes) planes = (narrow_workers(M, D) + 3) / 4 * 4;
+    size_t sums = 0;
+    if (D * 4 > kMaxRowBytes) {
+        sums = round256((size_t)M * sizeof(float2));
+        if (wide_row_ranges(M, D, 8) > planes) planes = wide_row_ranges(M, D, 8);
+    }
+    return sums + 2 * round256((size_t)planes * D * 4);
 }
 
 swiglu_status swiglu_mlp_layer_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const void* gamma,
@@ -1039,10 +1054,13 @@ swiglu_status swiglu_mlp_layer_norm_bwd(const void* dy, int64_t lddy, const void
     if (rc != SWIGLU_OK) return rc;
     Aligned v{(int)n};
     v.add(dy, lddy), v.add(s, lds), v.add(dskip, ldskip), v.add(dx, lddx), v.add(dy, D);
-    if (D * (int64_t)n > kMaxRowBytes) v.add(gamma, 0);
+    if (D * (int64_t)n > kMaxRowBytes) v.add(gamma, 0);   // read in packs there
     const NormPlan p = bwd_plan(M, D, (int)n, dskip != nullptr);
-    const bool wide = D * (int64_t)n > kMaxRowBytes, shift = !v.ok();
-    const int planes = (int)(wide ? wide_row_ranges(M, D, shift ? 1 : 16 / (int)n) : bwd_ctas(M, p));
+    const bool shift = !v.ok(), wide = shift ? D > kNarrowWidth : D * (int64_t)n > kMaxRowBytes;
+    // a worker of one warp comes with three others
+    const int planes = (int)(wide    ? wide_row_ranges(M, D, shift ? 1 : 16 / (int)n)
+                             : shift ? narrow_threads(D) == 32 ? (narrow_workers(M, D) + 3) / 4 * 4 : narrow_workers(M, D)
+                                     : bwd_ctas(M, p));
     uint8_t* w = static_cast<uint8_t*>(workspace);
     float2* sums = reinterpret_cast<float2*>(w);
     if (wide) w += round256((size_t)M * sizeof(float2));
