@@ -100,6 +100,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded C library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -584,34 +586,53 @@ def swiglu_moe_routed_fwd(x, Wr, W1, W2, top_k: int, renormalize: bool = True, r
     """A whole MoE layer for up to 64 tokens, routed on the device: returns (y [T,Dout] bf16,
     ids [T,top_k] int32, gates [T,top_k] fp32).  Wr [E,D] bf16 or fp32; residual [T,Dout] is
     added to y; renormalize: the chosen gates sum to one."""
-    T, E, D, H, Dout = _moe_dims(x, W1, W2)
-    if Wr.dtype != torch.float32:
-        _expect(Wr, "Wr", (E, D), torch.bfloat16, x.device)
-    else:
-        _expect(Wr, "Wr", (E, D), torch.float32, x.device)
-    if residual is not None:
-        _expect(residual, "residual", (T, Dout), torch.bfloat16, x.device)
-    y = _out(y, "y", (T, Dout), x)
-    ids = _out(ids, "ids", (T, top_k), x, torch.int32)
-    gates = _out(gates, "gates", (T, top_k), x, torch.float32)
-    _same_device(x, workspace=workspace)
+    if x.dim() != 2 or W1.dim() != 3 or W2.dim() != 3:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, W1 {tuple(W1.shape)}, W2 {tuple(W2.shape)}")
+    T, D = x.shape
+    E, Dout, H = W2.shape
+    bf, device = torch.bfloat16, x.device
+    if W1.shape != (E, 2 * H, D):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, W1 {tuple(W1.shape)}, W2 {tuple(W2.shape)}")
+    fp32 = Wr.dtype == torch.float32
+    if y is None:
+        y = torch.empty((T, Dout), dtype=bf, device=device)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
+    if gates is None:
+        gates = torch.empty((T, top_k), dtype=torch.float32, device=device)
     if workspace is None:
         workspace = torch.empty(max(16, swiglu_moe_routed_fwd_workspace_size(T, H, top_k)), dtype=torch.uint8,
-                                device=x.device)
-    for name, t in (("Wr", Wr), ("ids", ids), ("gates", gates)):
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-    st = lib().swiglu_moe_routed_fwd(_ptr(x), Wr.data_ptr(), _ptr(W1), _ptr(W2), _ptr(residual), _ptr(y),
-                                     ids.data_ptr(), gates.data_ptr(), T, E, D, H, Dout, top_k, int(renormalize),
-                                     int(Wr.dtype == torch.float32), _ptr(workspace), _nbytes(workspace),
-                                     _stream(x.device))
-    _check(st, "swiglu_moe_routed_fwd")
+                                device=device)
+    st = lib().swiglu_moe_routed_fwd(
+        _vector(x, "x", (T, D), bf, device), _vector(Wr, "Wr", (E, D), torch.float32 if fp32 else bf, device),
+        _vector(W1, "W1", W1.shape, bf, device), _vector(W2, "W2", W2.shape, bf, device),
+        _vector(residual, "residual", (T, Dout), bf, device), _vector(y, "y", (T, Dout), bf, device),
+        _vector(ids, "ids", (T, top_k), torch.int32, device),
+        _vector(gates, "gates", (T, top_k), torch.float32, device), T, E, D, H, Dout, top_k, bool(renormalize), fp32,
+        _workspace_ptr(workspace, device), _nbytes(workspace), _device_stream(device))
+    if st:
+        _check(st, "swiglu_moe_routed_fwd")
     return y, ids, gates
 
 
 # ---------------------------------------------------------------------------- layer norm
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}      # swiglu_dtype
+
+
+# The calls below are short on the device (a few microseconds for a decode step's tokens), so
+# their checks compare first and explain (in _expect) only on a mismatch, and the stream comes
+# from torch's raw accessor.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _device_stream(device) -> int:
+    """The current stream of `device`, refused where that is not the current CUDA device."""
+    if device.type != "cuda":
+        raise ValueError("tensor must live on a CUDA device")
+    if _raw_stream is None or device.index != torch.cuda.current_device():
+        return _stream(device).value       # raises for another device than the current one
+    return _raw_stream(device.index)
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
@@ -621,39 +642,48 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _rows(t, name: str, shape, like: torch.Tensor):
+def _rows(t, name: str, shape, dtype, device):
     """(pointer, row stride) of a [M, D] tensor whose rows are contiguous; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t is not like:
-        _expect(t, name, shape, like.dtype, like.device)
-    ld = t.stride(0) if shape[0] > 1 else shape[1]
-    if (shape[1] > 1 and t.stride(1) != 1) or ld < shape[1]:
-        raise ValueError(f"{name}: each row must be contiguous and rows must not overlap (strides {t.stride()})")
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _expect(t, name, shape, dtype, device)
+    ld, one = t.stride()
+    if one != 1 or ld < shape[1]:
+        if (one != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
+            raise ValueError(f"{name}: each row must be contiguous and rows must not overlap (strides {t.stride()})")
+        ld = max(ld, shape[1])
     return t.data_ptr(), ld
 
 
-def _device_stream(device) -> ctypes.c_void_p:
-    """The current stream of `device`, refused where that is no CUDA device."""
-    if device.type != "cuda":
-        raise ValueError("tensor must live on a CUDA device")
-    return _stream(device)
-
-
-def _vector(t, name: str, n: int, dtype, like: torch.Tensor):
-    """Pointer of a contiguous vector of n elements, or None."""
+def _vector(t, name: str, shape, dtype, device):
+    """Pointer of a contiguous tensor, or None."""
     if t is None:
         return None
-    _expect(t, name, (n,), dtype, like.device)
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _expect(t, name, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _new_rows(like: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype,
+                                                                          device=like.device)
+
+
+def _workspace_ptr(t: torch.Tensor, device):
+    if t.device != device:
+        raise ValueError(f"workspace: on {t.device}, the call's other tensors are on {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
     return t.data_ptr()
 
 
 def _norm_params(x, gamma, beta):
     """dtype of gamma and beta (x's, where there are none)."""
     wdtype = gamma.dtype if gamma is not None else beta.dtype if beta is not None else x.dtype
-    if wdtype not in (x.dtype, torch.float32):
+    if wdtype != x.dtype and wdtype != torch.float32:
         raise TypeError(f"gamma, beta: {wdtype}, expected {x.dtype} or torch.float32")
     return wdtype
 
@@ -665,27 +695,30 @@ def swiglu_mlp_layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, resid
     [M, D] bf16, fp16 or fp32, rows at any stride; gamma, beta [D] of x's type or fp32."""
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected two dimensions")
-    M, D = x.shape
+    shape, dtype, device = x.shape, x.dtype, x.device
+    M, D = shape
     code, wdtype = _dtype(x, "x"), _norm_params(x, gamma, beta)
-    if s is not None and residual is None:
-        raise ValueError("s: only written with a residual")
-    y = torch.empty((M, D), dtype=x.dtype, device=x.device) if y is None else y
-    if residual is not None and s is None:
-        s = torch.empty((M, D), dtype=x.dtype, device=x.device)
+    if y is None:
+        y = _new_rows(x)
+    if residual is None:
+        if s is not None:
+            raise ValueError("s: only written with a residual")
+    elif s is None:
+        s = _new_rows(x)
     if mean is None:
-        mean = torch.empty(M, dtype=torch.float32, device=x.device)
+        mean = torch.empty(M, dtype=torch.float32, device=device)
     if rstd is None:
-        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
-    px, ldx = _rows(x, "x", (M, D), x)
-    pr, ldr = _rows(residual, "residual", (M, D), x)
-    py, ldy = _rows(y, "y", (M, D), x)
-    ps, lds = _rows(s, "s", (M, D), x)
-    st = lib().swiglu_mlp_layer_norm_fwd(px, ldx, pr, ldr, _vector(gamma, "gamma", D, wdtype, x),
-                                         _vector(beta, "beta", D, wdtype, x), py, ldy, ps, lds,
-                                         _vector(mean, "mean", M, torch.float32, x),
-                                         _vector(rstd, "rstd", M, torch.float32, x), M, D, eps, code, _DTYPES[wdtype],
-                                         _device_stream(x.device))
-    _check(st, "swiglu_mlp_layer_norm_fwd")
+        rstd = torch.empty(M, dtype=torch.float32, device=device)
+    px, ldx = _rows(x, "x", shape, dtype, device)
+    pr, ldr = _rows(residual, "residual", shape, dtype, device)
+    py, ldy = _rows(y, "y", shape, dtype, device)
+    ps, lds = _rows(s, "s", shape, dtype, device)
+    st = lib().swiglu_mlp_layer_norm_fwd(
+        px, ldx, pr, ldr, _vector(gamma, "gamma", (D,), wdtype, device), _vector(beta, "beta", (D,), wdtype, device),
+        py, ldy, ps, lds, _vector(mean, "mean", (M,), torch.float32, device),
+        _vector(rstd, "rstd", (M,), torch.float32, device), M, D, eps, code, _DTYPES[wdtype], _device_stream(device))
+    if st:
+        _check(st, "swiglu_mlp_layer_norm_fwd")
     return y, (x if s is None else s), mean, rstd
 
 
@@ -697,32 +730,38 @@ def swiglu_mlp_layer_norm_bwd(dy, s, gamma, mean, rstd, dskip=None, dx=None, dga
                               param_grads: bool = True):
     """Backward of the layer norm; returns (dx, dgamma, dbeta).  s: the forward's normalised
     input; dskip: a gradient added to dx (the residual stream's).  gamma None (= 1): dgamma
-    and dbeta have the type of the dbeta passed in, or s's.  param_grads False: neither is computed and both are None."""
+    and dbeta have the type of the dbeta passed in, or s's.  param_grads False: neither is
+    computed and both are None."""
     if s.dim() != 2:
         raise ValueError(f"s: shape {tuple(s.shape)}, expected two dimensions")
-    M, D = s.shape
+    shape, dtype, device = s.shape, s.dtype, s.device
+    M, D = shape
     code, wdtype = _dtype(s, "s"), _norm_params(s, gamma, dbeta)
-    dx = torch.empty((M, D), dtype=s.dtype, device=s.device) if dx is None else dx
-    if param_grads:
-        dgamma = _out(dgamma, "dgamma", (D,), s, wdtype)
-        dbeta = _out(dbeta, "dbeta", (D,), s, wdtype)
-    elif dgamma is not None or dbeta is not None:
-        raise ValueError("dgamma, dbeta: not computed with param_grads=False")
-    _same_device(s, workspace=workspace)
+    if dx is None:
+        dx = _new_rows(s)
+    if not param_grads:
+        if dgamma is not None or dbeta is not None:
+            raise ValueError("dgamma, dbeta: not computed with param_grads=False")
+    else:
+        if dgamma is None:
+            dgamma = torch.empty(D, dtype=wdtype, device=device)
+        if dbeta is None:
+            dbeta = torch.empty(D, dtype=wdtype, device=device)
     if workspace is None:
         workspace = torch.empty(max(16, swiglu_mlp_layer_norm_bwd_workspace_size(M, D)), dtype=torch.uint8,
-                                device=s.device)
-    pdy, lddy = _rows(dy, "dy", (M, D), s)
-    ps, lds = _rows(s, "s", (M, D), s)
-    pk, ldk = _rows(dskip, "dskip", (M, D), s)
-    pdx, lddx = _rows(dx, "dx", (M, D), s)
-    st = lib().swiglu_mlp_layer_norm_bwd(pdy, lddy, ps, lds, _vector(gamma, "gamma", D, wdtype, s),
-                                         _vector(mean, "mean", M, torch.float32, s),
-                                         _vector(rstd, "rstd", M, torch.float32, s), pk, ldk, pdx, lddx,
-                                         _vector(dgamma, "dgamma", D, wdtype, s),
-                                         _vector(dbeta, "dbeta", D, wdtype, s), M, D, code, _DTYPES[wdtype],
-                                         _ptr(workspace), _nbytes(workspace), _device_stream(s.device))
-    _check(st, "swiglu_mlp_layer_norm_bwd")
+                                device=device)
+    pdy, lddy = _rows(dy, "dy", shape, dtype, device)
+    ps, lds = _rows(s, "s", shape, dtype, device)
+    pk, ldk = _rows(dskip, "dskip", shape, dtype, device)
+    pdx, lddx = _rows(dx, "dx", shape, dtype, device)
+    st = lib().swiglu_mlp_layer_norm_bwd(
+        pdy, lddy, ps, lds, _vector(gamma, "gamma", (D,), wdtype, device),
+        _vector(mean, "mean", (M,), torch.float32, device), _vector(rstd, "rstd", (M,), torch.float32, device),
+        pk, ldk, pdx, lddx, _vector(dgamma, "dgamma", (D,), wdtype, device),
+        _vector(dbeta, "dbeta", (D,), wdtype, device), M, D, code, _DTYPES[wdtype],
+        _workspace_ptr(workspace, device), _nbytes(workspace), _device_stream(device))
+    if st:
+        _check(st, "swiglu_mlp_layer_norm_bwd")
     return dx, dgamma, dbeta
 
 
@@ -773,46 +812,45 @@ def swiglu_mlp_clip_grads_workspace_size(n: int) -> int:
 
 
 def _grad_arrays(tensors, name: str):
-    """Host arrays (pointers, counts, types) of dense CUDA tensors."""
-    n = len(tensors)
-    ptrs, counts, types = (ctypes.c_void_p * n)(), (_i64 * n)(), (_i32 * n)()
-    device = None
+    """(pointers, counts, type codes) of contiguous tensors on one device, and the device."""
+    device = tensors[0].device
     for i, t in enumerate(tensors):
         if t.device != device:
-            if device is not None:
-                raise ValueError(f"{name}[{i}]: on {t.device}, the call's other tensors are on {device}")
-            device = t.device
+            raise ValueError(f"{name}[{i}]: on {t.device}, the call's other tensors are on {device}")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}]: tensor must be contiguous")
-        code = _DTYPES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{name}[{i}]: {t.dtype}, expected bf16, fp16 or fp32")
-        ptrs[i], counts[i], types[i] = t.data_ptr(), t.numel(), code
-    return ptrs, counts, types, device
+    try:
+        codes = [_DTYPES[t.dtype] for t in tensors]
+    except KeyError:
+        i = next(i for i, t in enumerate(tensors) if t.dtype not in _DTYPES)
+        raise TypeError(f"{name}[{i}]: {tensors[i].dtype}, expected bf16, fp16 or fp32") from None
+    return [t.data_ptr() for t in tensors], [t.numel() for t in tensors], codes, device
 
 
 def _clip_call(grads, max_norm, eps, out, norm, workspace):
     if not grads:
         raise ValueError("grads: empty")
-    ptrs, counts, types, device = _grad_arrays(grads, "grads")
+    n = len(grads)
+    ptrs, counts, codes, device = _grad_arrays(grads, "grads")
+    pointers = ctypes.c_void_p * n
+    ptrs = pointers(*ptrs)
     outs = None
     if out is grads:
         outs = ptrs
     elif out is not None:
-        outs, ocounts, otypes, odevice = _grad_arrays(out, "out")
-        if len(out) != len(grads) or odevice != device or ocounts[:] != counts[:] or otypes[:] != types[:]:
+        outs, ocounts, ocodes, odevice = _grad_arrays(out, "out") if out else (None,) * 4
+        if odevice != device or ocounts != counts or ocodes != codes:
             raise ValueError("out: one tensor of the same type, element count and device for each gradient")
+        outs = pointers(*outs)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=device)
-    else:
-        _expect(norm, "norm", (), torch.float32, device)
     if workspace is None:
-        workspace = torch.empty(swiglu_mlp_clip_grads_workspace_size(len(grads)), dtype=torch.uint8, device=device)
-    elif workspace.device != device:
-        raise ValueError(f"workspace: on {workspace.device}, the call's other tensors are on {device}")
-    st = lib().swiglu_mlp_clip_grads(ptrs, outs, counts, types, len(grads), max_norm, eps, norm.data_ptr(),
-                                     _ptr(workspace), _nbytes(workspace), _device_stream(device))
-    _check(st, "swiglu_mlp_clip_grads")
+        workspace = torch.empty(swiglu_mlp_clip_grads_workspace_size(n), dtype=torch.uint8, device=device)
+    st = lib().swiglu_mlp_clip_grads(ptrs, outs, (_i64 * n)(*counts), (_i32 * n)(*codes), n, max_norm, eps,
+                                     _vector(norm, "norm", (), torch.float32, device),
+                                     _workspace_ptr(workspace, device), _nbytes(workspace), _device_stream(device))
+    if st:
+        _check(st, "swiglu_mlp_clip_grads")
     return norm
 
 

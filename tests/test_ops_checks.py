@@ -172,3 +172,9 @@ def test_routed_layer_refusals(b):
     need = b.swiglu_moe_routed_fwd_workspace_size(4, 64, 2)
     assert need == 4 * 2 * 64 * 2 and call(wsb=need - 1) == WS
     assert b.swiglu_moe_routed_fwd_workspace_size(0, 64, 2) == 0
+
+
+def test_tensors_on_another_device_than_the_current_one_are_refused(b, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        b._device_stream(torch.device("cuda", 0))
