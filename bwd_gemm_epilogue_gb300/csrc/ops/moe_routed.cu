@@ -13,12 +13,17 @@
 //   down   16 output columns of every token: W2 rows of all chosen experts against h,
 //          weighted by the gates and added in registers and shared memory
 //
-// Weights go from global memory straight into the registers of mma.m16n8k16 (A, 16 weight
-// rows) and are never staged: a lane's 16-byte load holds 8 consecutive k of one row, and
-// since a dot product does not care for the order of k, those 8 feed two MMAs (4 k each)
-// as long as the tokens' operand B is loaded with the same assignment.  A warp keeps
-// kDepth steps of 64 k (2 KB of weights each) in flight.
+// Weights (A, 16 rows a warp) go to shared memory by asynchronous 16-byte copies and from
+// there into the registers of mma.m16n8k16.  A warp copies and reads its own stages only, so
+// this ring needs no barrier of the CTA.  A lane's 16 bytes hold 8 consecutive k of one row,
+// and since a dot product does not care for the order of k, those 8 feed two MMAs (4 k each)
+// as long as the tokens' operand B is read with the same assignment.  Copies run ahead across
+// the ends of the warp's segments.  B, the rows of the tokens that chose the expert, is
+// shared by the CTA: every warp reads it from a chunk in shared memory.
 #include <cooperative_groups.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "../host.h"
 #include "convert.cuh"
@@ -33,9 +38,17 @@ constexpr int kPlanSms = 152;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxTop = 16;
 constexpr int kMaxExperts = 682;
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kCtas = kPlanSms * 2;          // two CTAs an SM: 16 warps x kDepth x 2 KB in flight
-constexpr int kDepth = 4;
+constexpr int kWarps = 16, kThreads = kWarps * 32;          // one CTA an SM
+constexpr int kStages = 2;                   // chunks of weights a warp has in flight or in use
+constexpr int kMaxPass = 32, kMinPass = 4;   // tokens of an expert taken at a time (64 / split, at most 32)
+constexpr int kEntries = kMaxExperts + kMaxTokens * kMaxTop / kMinPass;
+constexpr int kRows = 64;                    // tokens x split of a chunk of B
+
+// A chunk is STEPS * 64 k for each k group of the CTA's warps: 16 rows of weights a warp, kRows
+// rows of tokens (with 64 bytes between the rows of a token).
+__host__ __device__ constexpr int stage_bytes(int steps) { return 16 * steps * 128; }
+__host__ __device__ constexpr int ring_bytes(int steps) { return kWarps * kStages * stage_bytes(steps); }
+__host__ __device__ constexpr int token_bytes(int steps) { return kRows * steps * 128 + kMaxPass * 64; }
 
 struct Routed {
     const __nv_bfloat16 *x, *W1, *W2, *r;
@@ -64,17 +77,19 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// One cluster per token; CTA rank c computes the logits of experts c * kWarps + warp,
-// + cluster size * kWarps, ...; the first CTA's first warp chooses.
+constexpr int kRouteWarps = 8;
+
+// One cluster per token; CTA rank c computes the logits of experts c * kRouteWarps + warp,
+// + cluster size * kRouteWarps, ...; the first CTA's first warp chooses.
 template <class W>
-__global__ void __launch_bounds__(kThreads) moe_route_kernel(const Routed a) {
+__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Routed a) {
     __shared__ float logits[kMaxExperts];
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
     const int t = blockIdx.x / ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* all = cluster.map_shared_rank(logits, 0);
     const __nv_bfloat16* x = a.x + (int64_t)t * a.D;
-    for (int e = rank * kWarps + warp; e < a.E; e += ctas * kWarps) {
+    for (int e = rank * kRouteWarps + warp; e < a.E; e += ctas * kRouteWarps) {
         const W* w = static_cast<const W*>(a.Wr) + (int64_t)e * a.D;
         float s = 0.f;
 #pragma unroll 4
@@ -126,68 +141,62 @@ __global__ void __launch_bounds__(kThreads) moe_route_kernel(const Routed a) {
 
 // ---------------------------------------------------------------- what was chosen
 
-// Shared by the up and the down kernel: for every expert the tokens that chose it (a bit
-// each), and the experts chosen at all, in ascending order.
+// Shared by the up and the down kernel: the (token, choice) pairs sorted by expert, and within
+// an expert by token, and the entries of work: up to `pass` pairs of one expert each.
 struct Chosen {
-    unsigned long long tokens[kMaxExperts];
-    short expert[kMaxExperts + 2];
-    short ids[kMaxTokens * kMaxTop];
-    int count;
+    int count, most;                                       // entries; the most pairs of one
+    short expert[kEntries], first[kEntries], pairs[kEntries];
+    short order[kMaxTokens * kMaxTop];                     // pair = token * k + choice
 };
 
-__device__ __forceinline__ void read_choice(Chosen& c, const Routed& a) {
-    for (int e = threadIdx.x; e < a.E; e += kThreads) c.tokens[e] = 0;
+// `scratch`: kMaxExperts x 10 bytes.  Tokens choose an expert at most once, so a bit for each
+// of the 64 tokens is an expert's list, and the list's order does not depend on timing.
+__device__ __forceinline__ void read_choice(Chosen& c, const Routed& a, int pass, void* scratch) {
+    unsigned long long* tokens = static_cast<unsigned long long*>(scratch);
+    short* start = reinterpret_cast<short*>(tokens + kMaxExperts);
+    const int pairs = a.T * a.k;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) tokens[e] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < a.T * a.k; p += kThreads) {
-        const int e = a.ids[p];
-        c.ids[p] = (short)e;
-        atomicOr(&c.tokens[e], 1ull << (p / a.k));
-    }
+    for (int p = threadIdx.x; p < pairs; p += kThreads) atomicOr(&tokens[a.ids[p]], 1ull << (p / a.k));
     __syncthreads();
     if (threadIdx.x < 32) {
-        int n = 0;
+        const int lane = threadIdx.x;
+        int entries = 0, before = 0, most = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + threadIdx.x;
-            const bool in = e < a.E && c.tokens[e] != 0;
-            const unsigned m = __ballot_sync(0xffffffffu, in);
-            if (in) c.expert[n + __popc(m & ((1u << threadIdx.x) - 1))] = (short)e;
-            n += __popc(m);
+            const int e = e0 + lane, n = e < a.E ? __popcll(tokens[e]) : 0, w = (n + pass - 1) / pass;
+            int en = w, pn = n;                            // inclusive sums over the lanes
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int x = __shfl_up_sync(0xffffffffu, en, o), y = __shfl_up_sync(0xffffffffu, pn, o);
+                if (lane >= o) en += x, pn += y;
+            }
+            if (n) start[e] = (short)(before + pn - n);
+            for (int i = 0; i < w; ++i) {
+                const int at = entries + en - w + i, left = n - i * pass;
+                c.expert[at] = (short)e;
+                c.first[at] = (short)(before + pn - n + i * pass);
+                c.pairs[at] = (short)min(left, pass);
+            }
+            most = max(most, min(n, pass));
+            entries += __shfl_sync(0xffffffffu, en, 31);
+            before += __shfl_sync(0xffffffffu, pn, 31);
         }
-        if (threadIdx.x == 0) c.count = n;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) c.count = entries, c.most = most;
     }
     __syncthreads();
-}
-
-// This warp's list of expert e's (token, choice) pairs, in token order: pair = token * k + j.
-// Entries past the count repeat the last pair (their columns are computed and dropped).
-__device__ __forceinline__ int list_pairs(short* list, const Chosen& c, const Routed& a, int e) {
-    const int lane = threadIdx.x & 31;
-    const unsigned long long m = c.tokens[e];
-    const int n = __popcll(m);
-    __syncwarp();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int t = lane + 32 * half;
-        if (m >> t & 1) {
-            int j = 0;
-            while (c.ids[t * a.k + j] != e) ++j;
-            const int at = __popcll(m & ((1ull << t) - 1));
-            list[at] = (short)(t * a.k + j);
-            if (at == n - 1)
-                for (int q = n; q < kMaxTokens; ++q) list[q] = (short)(t * a.k + j);
-        }
+    for (int p = threadIdx.x; p < pairs; p += kThreads) {
+        const int e = a.ids[p], t = p / a.k;
+        c.order[start[e] + __popcll(tokens[e] & ((1ull << t) - 1))] = (short)p;
     }
-    __syncwarp();
-    return n;
+    __syncthreads();
 }
 
 // ---------------------------------------------------------------- products
 
-__device__ __forceinline__ uint4 load_weights(const __nv_bfloat16* p) {
+__device__ __forceinline__ uint4 load_smem(uint32_t at) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
 }
 
@@ -200,127 +209,265 @@ __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// acc += the products of 16 weight rows with NT * 8 token rows over k steps [s0, s1) of 64.
-// Lane (g, q) = (lane / 4, lane % 4): w0, w1 are its weight rows g and g + 8; token row
-// n * 8 + g starts at b + off[n].  acc[n]: rows g and g + 8 x tokens n * 8 + 2 q, + 1.
-template <int NT>
-__device__ __forceinline__ void products(float (*acc)[4], const __nv_bfloat16* w0, const __nv_bfloat16* w1,
-                                         const __nv_bfloat16* b, const int* off, int s0, int s1, int K) {
-    const int q = (threadIdx.x & 3) * 8;
-    uint4 w[kDepth][4];
-    auto load = [&](int d, int s) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const int c = s * 64 + q;
-        const bool in0 = s < s1 && c < K, in1 = s < s1 && c + 32 < K;
-        w[d][0] = in0 ? load_weights(w0 + c) : zero;
-        w[d][1] = in0 ? load_weights(w1 + c) : zero;
-        w[d][2] = in1 ? load_weights(w0 + c + 32) : zero;
-        w[d][3] = in1 ? load_weights(w1 + c + 32) : zero;
-    };
+__device__ __forceinline__ void store_smem(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// A CTA's work is a sequence of segments: an entry's tokens against rows of its expert, over
+// the steps [s, end) of 64 k.  Its kWarps warps are kWarps / split row groups x split k groups; a
+// chunk is STEPS steps of each k group, that is split * STEPS * 64 consecutive k.
+struct Segment {
+    int entry, tile, s, end;
+};
+
+// The weights of one warp, kStages chunks in flight.  A copy instruction takes runs of STEPS *
+// 128 bytes of 4 / STEPS rows: of the run lengths tried on 1.9 GB, 64 bytes a row read at 6.4
+// TB/s and 256 at 6.8, and a run off a 32-byte boundary costs one sector more whatever its
+// length.  Stage: 16 rows of STEPS * 128 bytes; odd rows have the halves of each 128 bytes
+// exchanged, so that a quarter-warp's reads (2 rows x 64 bytes) touch every bank once.
+// `next(segment)` moves on and returns false at the end; `rows(segment, w, second)` gives the
+// warp's rows 0..7 (w) and 8..15 (w + second), `ld` apart, and returns false where it has none.
+template <int STEPS, class Next, class RowsOf>
+struct Weights {
+    static constexpr int kLanes = STEPS * 8, kRun = 32 / kLanes;        // lanes of a row, rows of an instruction
+    Segment g;
+    const __nv_bfloat16* w = nullptr;        // this lane's row and column 0 of a run
+    int64_t second = 0, ld;
+    int at = 0, K, group, hop;               // at: the first step of the chunk copied next
+    bool live, mine = false;
+    uint32_t copy_to, read_from, wr = 0, rd = 0;
+    Next next;
+    RowsOf rows;
+    __device__ __forceinline__ Weights(Next n, RowsOf r, uint32_t ring, int K_, int64_t ld_, int group_, int split)
+        : ld(ld_), K(K_), group(group_), hop(STEPS * split), next(n), rows(r) {
+        const int lane = threadIdx.x & 31, run = lane / kLanes, line = lane % kLanes, g8 = lane >> 2;
+        ring += (threadIdx.x >> 5) * kStages * stage_bytes(STEPS);
+        // kRun is even or 1: a lane's rows are all odd or all even, or (1) the instruction's are
+        copy_to = ring + run * STEPS * 128 + line * 16;
+        read_from = ring + g8 * STEPS * 128 + (((lane & 3) * 16) ^ ((g8 & 1) * 64));
+        enter();
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(d, s0 + d);
-    for (int s = s0; s < s1; s += kDepth) {
+        for (int d = 0; d < kStages; ++d) issue();
+    }
+    __device__ __forceinline__ void enter() {
+        live = next(g);
+        if (!live) return;
+        mine = rows(g, w, second);
+        w += (int64_t)((threadIdx.x & 31) / kLanes) * ld + (threadIdx.x & 31) % kLanes * 8;
+        at = g.s + STEPS * group;
+    }
+    __device__ __forceinline__ void issue() {
+        if (live) {
+            if (mine && at < g.end) {
+                const int c = at * 64, last = g.end * 64 < K ? g.end * 64 : K;
+                const int n = c + (int)(threadIdx.x & 31) % kLanes * 8 < last ? 16 : 0;        // past the row: zeros
+                const uint32_t to = copy_to + (wr & (kStages - 1)) * stage_bytes(STEPS);
+                const __nv_bfloat16* from = w + (n ? c : 0);
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            if (s + d < s1) {
-                const int c = (s + d) * 64 + q;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-                    const uint4 u = c < K ? *reinterpret_cast<const uint4*>(b + off[n] + c) : zero;
-                    const uint4 v = c + 32 < K ? *reinterpret_cast<const uint4*>(b + off[n] + c + 32) : zero;
-                    mma(acc[n], w[d][0].x, w[d][1].x, w[d][0].y, w[d][1].y, u.x, u.y);
-                    mma(acc[n], w[d][0].z, w[d][1].z, w[d][0].w, w[d][1].w, u.z, u.w);
-                    mma(acc[n], w[d][2].x, w[d][3].x, w[d][2].y, w[d][3].y, v.x, v.y);
-                    mma(acc[n], w[d][2].z, w[d][3].z, w[d][2].w, w[d][3].w, v.z, v.w);
+                for (int i = 0; i < 16 / kRun; ++i) {
+                    const int row = i * kRun;              // of the lanes with run 0
+                    const uint32_t odd = ((row + (threadIdx.x & 31) / kLanes) & 1) * 64;
+                    copy((to + row * STEPS * 128) ^ odd, from + (row & 7) * ld + (row < 8 ? 0 : second), n);
                 }
-                load(d, s + d + kDepth);
+            }
+            at += hop;
+            if (at - STEPS * group >= g.end) enter();
+        }
+        ++wr;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ uint32_t wait() {           // this lane's place in the chunk to compute
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+        return read_from + (rd++ & (kStages - 1)) * stage_bytes(STEPS);
+    }
+    static __device__ __forceinline__ void copy(uint32_t to, const void* from, int bytes) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    }
+};
+
+// The tokens' rows, a chunk at a time: loaded to registers two chunks ahead and stored to one
+// of two buffers one chunk ahead.  Buffer: [token][split * STEPS * 64 k], rows 64 bytes off a
+// multiple of 128, so that the 8 rows x 64 bytes of an MMA's operand B touch every bank once a
+// quarter-warp.  `from(pair)`: the offset of a pair's row in `base`.
+template <int STEPS, class Next, class From>
+struct Tokens {
+    static constexpr int kPieces = kRows * STEPS * 8 / kThreads;          // 16-byte pieces a thread
+    Segment g;
+    const Chosen& chosen;
+    const __nv_bfloat16* base;
+    int at = 0, K, hop, lines, pitch;        // hop: steps of a chunk; lines: log2 of its 16-byte pieces a token
+    bool live;
+    uint32_t buffers, put = 0;
+    uint4 piece[kPieces];
+    Next next;
+    From from;
+    __device__ __forceinline__ Tokens(Next n, From f, const Chosen& c, const __nv_bfloat16* b, uint32_t smem, int K_, int split)
+        : chosen(c), base(b), K(K_), buffers(smem), next(n), from(f) {
+        hop = STEPS * split;
+        lines = (STEPS == 2 ? 4 : 3) + (31 - __clz(split));
+        pitch = (16 << lines) + 64;
+        live = next(g);
+        at = live ? g.s : 0;
+        load();
+        store();
+        load();
+    }
+    __device__ __forceinline__ void load() {
+        if (!live) return;
+        const int first = chosen.first[g.entry], n = chosen.pairs[g.entry];
+        const int end = g.end * 64 < K ? g.end * 64 : K;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int i = threadIdx.x + j * kThreads, row = i >> lines, col = at * 64 + (i & ((1 << lines) - 1)) * 8;
+            piece[j] = make_uint4(0, 0, 0, 0);
+            if (row < n && col < end) piece[j] = *reinterpret_cast<const uint4*>(base + from(chosen.order[first + row]) + col);
+        }
+        at += hop;
+        if (at >= g.end) {
+            live = next(g);
+            at = live ? g.s : 0;
+        }
+    }
+    __device__ __forceinline__ void store() {
+        const uint32_t to = buffers + (put++ & 1) * token_bytes(STEPS);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            const int i = threadIdx.x + j * kThreads, row = i >> lines;
+            if (row < kMaxPass) store_smem(to + row * pitch + (i & ((1 << lines) - 1)) * 16, piece[j]);
+        }
+    }
+};
+
+// acc += this warp's part of a segment with up to NT * 8 tokens: acc[n] is rows g and g + 8 x
+// tokens n * 8 + 2 q, + 1.
+template <int STEPS, int NT, class W, class B>
+__device__ __forceinline__ void products(float (*acc)[4], W& weights, B& tokens, const Segment& g, int n, bool mine,
+                                         int group, int split) {
+    const int lane = threadIdx.x & 31;
+    uint32_t row[NT];                        // of token n * 8 + g in a buffer; past the last, the last's
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+        row[i] = tokens.buffers + min(i * 8 + (lane >> 2), n - 1) * tokens.pitch + group * STEPS * 128 + (lane & 3) * 16;
+    for (int c = g.s; c < g.end; c += STEPS * split) {
+        __syncthreads();                     // this chunk's tokens are stored, the last chunk's are read
+        const uint32_t buffer = (tokens.put & 1 ? 0 : 1) * token_bytes(STEPS);         // stored last
+        tokens.store();
+        tokens.load();
+        const uint32_t from = weights.wait();
+        if (mine) {
+#pragma unroll
+            for (int d = 0; d < STEPS; ++d) {
+                if (c + STEPS * group + d < g.end) {
+                    const uint32_t at = from + d * 128, rows8 = 8 * STEPS * 128;
+                    const uint4 w0 = load_smem(at), w1 = load_smem(at + rows8), w2 = load_smem(at ^ 64), w3 = load_smem((at + rows8) ^ 64);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const uint4 u = load_smem(row[i] + buffer + d * 128), v = load_smem(row[i] + buffer + d * 128 + 64);
+                        mma(acc[i], w0.x, w1.x, w0.y, w1.y, u.x, u.y);
+                        mma(acc[i], w0.z, w1.z, w0.w, w1.w, u.z, u.w);
+                        mma(acc[i], w2.x, w3.x, w2.y, w3.y, v.x, v.y);
+                        mma(acc[i], w2.z, w3.z, w2.w, w3.w, v.z, v.w);
+                    }
+                }
             }
         }
+        __syncwarp();                        // every lane has read the stage that is filled next
+        weights.issue();
     }
 }
 
-// products() over the number of 8-token tiles that n tokens take.
-__device__ __forceinline__ void products_of(int n, float (*acc)[4], const __nv_bfloat16* w0, const __nv_bfloat16* w1,
-                                            const __nv_bfloat16* b, const int* off, int s0, int s1, int K) {
-    if (n <= 8) products<1>(acc, w0, w1, b, off, s0, s1, K);
-    else if (n <= 16) products<2>(acc, w0, w1, b, off, s0, s1, K);
-    else if (n <= 32) products<4>(acc, w0, w1, b, off, s0, s1, K);
-    else products<8>(acc, w0, w1, b, off, s0, s1, K);
+// products() over the number of 8-token tiles that n <= kMaxPass tokens take.
+template <int STEPS, class W, class B>
+__device__ __forceinline__ void products_of(float (*acc)[4], W& weights, B& tokens, const Segment& g, int n, bool mine,
+                                            int group, int split) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    if (n <= 8) products<STEPS, 1>(acc, weights, tokens, g, n, mine, group, split);
+    else if (n <= 16) products<STEPS, 2>(acc, weights, tokens, g, n, mine, group, split);
+    else products<STEPS, 4>(acc, weights, tokens, g, n, mine, group, split);
 }
 
-// Unit = 8 hidden units of a chosen expert: MMA rows 0..7 are their left rows of W1, rows
-// 8..15 the gate rows of the same units, so a lane ends with left and gate of its unit.
-// A unit's k range is split over `split` warps of the CTA, whose sums meet in shared memory.
-__global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const Routed a) {
+// A segment is 8 * (kWarps / split) hidden units of an entry's expert over the whole of D: MMA
+// rows 0..7 of a warp are 8 units' left rows of W1, rows 8..15 the gate rows of the same
+// units, so a lane ends with left and gate of its unit.
+constexpr int kUpSteps = 2;
+constexpr int kUpSmem = ring_bytes(kUpSteps) + 2 * token_bytes(kUpSteps) + kWarps * 16 * 32 * 4;
+
+__global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     __shared__ Chosen chosen;
-    __shared__ short lists[kWarps][kMaxTokens];
-    __shared__ float part[kWarps][32][33];
-    read_choice(chosen, a);
+    extern __shared__ __align__(128) unsigned char smem[];
+    read_choice(chosen, a, kMaxPass, smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int groups = a.H / 8, units = chosen.count * groups, steps = (a.D + 63) / 64;
-    // the split whose last round wastes least: time of a launch in whole units
+    const int groups = a.H / 8, steps = (a.D + 63) / 64;
+    // the split whose last round of segments wastes least (time of the launch in whole segments
+    // of kWarps groups), among those whose chunk of tokens fits
     int split = 1;
     float best = INFINITY;
-    for (int s = 1; s <= kWarps; s *= 2) {
-        const int per = gridDim.x * (kWarps / s);
-        const float cost = (float)((units + per - 1) / per) / (float)s * (1.f + 0.01f * s);
+    for (int s = 1; s <= kWarps && s * chosen.most <= kRows; s *= 2) {
+        const int per = kWarps / s, all = chosen.count * ((groups + per - 1) / per);
+        const float cost = (float)((all + gridDim.x - 1) / gridDim.x) / (float)s * (1.f + 0.01f * s);
         if (cost < best) best = cost, split = s;
     }
-    const int sub = warp / split, piece = warp % split, subs = kWarps / split;
-    const int s0 = steps * piece / split, s1 = steps * (piece + 1) / split;
-    const int rounds = (units + gridDim.x * subs - 1) / (gridDim.x * subs);
-    int last = -1, n = 0;
-    int off[8];
-    for (int r = 0; r < rounds; ++r) {
-        const int u = (r * subs + sub) * gridDim.x + blockIdx.x;
-        const bool on = u < units;
-        float acc[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-        const int unit = on ? u % groups * 8 + g : 0;
-        if (on) {
-            const int e = chosen.expert[u / groups];
-            if (e != last) {
-                last = e;
-                n = list_pairs(lists[warp], chosen, a, e);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) off[i] = lists[warp][i * 8 + g] / a.k * a.D;
-            }
-            const __nv_bfloat16* w0 = a.W1 + ((int64_t)e * 2 * a.H + unit) * a.D;
-            products_of(n, acc, w0, w0 + (int64_t)a.H * a.D, a.x, off, s0, s1, a.D);
-        }
+    const int per = kWarps / split, tiles = (groups + per - 1) / per, all = chosen.count * tiles;
+    const int row = warp / split, group = warp % split;
+    int ahead_w = blockIdx.x, ahead_t = blockIdx.x;
+    auto segment = [&](int& ahead, Segment& f) {
+        if (ahead >= all) return false;
+        f = {ahead / tiles, ahead % tiles, 0, steps};
+        ahead += gridDim.x;
+        return true;
+    };
+    auto next_w = [&](Segment& f) { return segment(ahead_w, f); };
+    auto next_t = [&](Segment& f) { return segment(ahead_t, f); };
+    auto rows = [&](const Segment& f, const __nv_bfloat16*& w, int64_t& second) {
+        const int unit = (f.tile * per + row) * 8;
+        if (unit >= a.H) return false;       // H is a multiple of 8: a warp's units are all inside or all past it
+        w = a.W1 + ((int64_t)chosen.expert[f.entry] * 2 * a.H + unit) * a.D;
+        second = (int64_t)a.H * a.D;
+        return true;
+    };
+    auto from = [&](int pair) { return pair / a.k * a.D; };
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
+    float* part = reinterpret_cast<float*>(smem + ring_bytes(kUpSteps) + 2 * token_bytes(kUpSteps));       // [warp][value][lane]
+    Weights<kUpSteps, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.D, a.D, group, split);
+    Tokens<kUpSteps, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.x, ring + ring_bytes(kUpSteps), a.D, split);
+    for (int at = blockIdx.x; at < all; at += gridDim.x) {
+        const Segment f{at / tiles, at % tiles, 0, steps};
+        const int n = chosen.pairs[f.entry], unit = (f.tile * per + row) * 8 + g;
+        const bool mine = unit < a.H;
+        float acc[4][4];
+        products_of<kUpSteps>(acc, weights, tokens, f, n, mine, group, split);
         if (split > 1) {
-            if (piece > 0 && on) {
+            if (group > 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 4; ++i)
                     if (i * 8 < n)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) part[warp][i * 4 + j][lane] = acc[i][j];
+                        for (int j = 0; j < 4; ++j) part[(warp * 16 + i * 4 + j) * 32 + lane] = acc[i][j];
             }
-            __syncthreads();
-            if (piece == 0 && on) {
+            __syncthreads();                 // (the next segment's first chunk has one before part is written again)
+            if (group == 0) {
                 for (int p = 1; p < split; ++p)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 0; i < 4; ++i)
                         if (i * 8 < n)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[i][j] += part[warp + p][i * 4 + j][lane];
+                            for (int j = 0; j < 4; ++j) acc[i][j] += part[((warp + p) * 16 + i * 4 + j) * 32 + lane];
             }
-            __syncthreads();
         }
-        if (on && piece == 0) {
+        if (mine && group == 0) {
             // h is rounded to bf16 once, for the down product's MMA; left and gate stay fp32
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int col = i * 8 + 2 * q + j;
                     if (col < n) {
                         const float left = acc[i][j], gate = acc[i][2 + j];
-                        a.h[(int64_t)lists[warp][col] * a.H + unit] =
+                        a.h[(int64_t)chosen.order[chosen.first[f.entry] + col] * a.H + unit] =
                             __float2bfloat16_rn(left * (gate / (1.f + __expf(-gate))));
                     }
                 }
@@ -329,82 +476,96 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const Routed a) {
     }
 }
 
-// Cluster of CTAs = 16 output columns.  The steps of all chosen experts, one after the
-// other, are divided evenly over the cluster's warps; a warp adds each expert's sums,
-// times the gates, into its own fp32 tile [T][16], and the tiles are added in warp order.
-__global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const Routed a) {
+// A cluster has 16 * (kWarps / split) output columns; the steps of all entries, one after the
+// other, are divided evenly over its CTAs.  A warp adds each segment's sums, times the gates,
+// into its own fp32 tile [T][16], and the tiles are added in CTA and warp order.
+template <int STEPS>
+__global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, int split) {
     __shared__ Chosen chosen;
-    __shared__ short lists[kWarps][kMaxTokens];
-    extern __shared__ float sums[];                        // [kWarps][T][16]
+    extern __shared__ __align__(128) unsigned char smem[];
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
-    read_choice(chosen, a);
+    read_choice(chosen, a, min(kMaxPass, kRows / split), smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int row0 = blockIdx.x / ctas * 16, steps = (a.H + 63) / 64;
-    float* mine = sums + warp * a.T * 16;
-    for (int i = lane; i < a.T * 16; i += 32) mine[i] = 0.f;
-    const int64_t total = (int64_t)chosen.count * steps;
-    const int workers = ctas * kWarps, me = rank * kWarps + warp;
-    int64_t at = total * me / workers;
-    const int64_t end = total * (me + 1) / workers;
-    const int r1 = row0 + g + 8 < a.Dout ? row0 + g + 8 : row0 + g;     // Dout is a multiple of 8
-    while (at < end) {
-        const int e = chosen.expert[at / steps];
-        const int s0 = (int)(at % steps);
-        const int s1 = (int)(end - at < steps - s0 ? s0 + (end - at) : steps);
-        const int n = list_pairs(lists[warp], chosen, a, e);
-        int off[8];
+    const int steps = (a.H + 63) / 64, per = kWarps / split, row = warp / split, group = warp % split;
+    const int row0 = blockIdx.x / ctas * per * 16, out = row0 + row * 16 + g;
+    const int total = chosen.count * steps;
+    const int begin = (int)((int64_t)total * rank / ctas), end = (int)((int64_t)total * (rank + 1) / ctas);
+    int ahead_w = begin, ahead_t = begin;
+    auto segment = [&](int& ahead, Segment& f) {
+        if (ahead >= end) return false;
+        const int entry = ahead / steps, first = ahead - entry * steps;
+        f = {entry, 0, first, min(steps, first + end - ahead)};
+        ahead += f.end - first;
+        return true;
+    };
+    auto next_w = [&](Segment& f) { return segment(ahead_w, f); };
+    auto next_t = [&](Segment& f) { return segment(ahead_t, f); };
+    const bool mine = out - g < a.Dout;
+    auto rows = [&](const Segment& f, const __nv_bfloat16*& w, int64_t& second) {
+        w = a.W2 + ((int64_t)chosen.expert[f.entry] * a.Dout + out - g) * a.H;
+        second = out - g + 8 < a.Dout ? 8 * (int64_t)a.H : 0;          // Dout is a multiple of 8
+        return mine;
+    };
+    auto from = [&](int pair) { return pair * a.H; };
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
+    float* sums = reinterpret_cast<float*>(smem + ring_bytes(STEPS) + 2 * token_bytes(STEPS));      // [kWarps][T][16]
+    float* tile = sums + warp * a.T * 16;
+    Weights<STEPS, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.H, a.H, group, split);
+    Tokens<STEPS, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.h, ring + ring_bytes(STEPS), a.H, split);
+    for (int i = lane; i < a.T * 16; i += 32) tile[i] = 0.f;
+    __syncwarp();
+    int at = begin;
+    for (Segment f; segment(at, f);) {
+        const int n = chosen.pairs[f.entry], first = chosen.first[f.entry];
+        float acc[4][4];
+        products_of<STEPS>(acc, weights, tokens, f, n, mine, group, split);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) off[i] = lists[warp][i * 8 + g] * a.H;
-        float acc[8][4];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-        const __nv_bfloat16* w = a.W2 + (int64_t)e * a.Dout * a.H;
-        products_of(n, acc, w + (int64_t)(row0 + g) * a.H, w + (int64_t)r1 * a.H, a.h, off, s0, s1, a.H);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int col = i * 8 + 2 * q + j;
                 if (col < n) {
-                    const int p = lists[warp][col];
+                    const int p = chosen.order[first + col];
                     const float gate = a.gates[p];
-                    float* o = mine + p / a.k * 16 + g;
+                    float* o = tile + p / a.k * 16 + g;
                     o[0] += gate * acc[i][j];
                     o[8] += gate * acc[i][2 + j];
                 }
             }
         }
-        at += s1 - s0;
+        __syncwarp();
     }
     cluster.sync();
-    if (rank == 0) {
-        for (int i = threadIdx.x; i < a.T * 16; i += kThreads) {
-            const int t = i / 16, col = row0 + i % 16;
-            float v = 0.f;
-            for (int c = 0; c < ctas; ++c) {
-                const float* s = cluster.map_shared_rank(sums, c);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) v += s[w * a.T * 16 + i];
-            }
-            if (col < a.Dout) {
-                const int64_t o = (int64_t)t * a.Dout + col;
-                if (a.r) v += to_f32(a.r[o]);
-                a.y[o] = __float2bfloat16_rn(v);
-            }
+    const int width = per * 16, all = a.T * width;         // of the cluster; each CTA finishes its share
+    for (int i = rank * kThreads + threadIdx.x; i < all; i += ctas * kThreads) {
+        const int t = i / width, c = i % width, col = row0 + c;
+        float v = 0.f;
+        for (int r = 0; r < ctas; ++r) {
+            const float* s = cluster.map_shared_rank(sums, r) + c / 16 * split * a.T * 16 + t * 16 + c % 16;
+            for (int w = 0; w < split; ++w) v += s[w * a.T * 16];
+        }
+        if (col < a.Dout) {
+            const int64_t o = (int64_t)t * a.Dout + col;
+            if (a.r) v += to_f32(a.r[o]);
+            a.y[o] = __float2bfloat16_rn(v);
         }
     }
-    cluster.sync();                                        // the sums stay until rank 0 has read them
+    cluster.sync();                                        // the sums stay until every CTA has read them
 }
 
 // ---------------------------------------------------------------- host side
 
 bool width_ok(int64_t v) { return v > 0 && v % 8 == 0 && v < (int64_t(1) << 24); }
 
-cudaError_t launch_clusters(void (*kernel)(Routed), const Routed& a, int clusters, int size, size_t smem,
-                            cudaStream_t s) {
+// `clusters` clusters of `size` CTAs.
+template <class... Args>
+cudaError_t launch_clusters(void (*kernel)(Args...), int clusters, int size, int threads, size_t smem, cudaStream_t s,
+                            Args... args) {
+    cudaError_t e = smem <= 48 * 1024
+                        ? cudaSuccess
+                        : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -414,10 +575,75 @@ cudaError_t launch_clusters(void (*kernel)(Routed), const Routed& a, int cluster
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(clusters * size);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int down_smem(int steps, int64_t T) {
+    return ring_bytes(steps) + 2 * token_bytes(steps) + (int)(kWarps * T * 16 * sizeof(float));
+}
+
+// Clusters of each size 1 .. kMaxCluster that are resident at once with one CTA an SM, on the
+// current device (asked once: 152, 76, 46, 36, 28, 23, 15, 15 on the GB300, whose GPCs differ in
+// their SMs).  One cluster more than that would run alone in a second wave.
+constexpr int kMaxCluster = 8;
+struct Resident {
+    int clusters[kMaxCluster + 1];
+};
+cudaError_t resident_clusters(const Resident** out) {
+    constexpr int kMaxDevices = 64;
+    static std::mutex mutex;
+    static Resident table[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mutex);
+    Resident& r = table[dev];
+    if (r.clusters[1] == 0) {
+        const int smem = down_smem(2, 32);
+        e = cudaFuncSetAttribute(moe_down_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        for (int size = kMaxCluster; size >= 1; --size) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = size;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(size);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem;
+            e = cudaOccupancyMaxActiveClusters(&r.clusters[size], moe_down_kernel<2>, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    *out = &r;
+    return cudaSuccess;
+}
+
+// The down kernel's shape: the most CTAs that are resident at once, and among shapes within a
+// tenth of that the most output columns a CTA (its warps share the tokens' chunks), where an
+// expert's tokens, spread evenly with room for twice as many, fit a pass.
+struct DownPlan {
+    int split, tiles, cluster;
+};
+DownPlan down_plan(const Resident& r, int64_t T, int64_t E, int64_t Dout, int64_t k) {
+    const int64_t likely = std::min<int64_t>(std::min(T, (2 * T * k + E - 1) / E), kMaxPass);
+    DownPlan best{1, (int)((Dout + kWarps * 16 - 1) / (kWarps * 16)), 1};
+    for (int split = 1; split <= kWarps; split *= 2) {
+        if (split > 1 && kRows / split < likely) break;
+        const int width = kWarps / split * 16, tiles = (int)((Dout + width - 1) / width);
+        int cluster = 1;
+        for (int c = 2; c <= kMaxCluster; ++c)
+            if (tiles <= r.clusters[c]) cluster = c;
+        if (tiles * cluster * 10 > best.tiles * best.cluster * 11 && best.tiles * best.cluster < r.clusters[1]) best = {split, tiles, cluster};
+    }
+    return best;
 }
 
 }  // namespace
@@ -459,21 +685,22 @@ swiglu_status swiglu_moe_routed_fwd(const void* x, const void* Wr, const void* W
     // route: up to 8 CTAs of 8 warps share a token's experts
     const int route_ctas = E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8;
     rc = launch_traced(SWIGLU_KERNEL_MOE_ROUTE, s, [&] {
-        return launch_clusters(router_fp32 ? moe_route_kernel<float> : moe_route_kernel<__nv_bfloat16>, a, (int)T,
-                               route_ctas, 0, s);
+        return launch_clusters(router_fp32 ? moe_route_kernel<float> : moe_route_kernel<__nv_bfloat16>, (int)T, route_ctas,
+                               kRouteWarps * 32, 0, s, a);
     });
     if (rc != SWIGLU_OK) return rc;
     rc = launch_traced(SWIGLU_KERNEL_MOE_UP, s, [&] {
-        moe_up_kernel<<<kCtas, kThreads, 0, s>>>(a);
-        return cudaGetLastError();
+        return launch_clusters(moe_up_kernel, kPlanSms, 1, kThreads, kUpSmem, s, a);
     });
     if (rc != SWIGLU_OK) return rc;
-    // down: the largest cluster that leaves the CTAs resident at once
-    const int tiles = (int)((Dout + 15) / 16);
-    int size = 1;
-    while (size < 8 && tiles * size * 2 <= kCtas) size *= 2;
+    const Resident* resident;
+    cudaError_t e = resident_clusters(&resident);
+    if (e != cudaSuccess) return fail(SWIGLU_ERR_CUDA, "cudaOccupancyMaxActiveClusters", e);
+    const DownPlan p = down_plan(*resident, T, E, Dout, top_k);
     return launch_traced(SWIGLU_KERNEL_MOE_DOWN, s, [&] {
-        return launch_clusters(moe_down_kernel, a, tiles, size, (size_t)kWarps * T * 16 * sizeof(float), s);
+        // the longer runs where the tokens' sums leave room for them
+        return T <= 32 ? launch_clusters(moe_down_kernel<2>, p.tiles, p.cluster, kThreads, down_smem(2, T), s, a, p.split)
+                       : launch_clusters(moe_down_kernel<1>, p.tiles, p.cluster, kThreads, down_smem(1, T), s, a, p.split);
     });
 }
 
