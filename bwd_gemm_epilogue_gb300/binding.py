@@ -68,7 +68,7 @@ SIGNATURES = {
     "swiglu_moe_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _sz, _vp]),
     "swiglu_moe_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _sz,
                               _vp]),
-    "swiglu_moe_routed_fwd_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "swiglu_moe_routed_fwd_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
     "swiglu_moe_routed_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _i32,
                                      _i32, _vp, _sz, _vp]),
     "swiglu_mlp_layer_norm_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64,
@@ -82,7 +82,7 @@ SIGNATURES = {
 
 KERNEL_KINDS = {1: "fwd_preact", 2: "fwd_down", 3: "bwd_grad_h", 4: "bwd_dW2", 5: "bwd_dx", 6: "bwd_dW1", 7: "gemm",
                 8: "bwd_gemms", 9: "elementwise", 10: "norm_fwd", 11: "norm_bwd", 12: "norm_params", 13: "grad_norm",
-                14: "grad_scale", 15: "moe_route", 16: "moe_up", 17: "moe_down"}
+                14: "grad_scale", 15: "moe_route", 16: "moe_up", 17: "moe_down", 18: "moe_join"}
 
 
 class SwigluError(RuntimeError):
@@ -577,8 +577,8 @@ def swiglu_moe_bwd(x, W1, W2, preact, dy, counts, dx=None, dW1=None, dW2=None, w
     return dx, dW1, dW2
 
 
-def swiglu_moe_routed_fwd_workspace_size(T: int, H: int, top_k: int) -> int:
-    return int(lib().swiglu_moe_routed_fwd_workspace_size(T, H, top_k))
+def swiglu_moe_routed_fwd_workspace_size(T: int, H: int, Dout: int, top_k: int) -> int:
+    return int(lib().swiglu_moe_routed_fwd_workspace_size(T, H, Dout, top_k))
 
 
 def swiglu_moe_routed_fwd(x, Wr, W1, W2, top_k: int, renormalize: bool = True, residual=None, y=None, ids=None,
@@ -601,7 +601,7 @@ def swiglu_moe_routed_fwd(x, Wr, W1, W2, top_k: int, renormalize: bool = True, r
     if gates is None:
         gates = torch.empty((T, top_k), dtype=torch.float32, device=device)
     if workspace is None:
-        workspace = torch.empty(max(16, swiglu_moe_routed_fwd_workspace_size(T, H, top_k)), dtype=torch.uint8,
+        workspace = torch.empty(max(16, swiglu_moe_routed_fwd_workspace_size(T, H, Dout, top_k)), dtype=torch.uint8,
                                 device=device)
     st = lib().swiglu_moe_routed_fwd(
         _vector(x, "x", (T, D), bf, device), _vector(Wr, "Wr", (E, D), torch.float32 if fp32 else bf, device),

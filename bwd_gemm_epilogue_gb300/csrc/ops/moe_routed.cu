@@ -3,15 +3,17 @@
 // the weighted sum per token.
 //
 // With at most 64 tokens the work is to read the chosen experts' weights once; the tokens
-// that share an expert share that read.  Three launches, and nothing on the host depends
+// that share an expert share that read.  Four launches, each coming up while the one before
+// it ends, and nothing on the host depends
 // on the routing: the kernels read the chosen ids and divide what was chosen among
 // themselves.
 //
 //   route  one thread-block cluster per token: logits, softmax, top-k
 //   up     per chosen expert, 8 hidden units: left and gate rows of W1 against the
 //          expert's tokens, h = left * silu(gate) -> h [T * k, H] bf16 in the workspace
-//   down   16 output columns of every token: W2 rows of all chosen experts against h,
-//          weighted by the gates and added in registers and shared memory
+//   down   the steps of all chosen experts against every tile of output columns, divided
+//          evenly over the CTAs; a CTA weights its part of a tile by the gates
+//   join   adds the parts of every output, in a fixed order, and the residual
 //
 // Weights (A, 16 rows a warp) go to shared memory by asynchronous 16-byte copies and from
 // there into the registers of mma.m16n8k16.  A warp copies and reads its own stages only, so
@@ -23,7 +25,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <mutex>
+#include <type_traits>
 
 #include "../host.h"
 #include "convert.cuh"
@@ -39,6 +41,7 @@ constexpr int kMaxTokens = 64;
 constexpr int kMaxTop = 16;
 constexpr int kMaxExperts = 682;
 constexpr int kWarps = 16, kThreads = kWarps * 32;          // one CTA an SM
+constexpr int kSteps = 2;                    // steps of 64 k of a chunk
 constexpr int kStages = 2;                   // chunks of weights a warp has in flight or in use
 constexpr int kMaxPass = 32, kMinPass = 4;   // tokens of an expert taken at a time (64 / split, at most 32)
 constexpr int kEntries = kMaxExperts + kMaxTokens * kMaxTop / kMinPass;
@@ -57,7 +60,12 @@ struct Routed {
     int* ids;
     float* gates;
     int T, E, D, H, Dout, k, renorm, wr32;
+    float* parts;                            // [CTA + tile][T][width]: a CTA's part of a tile
+    long long* steps;                        // the span of a tile, then every CTA's first step: for the join kernel
+    int width, tiles, ctas;                  // output columns of a tile; tiles; CTAs of the down kernel
 };
+
+
 
 // ---------------------------------------------------------------- route
 
@@ -84,6 +92,7 @@ constexpr int kRouteWarps = 8;
 template <class W>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Routed a) {
     __shared__ float logits[kMaxExperts];
+    cudaTriggerProgrammaticLaunchCompletion();
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
     const int t = blockIdx.x / ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,6 +165,9 @@ __device__ __forceinline__ void read_choice(Chosen& c, const Routed& a, int pass
     short* start = reinterpret_cast<short*>(tokens + kMaxExperts);
     const int pairs = a.T * a.k;
     for (int e = threadIdx.x; e < a.E; e += kThreads) tokens[e] = 0;
+    // each launch may come up while the one before it runs, whose results it waits for here
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += kThreads) atomicOr(&tokens[a.ids[p]], 1ull << (p / a.k));
     __syncthreads();
@@ -286,11 +298,12 @@ struct Weights {
     }
 };
 
-// The tokens' rows, a chunk at a time: loaded to registers two chunks ahead and stored to one
-// of two buffers one chunk ahead.  Buffer: [token][split * STEPS * 64 k], rows 64 bytes off a
-// multiple of 128, so that the 8 rows x 64 bytes of an MMA's operand B touch every bank once a
-// quarter-warp.  `from(pair)`: the offset of a pair's row in `base`.
-template <int STEPS, class Next, class From>
+// The tokens' rows, a chunk at a time: loaded to registers and stored to one of BUFS buffers a
+// chunk ahead of that (BUFS 1: once the last chunk has been read, with a barrier more).  Buffer:
+// [token][split * STEPS * 64 k], rows 64 bytes off a multiple of 128, so that the 8 rows x 64
+// bytes of an MMA's operand B touch every bank once a quarter-warp.  `from(pair)`: the row of
+// `base` that a pair reads.
+template <int STEPS, int BUFS, class Next, class From>
 struct Tokens {
     static constexpr int kPieces = kRows * STEPS * 8 / kThreads;          // 16-byte pieces a thread
     Segment g;
@@ -310,8 +323,10 @@ struct Tokens {
         live = next(g);
         at = live ? g.s : 0;
         load();
-        store();
-        load();
+        if (BUFS == 2) {
+            store();
+            load();
+        }
     }
     __device__ __forceinline__ void load() {
         if (!live) return;
@@ -321,7 +336,7 @@ struct Tokens {
         for (int j = 0; j < kPieces; ++j) {
             const int i = threadIdx.x + j * kThreads, row = i >> lines, col = at * 64 + (i & ((1 << lines) - 1)) * 8;
             piece[j] = make_uint4(0, 0, 0, 0);
-            if (row < n && col < end) piece[j] = *reinterpret_cast<const uint4*>(base + from(chosen.order[first + row]) + col);
+            if (row < n && col < end) piece[j] = *reinterpret_cast<const uint4*>(base + from(chosen.order[first + row]) * K + col);
         }
         at += hop;
         if (at >= g.end) {
@@ -330,30 +345,63 @@ struct Tokens {
         }
     }
     __device__ __forceinline__ void store() {
-        const uint32_t to = buffers + (put++ & 1) * token_bytes(STEPS);
+        const uint32_t to = buffers + (put++ & (BUFS - 1)) * token_bytes(STEPS);
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
             const int i = threadIdx.x + j * kThreads, row = i >> lines;
             if (row < kMaxPass) store_smem(to + row * pitch + (i & ((1 << lines) - 1)) * 16, piece[j]);
         }
     }
+    __device__ __forceinline__ uint32_t row(const Segment&, int i) const { return buffers + i * pitch; }
+};
+
+// All rows that any pair reads, kept in the buffers' place for the whole launch where they fit:
+// warps then go through their segments without a barrier a chunk.
+__host__ __device__ constexpr int kept_pitch(int K) { return (K + 63) / 64 * 128 + 64; }
+__host__ __device__ constexpr bool kept_fits(int64_t rows, int64_t K) {
+    return rows * kept_pitch((int)K) <= 2 * token_bytes(kSteps);
+}
+
+template <class From>
+struct Kept {
+    const Chosen& chosen;
+    uint32_t rows;
+    int pitch;
+    From from;
+    __device__ __forceinline__ Kept(From f, const Chosen& c, const __nv_bfloat16* base, uint32_t smem, int n, int K)
+        : chosen(c), rows(smem), pitch(kept_pitch(K)), from(f) {
+        const int lines = (K + 63) / 64 * 8;               // 16-byte pieces of a row, the last ones zeros
+        for (int i = threadIdx.x; i < n * lines; i += kThreads) {
+            const int r = i / lines, c16 = i - r * lines;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (c16 * 8 < K) v = *reinterpret_cast<const uint4*>(base + (int64_t)r * K + c16 * 8);
+            store_smem(rows + r * pitch + c16 * 16, v);
+        }
+    }
+    __device__ __forceinline__ uint32_t row(const Segment& g, int i) const {
+        return rows + from(chosen.order[chosen.first[g.entry] + i]) * pitch;
+    }
 };
 
 // acc += this warp's part of a segment with up to NT * 8 tokens: acc[n] is rows g and g + 8 x
 // tokens n * 8 + 2 q, + 1.
-template <int STEPS, int NT, class W, class B>
+template <int STEPS, int BUFS, int NT, class W, class B>
 __device__ __forceinline__ void products(float (*acc)[4], W& weights, B& tokens, const Segment& g, int n, bool mine,
                                          int group, int split) {
     const int lane = threadIdx.x & 31;
     uint32_t row[NT];                        // of token n * 8 + g in a buffer; past the last, the last's
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-        row[i] = tokens.buffers + min(i * 8 + (lane >> 2), n - 1) * tokens.pitch + group * STEPS * 128 + (lane & 3) * 16;
+        row[i] = tokens.row(g, min(i * 8 + (lane >> 2), n - 1)) + group * STEPS * 128 + (lane & 3) * 16;
     for (int c = g.s; c < g.end; c += STEPS * split) {
-        __syncthreads();                     // this chunk's tokens are stored, the last chunk's are read
-        const uint32_t buffer = (tokens.put & 1 ? 0 : 1) * token_bytes(STEPS);         // stored last
-        tokens.store();
-        tokens.load();
+        uint32_t buffer = c * 128;           // kept rows: the chunk's place in them
+        if constexpr (BUFS > 0) {
+            __syncthreads();                 // the last chunk's tokens are read, and (BUFS 2) this chunk's stored
+            buffer = BUFS == 1 ? 0 : (tokens.put & 1 ? 0 : 1) * token_bytes(STEPS);        // stored last
+            tokens.store();
+            if (BUFS == 1) __syncthreads();
+            tokens.load();
+        }
         const uint32_t from = weights.wait();
         if (mine) {
 #pragma unroll
@@ -378,202 +426,274 @@ __device__ __forceinline__ void products(float (*acc)[4], W& weights, B& tokens,
 }
 
 // products() over the number of 8-token tiles that n <= kMaxPass tokens take.
-template <int STEPS, class W, class B>
+template <int STEPS, int BUFS, class W, class B>
 __device__ __forceinline__ void products_of(float (*acc)[4], W& weights, B& tokens, const Segment& g, int n, bool mine,
                                             int group, int split) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    if (n <= 8) products<STEPS, 1>(acc, weights, tokens, g, n, mine, group, split);
-    else if (n <= 16) products<STEPS, 2>(acc, weights, tokens, g, n, mine, group, split);
-    else products<STEPS, 4>(acc, weights, tokens, g, n, mine, group, split);
+    if (n <= 8) products<STEPS, BUFS, 1>(acc, weights, tokens, g, n, mine, group, split);
+    else if (n <= 16) products<STEPS, BUFS, 2>(acc, weights, tokens, g, n, mine, group, split);
+    else products<STEPS, BUFS, 4>(acc, weights, tokens, g, n, mine, group, split);
 }
 
-// A segment is 8 * (kWarps / split) hidden units of an entry's expert over the whole of D: MMA
-// rows 0..7 of a warp are 8 units' left rows of W1, rows 8..15 the gate rows of the same
-// units, so a lane ends with left and gate of its unit.
-constexpr int kUpSteps = 2;
-constexpr int kUpSmem = ring_bytes(kUpSteps) + 2 * token_bytes(kUpSteps) + kWarps * 16 * 32 * 4;
+// A segment is, for a warp, 8 hidden units (`tile`) of an entry's expert over the whole of D:
+// MMA rows 0..7 are their left rows of W1, rows 8..15 the gate rows of the same units, so a
+// lane ends with left and gate of its unit.  KEPT: the tokens stay in shared memory, and the
+// units of all entries are dealt to the warps one by one; otherwise a CTA's row groups take
+// neighbouring units of one entry, which share its chunks of tokens.
+constexpr int kUpSmem = ring_bytes(kSteps) + 2 * token_bytes(kSteps) + kWarps * 16 * 32 * 4;
 
+template <bool KEPT>
 __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     __shared__ Chosen chosen;
     extern __shared__ __align__(128) unsigned char smem[];
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
+    auto from = [&](int pair) { return pair / a.k; };
+    // x is older than the launch ahead of this one
+    Kept<decltype(from)> kept(from, chosen, a.x, ring + ring_bytes(kSteps), KEPT ? a.T : 0, a.D);
     read_choice(chosen, a, kMaxPass, smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int groups = a.H / 8, steps = (a.D + 63) / 64;
-    // the split whose last round of segments wastes least (time of the launch in whole segments
-    // of kWarps groups), among those whose chunk of tokens fits
+    const int groups = a.H / 8, units = chosen.count * groups, steps = (a.D + 63) / 64, ctas = gridDim.x;
     int split = 1;
-    float best = INFINITY;
-    for (int s = 1; s <= kWarps && s * chosen.most <= kRows; s *= 2) {
-        const int per = kWarps / s, all = chosen.count * ((groups + per - 1) / per);
-        const float cost = (float)((all + gridDim.x - 1) / gridDim.x) / (float)s * (1.f + 0.01f * s);
-        if (cost < best) best = cost, split = s;
+    if (KEPT) {
+        // The smallest split whose rounds, at about 6.8 KB/us that a warp's copies in flight
+        // bring, take no longer than the units at the HBM rate (in units of a unit's 32 D bytes)
+        float least = INFINITY;
+        for (int s = 1; s <= kWarps; s *= 2) {
+            const int per = ctas * (kWarps / s);
+            const float rounds = (float)((units + per - 1) / per) / (float)s;
+            if (rounds < 0.95f * least) least = rounds, split = s;
+            if (rounds <= 1.1e-3f * (float)units) break;
+        }
+    } else {
+        // the split whose last round of segments wastes least, among those whose chunk of tokens
+        // fits; every split costs an exchange of sums
+        float best = INFINITY;
+        for (int s = 1; s <= kWarps && s * chosen.most <= kRows; s *= 2) {
+            const int per = kWarps / s, all = chosen.count * ((groups + per - 1) / per);
+            const float cost = (float)((all + ctas - 1) / ctas) / (float)s * (1.f + 0.1f * s);
+            if (cost < best) best = cost, split = s;
+        }
     }
-    const int per = kWarps / split, tiles = (groups + per - 1) / per, all = chosen.count * tiles;
-    const int row = warp / split, group = warp % split;
-    int ahead_w = blockIdx.x, ahead_t = blockIdx.x;
-    auto segment = [&](int& ahead, Segment& f) {
-        if (ahead >= all) return false;
-        f = {ahead / tiles, ahead % tiles, 0, steps};
-        ahead += gridDim.x;
+    const int per = kWarps / split, tiles = (groups + per - 1) / per, row = warp / split, group = warp % split;
+    const int rounds = KEPT ? (units + ctas * per - 1) / (ctas * per)
+                            : (chosen.count * tiles - (int)blockIdx.x + ctas - 1) / ctas;
+    auto segment = [&](int j, Segment& f) {                // this warp's in round j
+        if (j >= rounds) return false;
+        if (KEPT) {
+            const int u = (j * per + row) * ctas + blockIdx.x;
+            f = {u / groups, u % groups, 0, steps};
+            return u < units;
+        }
+        const int t = j * ctas + blockIdx.x;
+        f = {t / tiles, t % tiles * per + row, 0, steps};
         return true;
     };
-    auto next_w = [&](Segment& f) { return segment(ahead_w, f); };
-    auto next_t = [&](Segment& f) { return segment(ahead_t, f); };
+    int ahead_w = 0, ahead_t = 0;
+    auto next_w = [&](Segment& f) { return segment(ahead_w++, f); };
+    auto next_t = [&](Segment& f) { return segment(ahead_t++, f); };
     auto rows = [&](const Segment& f, const __nv_bfloat16*& w, int64_t& second) {
-        const int unit = (f.tile * per + row) * 8;
-        if (unit >= a.H) return false;       // H is a multiple of 8: a warp's units are all inside or all past it
-        w = a.W1 + ((int64_t)chosen.expert[f.entry] * 2 * a.H + unit) * a.D;
+        if (f.tile >= groups) return false;
+        w = a.W1 + ((int64_t)chosen.expert[f.entry] * 2 * a.H + f.tile * 8) * a.D;
         second = (int64_t)a.H * a.D;
         return true;
     };
-    auto from = [&](int pair) { return pair / a.k * a.D; };
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
-    float* part = reinterpret_cast<float*>(smem + ring_bytes(kUpSteps) + 2 * token_bytes(kUpSteps));       // [warp][value][lane]
-    Weights<kUpSteps, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.D, a.D, group, split);
-    Tokens<kUpSteps, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.x, ring + ring_bytes(kUpSteps), a.D, split);
-    for (int at = blockIdx.x; at < all; at += gridDim.x) {
-        const Segment f{at / tiles, at % tiles, 0, steps};
-        const int n = chosen.pairs[f.entry], unit = (f.tile * per + row) * 8 + g;
-        const bool mine = unit < a.H;
-        float acc[4][4];
-        products_of<kUpSteps>(acc, weights, tokens, f, n, mine, group, split);
-        if (split > 1) {
-            if (group > 0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i * 8 < n)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) part[(warp * 16 + i * 4 + j) * 32 + lane] = acc[i][j];
-            }
-            __syncthreads();                 // (the next segment's first chunk has one before part is written again)
-            if (group == 0) {
-                for (int p = 1; p < split; ++p)
+    float* part = reinterpret_cast<float*>(smem + ring_bytes(kSteps) + 2 * token_bytes(kSteps));       // [warp][value][lane]
+    Weights<kSteps, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.D, a.D, group, split);
+    auto run = [&](auto& tokens, auto bufs) {
+        for (int j = 0; j < rounds; ++j) {
+            Segment f;
+            const bool mine = segment(j, f) && f.tile < groups;
+            if (KEPT && !mine && split == 1) break;
+            const int n = KEPT && !mine ? 0 : chosen.pairs[f.entry], unit = f.tile * 8 + g;
+            float acc[4][4];
+            if (!KEPT || mine) products_of<kSteps, decltype(bufs)::value>(acc, weights, tokens, f, n, mine, group, split);
+            if (split > 1) {
+                if (group > 0) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (i * 8 < n)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) acc[i][j] += part[((warp + p) * 16 + i * 4 + j) * 32 + lane];
+                            for (int v = 0; v < 4; ++v) part[(warp * 16 + i * 4 + v) * 32 + lane] = acc[i][v];
+                }
+                __syncthreads();             // (unless KEPT, the next segment's first chunk has one before part is written again)
+                if (group == 0) {
+                    for (int p = 1; p < split; ++p)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i * 8 < n)
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) acc[i][v] += part[((warp + p) * 16 + i * 4 + v) * 32 + lane];
+                }
+                if (KEPT) __syncthreads();
             }
-        }
-        if (mine && group == 0) {
-            // h is rounded to bf16 once, for the down product's MMA; left and gate stay fp32
+            if (mine && group == 0) {
+                // h is rounded to bf16 once, for the down product's MMA; left and gate stay fp32
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int col = i * 8 + 2 * q + j;
-                    if (col < n) {
-                        const float left = acc[i][j], gate = acc[i][2 + j];
-                        a.h[(int64_t)chosen.order[chosen.first[f.entry] + col] * a.H + unit] =
-                            __float2bfloat16_rn(left * (gate / (1.f + __expf(-gate))));
+                    for (int v = 0; v < 2; ++v) {
+                        const int col = i * 8 + 2 * q + v;
+                        if (col < n) {
+                            const float left = acc[i][v], gate = acc[i][2 + v];
+                            a.h[(int64_t)chosen.order[chosen.first[f.entry] + col] * a.H + unit] =
+                                __float2bfloat16_rn(left * (gate / (1.f + __expf(-gate))));
+                        }
                     }
                 }
             }
         }
+    };
+    if constexpr (KEPT) {
+        run(kept, std::integral_constant<int, 0>{});       // read_choice's barriers have published the rows
+    } else {
+        Tokens<kSteps, 2, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.x, ring + ring_bytes(kSteps), a.D, split);
+        run(tokens, std::integral_constant<int, 2>{});
     }
 }
 
-// A cluster has 16 * (kWarps / split) output columns; the steps of all entries, one after the
-// other, are divided evenly over its CTAs.  A warp adds each segment's sums, times the gates,
-// into its own fp32 tile [T][16], and the tiles are added in CTA and warp order.
-template <int STEPS>
+// A tile is `width` = 16 * (kWarps / split) output columns, and its span the steps of all
+// entries, one after the other; the spans of all tiles are divided evenly over the CTAs.  A
+// warp adds each segment's sums, times the gates, into its own fp32 tile [T][16]; at the end
+// of a tile (or of the CTA's steps) the warps' are added in order and stored as a part.
+// (Clusters whose CTAs shared a tile and added in distributed shared memory were tried: at
+// most 128 of the 152 SMs fit whole clusters, and 16 tokens took 154 us of @@.)
+// BUFS 0: the hidden rows are kept in shared memory.
+template <int BUFS>
 __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, int split) {
     __shared__ Chosen chosen;
     extern __shared__ __align__(128) unsigned char smem[];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
     read_choice(chosen, a, min(kMaxPass, kRows / split), smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int steps = (a.H + 63) / 64, per = kWarps / split, row = warp / split, group = warp % split;
-    const int row0 = blockIdx.x / ctas * per * 16, out = row0 + row * 16 + g;
-    const int total = chosen.count * steps;
-    const int begin = (int)((int64_t)total * rank / ctas), end = (int)((int64_t)total * (rank + 1) / ctas);
-    int ahead_w = begin, ahead_t = begin;
-    auto segment = [&](int& ahead, Segment& f) {
+    const int steps = (a.H + 63) / 64, row = warp / split, group = warp % split;
+    const long long span = (long long)chosen.count * steps;
+    const long long begin = a.tiles * span * blockIdx.x / a.ctas, end = a.tiles * span * (blockIdx.x + 1) / a.ctas;
+    if (threadIdx.x == 0) {
+        if (blockIdx.x == 0) a.steps[0] = span;
+        a.steps[1 + blockIdx.x] = begin;
+        if (blockIdx.x == a.ctas - 1) a.steps[2 + blockIdx.x] = end;
+    }
+    long long ahead_w = begin, ahead_t = begin;
+    auto segment = [&](long long& ahead, Segment& f) {
         if (ahead >= end) return false;
-        const int entry = ahead / steps, first = ahead - entry * steps;
-        f = {entry, 0, first, min(steps, first + end - ahead)};
+        const int tile = (int)(ahead / span), in = (int)(ahead - tile * span), entry = in / steps, first = in - entry * steps;
+        f = {entry, tile, first, (int)min((long long)steps, first + end - ahead)};
         ahead += f.end - first;
         return true;
     };
     auto next_w = [&](Segment& f) { return segment(ahead_w, f); };
     auto next_t = [&](Segment& f) { return segment(ahead_t, f); };
-    const bool mine = out - g < a.Dout;
     auto rows = [&](const Segment& f, const __nv_bfloat16*& w, int64_t& second) {
-        w = a.W2 + ((int64_t)chosen.expert[f.entry] * a.Dout + out - g) * a.H;
-        second = out - g + 8 < a.Dout ? 8 * (int64_t)a.H : 0;          // Dout is a multiple of 8
-        return mine;
+        const int out = f.tile * a.width + row * 16;
+        if (out >= a.Dout) return false;
+        w = a.W2 + ((int64_t)chosen.expert[f.entry] * a.Dout + out) * a.H;
+        second = out + 8 < a.Dout ? 8 * (int64_t)a.H : 0;              // Dout is a multiple of 8
+        return true;
     };
-    auto from = [&](int pair) { return pair * a.H; };
+    auto from = [&](int pair) { return pair; };
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
-    float* sums = reinterpret_cast<float*>(smem + ring_bytes(STEPS) + 2 * token_bytes(STEPS));      // [kWarps][T][16]
+    float* sums = reinterpret_cast<float*>(smem + ring_bytes(kSteps) + (BUFS == 1 ? 1 : 2) * token_bytes(kSteps));      // [kWarps][T][16]
     float* tile = sums + warp * a.T * 16;
-    Weights<STEPS, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.H, a.H, group, split);
-    Tokens<STEPS, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.h, ring + ring_bytes(STEPS), a.H, split);
+    Weights<kSteps, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.H, a.H, group, split);
     for (int i = lane; i < a.T * 16; i += 32) tile[i] = 0.f;
     __syncwarp();
-    int at = begin;
-    for (Segment f; segment(at, f);) {
-        const int n = chosen.pairs[f.entry], first = chosen.first[f.entry];
-        float acc[4][4];
-        products_of<STEPS>(acc, weights, tokens, f, n, mine, group, split);
+    auto finish = [&](int t) {               // tile t's part, and zeros for the next
+        __syncthreads();
+        float* part = a.parts + (int64_t)(blockIdx.x + t) * a.T * a.width;
+        for (int i = threadIdx.x; i < a.T * a.width; i += kThreads) {
+            const int c = i % a.width;
+            float* p = sums + c / 16 * split * a.T * 16 + i / a.width * 16 + c % 16;
+            float v = 0.f;
+            for (int w = 0; w < split; ++w) {
+                v += p[w * a.T * 16];
+                p[w * a.T * 16] = 0.f;
+            }
+            part[i] = v;
+        }
+        __syncthreads();
+    };
+    auto run = [&](auto& tokens) {
+        long long at = begin;
+        int open = -1;
+        for (Segment f; segment(at, f);) {
+            if (open >= 0 && f.tile != open) finish(open);
+            open = f.tile;
+            const int n = chosen.pairs[f.entry], first = chosen.first[f.entry];
+            const bool mine = f.tile * a.width + row * 16 < a.Dout;
+            float acc[4][4];
+            products_of<kSteps, BUFS>(acc, weights, tokens, f, n, mine, group, split);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int col = i * 8 + 2 * q + j;
-                if (col < n) {
-                    const int p = chosen.order[first + col];
-                    const float gate = a.gates[p];
-                    float* o = tile + p / a.k * 16 + g;
-                    o[0] += gate * acc[i][j];
-                    o[8] += gate * acc[i][2 + j];
+                for (int v = 0; v < 2; ++v) {
+                    const int col = i * 8 + 2 * q + v;
+                    if (col < n) {
+                        const int p = chosen.order[first + col];
+                        const float gate = a.gates[p];
+                        float* o = tile + p / a.k * 16 + g;
+                        o[0] += gate * acc[i][v];
+                        o[8] += gate * acc[i][2 + v];
+                    }
                 }
             }
+            __syncwarp();
         }
-        __syncwarp();
+        if (open >= 0) finish(open);
+    };
+    if constexpr (BUFS == 0) {
+        Kept<decltype(from)> kept(from, chosen, a.h, ring + ring_bytes(kSteps), a.T * a.k, a.H);
+        __syncthreads();
+        run(kept);
+    } else {
+        Tokens<kSteps, BUFS, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.h, ring + ring_bytes(kSteps), a.H, split);
+        run(tokens);
     }
-    cluster.sync();
-    const int width = per * 16, all = a.T * width;         // of the cluster; each CTA finishes its share
-    for (int i = rank * kThreads + threadIdx.x; i < all; i += ctas * kThreads) {
-        const int t = i / width, c = i % width, col = row0 + c;
-        float v = 0.f;
-        for (int r = 0; r < ctas; ++r) {
-            const float* s = cluster.map_shared_rank(sums, r) + c / 16 * split * a.T * 16 + t * 16 + c % 16;
-            for (int w = 0; w < split; ++w) v += s[w * a.T * 16];
-        }
-        if (col < a.Dout) {
-            const int64_t o = (int64_t)t * a.Dout + col;
-            if (a.r) v += to_f32(a.r[o]);
-            a.y[o] = __float2bfloat16_rn(v);
-        }
+}
+
+// y: the parts of a tile, from the CTAs whose steps meet its span, in order.
+__global__ void __launch_bounds__(256) moe_join_kernel(const Routed a) {
+    cudaGridDependencySynchronize();
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.T * a.Dout) return;
+    const int t = i / a.Dout, col = i - t * a.Dout, tile = col / a.width;
+    const long long lo = tile * a.steps[0], hi = lo + a.steps[0];
+    const float* part = a.parts + (int64_t)t * a.width + (col - tile * a.width);
+    const float v = a.r ? to_f32(a.r[i]) : 0.f;
+    float sum = 0.f;
+    int c = tile * a.ctas / a.tiles;         // the first CTA that has steps of the tile, or the one before it
+    long long end = a.steps[1 + c];
+    for (; c < a.ctas && end < hi; ++c) {
+        const long long begin = end;
+        end = a.steps[2 + c];
+        if (end > lo && end > begin) sum += part[(int64_t)(c + tile) * a.T * a.width];
     }
-    cluster.sync();                                        // the sums stay until every CTA has read them
+    a.y[i] = __float2bfloat16_rn(v + sum);
 }
 
 // ---------------------------------------------------------------- host side
 
 bool width_ok(int64_t v) { return v > 0 && v % 8 == 0 && v < (int64_t(1) << 24); }
 
-// `clusters` clusters of `size` CTAs.
+// `clusters` clusters of `size` CTAs; early: the launch may start before the one ahead of it ends.
 template <class... Args>
 cudaError_t launch_clusters(void (*kernel)(Args...), int clusters, int size, int threads, size_t smem, cudaStream_t s,
-                            Args... args) {
+                            bool early, Args... args) {
     cudaError_t e = smem <= 48 * 1024
                         ? cudaSuccess
                         : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 2 : 1;
     cfg.gridDim = dim3(clusters * size);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
@@ -581,69 +701,26 @@ cudaError_t launch_clusters(void (*kernel)(Args...), int clusters, int size, int
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-int down_smem(int steps, int64_t T) {
-    return ring_bytes(steps) + 2 * token_bytes(steps) + (int)(kWarps * T * 16 * sizeof(float));
+int down_smem(int bufs, int64_t T) {
+    return ring_bytes(kSteps) + bufs * token_bytes(kSteps) + (int)(kWarps * T * 16 * sizeof(float));
 }
 
-// Clusters of each size 1 .. kMaxCluster that are resident at once with one CTA an SM, on the
-// current device (asked once: 152, 76, 46, 36, 28, 23, 15, 15 on the GB300, whose GPCs differ in
-// their SMs).  One cluster more than that would run alone in a second wave.
-constexpr int kMaxCluster = 8;
-struct Resident {
-    int clusters[kMaxCluster + 1];
-};
-cudaError_t resident_clusters(const Resident** out) {
-    constexpr int kMaxDevices = 64;
-    static std::mutex mutex;
-    static Resident table[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lock(mutex);
-    Resident& r = table[dev];
-    if (r.clusters[1] == 0) {
-        const int smem = down_smem(2, 32);
-        e = cudaFuncSetAttribute(moe_down_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        for (int size = kMaxCluster; size >= 1; --size) {
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = size;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            cfg.gridDim = dim3(size);
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = smem;
-            e = cudaOccupancyMaxActiveClusters(&r.clusters[size], moe_down_kernel<2>, &cfg);
-            if (e != cudaSuccess) return e;
-        }
-    }
-    *out = &r;
-    return cudaSuccess;
+// Output columns of a tile: as many as leave 12 tiles (wide tiles share the tokens' chunks among
+// more warps; few tiles have many parts each to add).
+int down_width(int64_t Dout) {
+    int width = kWarps * 16;
+    while (width > 16 && (Dout + width - 1) / width < 12) width /= 2;
+    return width;
 }
+int down_tiles(int64_t Dout) { return (int)((Dout + down_width(Dout) - 1) / down_width(Dout)); }
+int down_ctas(int64_t Dout) { return std::min(kPlanSms, 16 * down_tiles(Dout)); }
 
-// The down kernel's shape: the most CTAs that are resident at once, and among shapes within a
-// tenth of that the most output columns a CTA (its warps share the tokens' chunks), where an
-// expert's tokens, spread evenly with room for twice as many, fit a pass.
-struct DownPlan {
-    int split, tiles, cluster;
-};
-DownPlan down_plan(const Resident& r, int64_t T, int64_t E, int64_t Dout, int64_t k) {
-    const int64_t likely = std::min<int64_t>(std::min(T, (2 * T * k + E - 1) / E), kMaxPass);
-    DownPlan best{1, (int)((Dout + kWarps * 16 - 1) / (kWarps * 16)), 1};
-    for (int split = 1; split <= kWarps; split *= 2) {
-        if (split > 1 && kRows / split < likely) break;
-        const int width = kWarps / split * 16, tiles = (int)((Dout + width - 1) / width);
-        int cluster = 1;
-        for (int c = 2; c <= kMaxCluster; ++c)
-            if (tiles <= r.clusters[c]) cluster = c;
-        if (tiles * cluster * 10 > best.tiles * best.cluster * 11 && best.tiles * best.cluster < r.clusters[1]) best = {split, tiles, cluster};
-    }
-    return best;
+size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
+constexpr size_t kStepsBytes = 1536;         // the join kernel's table: kPlanSms + 2 entries
+static_assert((kPlanSms + 2) * sizeof(long long) <= kStepsBytes, "the table fits");
+size_t h_bytes(int64_t T, int64_t H, int64_t k) { return round256((size_t)T * (size_t)k * (size_t)H * 2); }
+size_t part_bytes(int64_t T, int64_t Dout) {
+    return (size_t)(down_ctas(Dout) + down_tiles(Dout)) * (size_t)T * (size_t)down_width(Dout) * sizeof(float);
 }
 
 }  // namespace
@@ -653,9 +730,9 @@ using namespace swiglu;
 
 extern "C" {
 
-size_t swiglu_moe_routed_fwd_workspace_size(int64_t T, int64_t H, int64_t top_k) {
-    if (T <= 0 || H <= 0 || top_k <= 0) return 0;
-    return ((size_t)T * (size_t)top_k * (size_t)H * 2 + 255) & ~size_t(255);
+size_t swiglu_moe_routed_fwd_workspace_size(int64_t T, int64_t H, int64_t Dout, int64_t top_k) {
+    if (T <= 0 || H <= 0 || Dout <= 0 || top_k <= 0) return 0;
+    return h_bytes(T, H, top_k) + kStepsBytes + round256(part_bytes(T, Dout));
 }
 
 swiglu_status swiglu_moe_routed_fwd(const void* x, const void* Wr, const void* W1, const void* W2,
@@ -673,34 +750,41 @@ swiglu_status swiglu_moe_routed_fwd(const void* x, const void* Wr, const void* W
     if (!aligned16(x) || !aligned16(Wr) || !aligned16(W1) || !aligned16(W2) || !aligned16(residual) || !aligned16(y) ||
         !aligned16(workspace) || (reinterpret_cast<uintptr_t>(ids) & 3) || (reinterpret_cast<uintptr_t>(gates) & 3))
         return fail(SWIGLU_ERR_MISALIGNED, "routed layer: a pointer is not 16-byte aligned (ids, gates: 4)");
-    if (workspace_bytes < swiglu_moe_routed_fwd_workspace_size(T, H, top_k))
+    if (workspace_bytes < swiglu_moe_routed_fwd_workspace_size(T, H, Dout, top_k))
         return fail(SWIGLU_ERR_WORKSPACE_TOO_SMALL, "routed layer: workspace smaller than the size query returns");
     int sms;
     swiglu_status rc = device_sms(&sms);
     if (rc != SWIGLU_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     typedef const __nv_bfloat16* In;
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + h_bytes(T, H, top_k);
     const Routed a{(In)x, (In)W1, (In)W2, (In)residual, Wr, (__nv_bfloat16*)y, (__nv_bfloat16*)workspace, ids, gates,
-                   (int)T, (int)E, (int)D, (int)H, (int)Dout, (int)top_k, renormalize != 0, router_fp32 != 0};
+                   (int)T, (int)E, (int)D, (int)H, (int)Dout, (int)top_k, renormalize != 0, router_fp32 != 0,
+                   reinterpret_cast<float*>(ws + kStepsBytes), reinterpret_cast<long long*>(ws), down_width(Dout), down_tiles(Dout),
+                   down_ctas(Dout)};
     // route: up to 8 CTAs of 8 warps share a token's experts
     const int route_ctas = E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8;
     rc = launch_traced(SWIGLU_KERNEL_MOE_ROUTE, s, [&] {
         return launch_clusters(router_fp32 ? moe_route_kernel<float> : moe_route_kernel<__nv_bfloat16>, (int)T, route_ctas,
-                               kRouteWarps * 32, 0, s, a);
+                               kRouteWarps * 32, 0, s, false, a);
     });
     if (rc != SWIGLU_OK) return rc;
     rc = launch_traced(SWIGLU_KERNEL_MOE_UP, s, [&] {
-        return launch_clusters(moe_up_kernel, kPlanSms, 1, kThreads, kUpSmem, s, a);
+        return kept_fits(T, D) ? launch_clusters(moe_up_kernel<true>, kPlanSms, 1, kThreads, kUpSmem, s, true, a)
+                               : launch_clusters(moe_up_kernel<false>, kPlanSms, 1, kThreads, kUpSmem, s, true, a);
     });
     if (rc != SWIGLU_OK) return rc;
-    const Resident* resident;
-    cudaError_t e = resident_clusters(&resident);
-    if (e != cudaSuccess) return fail(SWIGLU_ERR_CUDA, "cudaOccupancyMaxActiveClusters", e);
-    const DownPlan p = down_plan(*resident, T, E, Dout, top_k);
-    return launch_traced(SWIGLU_KERNEL_MOE_DOWN, s, [&] {
-        // the longer runs where the tokens' sums leave room for them
-        return T <= 32 ? launch_clusters(moe_down_kernel<2>, p.tiles, p.cluster, kThreads, down_smem(2, T), s, a, p.split)
-                       : launch_clusters(moe_down_kernel<1>, p.tiles, p.cluster, kThreads, down_smem(1, T), s, a, p.split);
+    rc = launch_traced(SWIGLU_KERNEL_MOE_DOWN, s, [&] {
+        const int split = kWarps * 16 / a.width;
+        if (T <= 32 && kept_fits(T * top_k, H))
+            return launch_clusters(moe_down_kernel<0>, a.ctas, 1, kThreads, down_smem(2, T), s, true, a, split);
+        // two buffers of tokens where their sums leave room
+        return T <= 32 ? launch_clusters(moe_down_kernel<2>, a.ctas, 1, kThreads, down_smem(2, T), s, true, a, split)
+                       : launch_clusters(moe_down_kernel<1>, a.ctas, 1, kThreads, down_smem(1, T), s, true, a, split);
+    });
+    if (rc != SWIGLU_OK) return rc;
+    return launch_traced(SWIGLU_KERNEL_MOE_JOIN, s, [&] {
+        return launch_clusters(moe_join_kernel, (int)((T * Dout + 255) / 256), 1, 256, 0, s, true, a);
     });
 }
 

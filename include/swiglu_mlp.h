@@ -337,7 +337,8 @@ typedef enum {
     SWIGLU_KERNEL_GRAD_SCALE = 14,  /* global norm and clipped gradients */
     SWIGLU_KERNEL_MOE_ROUTE = 15,   /* routed MoE layer (swiglu_moe.h): router and choice of experts */
     SWIGLU_KERNEL_MOE_UP = 16,      /* routed MoE layer: x @ W1^T and SwiGLU of the chosen experts */
-    SWIGLU_KERNEL_MOE_DOWN = 17     /* routed MoE layer: h @ W2^T, weighted and added per token */
+    SWIGLU_KERNEL_MOE_DOWN = 17,    /* routed MoE layer: parts of h @ W2^T, weighted per token */
+    SWIGLU_KERNEL_MOE_JOIN = 18     /* routed MoE layer: the parts added */
 } swiglu_kernel_kind;
 
 /*

@@ -90,9 +90,10 @@ swiglu_status swiglu_moe_bwd(const void* x, const void* W1, const void* W2, cons
  * once however many tokens chose it.  Sums have a fixed order: the same call returns the
  * same bits on every run.
  *   Needs T in 0..64, E in 1..682, top_k in 1..min(E, 16), widths as above (below 2^24).
- *   workspace >= swiglu_moe_routed_fwd_workspace_size bytes (h [T * top_k, H] bf16).
+ *   workspace >= swiglu_moe_routed_fwd_workspace_size bytes (h [T * top_k, H] bf16 and
+ *   fp32 parts of y, which a last launch adds).
  */
-size_t swiglu_moe_routed_fwd_workspace_size(int64_t T, int64_t H, int64_t top_k);
+size_t swiglu_moe_routed_fwd_workspace_size(int64_t T, int64_t H, int64_t Dout, int64_t top_k);
 
 swiglu_status swiglu_moe_routed_fwd(const void* x, const void* Wr, const void* W1, const void* W2,
                                     const void* residual, void* y, int32_t* ids, float* gates, int64_t T, int64_t E,

@@ -167,7 +167,7 @@ def test_same_bits_every_run_on_another_stream_and_in_a_graph(b):
     for got, ref in zip(b.swiglu_moe_routed_fwd(*args, residual=t["r"]), want):
         assert torch.equal(got, ref)
     y, ids, gates = (torch.empty_like(v) for v in want)
-    ws = torch.empty(b.swiglu_moe_routed_fwd_workspace_size(30, 264, 4), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(b.swiglu_moe_routed_fwd_workspace_size(30, 264, 520, 4), dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
