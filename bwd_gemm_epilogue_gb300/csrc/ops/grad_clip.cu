@@ -3,8 +3,9 @@
 // Two launches: sums of squares (one fp64 sum per CTA), then the scaling, whose CTAs each
 // add those sums in the same order, so every one of them holds the same norm and no CTA
 // waits for another.  The tensors' table travels in the kernels' parameters (no copy, no
-// allocation, fit for stream capture); every tensor is cut into chunks of kChunkBytes and
-// CTA b takes chunks b, b + gridDim, ...
+// allocation, fit for stream capture).  All tensors, in granules of kGranule bytes, are
+// divided evenly over the CTAs; a CTA walks its share tensor by tensor with the next 32 KB in
+// flight, and the scaling walks it backwards, so that what the norm read last is still in L2.
 #include "../host.h"
 #include "convert.cuh"
 #include "swiglu_ops.h"
@@ -14,90 +15,109 @@ namespace {
 
 constexpr int kPlanSms = 152;
 constexpr int kThreads = 512;
-constexpr int kCtas = kPlanSms * 4;          // persistent CTAs = fp64 sums of one launch
+constexpr int kCtas = kPlanSms * 3;          // CTAs = fp64 sums of one launch; 3 an SM (4: 568 us, 2: 559, 3: 561 for 616.6 M bf16)
 constexpr int kMaxTensors = 768;             // per launch: 22 KB of parameters
 constexpr int kFewTensors = 64;              // a second, 2 KB table for the usual few (shorter launches)
-constexpr int64_t kChunkBytes = 32768;
+constexpr int64_t kGranule = 16384;
+constexpr int kBlock = 4;                    // 16-byte packs a thread loads at a time
 
 template <int N>
 struct ClipTable {
     const void* in[N];
     void* out[N];
     int64_t count[N];
-    uint32_t first[N + 1];                   // first chunk of each tensor; entry n: the number of chunks
+    uint32_t first[N + 1];                   // first granule of each tensor; entry n: their number
     uint8_t type[N];
     int n;
 };
 
-struct Chunk {
-    int t;
-    int64_t begin, end;                      // elements
-};
+__host__ __device__ constexpr int64_t granule_elements(int type) { return kGranule / (type == SWIGLU_FP32 ? 4 : 2); }
 
+// This CTA's share of the granules: [begin, end).
 template <int N>
-__device__ __forceinline__ Chunk find_chunk(const ClipTable<N>& c, uint32_t chunk) {
-    int lo = 0, hi = c.n;                    // first[lo] <= chunk < first[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (c.first[mid] <= chunk) lo = mid;
-        else hi = mid;
-    }
-    const int64_t per = kChunkBytes / (c.type[lo] == SWIGLU_FP32 ? 4 : 2);
-    Chunk k;
-    k.t = lo;
-    k.begin = (int64_t)(chunk - c.first[lo]) * per;
-    k.end = k.begin + per < c.count[lo] ? k.begin + per : c.count[lo];
-    return k;
+__device__ __forceinline__ uint2 share_of(const ClipTable<N>& c) {
+    const uint64_t all = c.first[c.n];
+    return make_uint2((uint32_t)(all * blockIdx.x / gridDim.x), (uint32_t)(all * (blockIdx.x + 1) / gridDim.x));
 }
 
-// Elements of [begin, end) before the first 16-byte boundary of p.
+// The tensor that has granule g.
+template <int N>
+__device__ __forceinline__ int tensor_of(const ClipTable<N>& c, uint32_t g) {
+    int lo = 0, hi = c.n;                    // first[lo] <= g < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (c.first[mid] <= g) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Of n elements at p, those before the first 16-byte boundary.
 template <class T>
 __device__ __forceinline__ int64_t head_of(const T* p, int64_t n) {
     const int64_t h = (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int64_t)sizeof(T);
     return h < n ? h : n;
 }
 
-// This thread's share of the sum of squares of n elements at p.
-template <class T, class Acc>
-__device__ __forceinline__ Acc squares(const T* p, int64_t n) {
-    constexpr int V = 16 / sizeof(T);
-    const int64_t head = head_of(p, n);
-    Acc s0 = 0, s1 = 0;
-    if (threadIdx.x < head) {
-        const Acc v = to_f32(p[threadIdx.x]);
-        s0 = v * v;
-    }
-    const T* q = p + head;
-    const int packs = (int)((n - head) / V);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < packs; i += kThreads) {
-        float v[V];
-        load_pack<T, V>(q + (int64_t)i * V).unpack(v);
+// Packs from + j * kThreads (j < kBlock) of q, zeros past `packs`.
+template <class T>
+__device__ __forceinline__ void load_block(uint4* b, const T* q, int from, int packs) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            const Acc a = v[j], b = v[j + 1];
-            s0 += a * a;
-            s1 += b * b;
-        }
+    for (int j = 0; j < kBlock; ++j) {
+        const int i = from + j * kThreads;
+        b[j] = i < packs ? reinterpret_cast<const uint4*>(q)[i] : make_uint4(0, 0, 0, 0);
     }
-    const int64_t tail = head + (int64_t)packs * V;
-    if (tail + threadIdx.x < n) {
-        const Acc v = to_f32(p[tail + threadIdx.x]);
-        s1 += v * v;
+}
+
+// Sum of a block's squares, 16 to each of two sums.
+template <class T, class Acc>
+__device__ __forceinline__ Acc block_squares(const uint4* b) {
+    constexpr int V = 16 / sizeof(T);
+    Acc s0 = 0, s1 = 0;
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+        F2 v[V / 2];
+        unpack16<T>(b[j], v);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 f = split(v[i]);
+            s0 += (Acc)f.x * (Acc)f.x;
+            s1 += (Acc)f.y * (Acc)f.y;
+        }
     }
     return s0 + s1;
 }
 
-template <class T>
-__device__ __noinline__ double squares_again(const T* p, int64_t n) {
-    return squares<T, double>(p, n);
-}
-
 // In fp32, and once more in fp64 where that overflowed (finite elements above 1.8e19 do).
 template <class T>
-__device__ __forceinline__ double chunk_squares(const T* p, int64_t n) {
-    const float s = squares<T, float>(p, n);
-    return isinf(s) ? squares_again(p, n) : (double)s;
+__device__ __noinline__ double block_squares_f64(const T* q, int from, int packs) {
+    uint4 b[kBlock];
+    load_block(b, q, from, packs);
+    return block_squares<T, double>(b);
+}
+template <class T>
+__device__ __forceinline__ double squares(const T* p, int64_t n) {
+    constexpr int V = 16 / sizeof(T);
+    double s = 0.0;
+    const int64_t head = head_of(p, n);
+    const int packs = (int)((n - head) / V);
+    const int64_t tail = head + (int64_t)packs * V;
+    if (threadIdx.x < head) {
+        const double v = to_f32(p[threadIdx.x]);
+        s = v * v;
+    }
+    if (tail + threadIdx.x < n) {
+        const double v = to_f32(p[tail + threadIdx.x]);
+        s += v * v;
+    }
+    const T* q = p + head;
+    for (int i = threadIdx.x; i < packs; i += kBlock * kThreads) {
+        uint4 b[kBlock];
+        load_block(b, q, i, packs);
+        const float f = block_squares<T, float>(b);
+        s += isinf(f) ? block_squares_f64(q, i, packs) : (double)f;
+    }
+    return s;
 }
 
 // Sum over the CTA's threads, in a fixed order; valid in thread 0.
@@ -116,47 +136,66 @@ __device__ __forceinline__ double cta_sum(double v) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) grad_squares_kernel(const __grid_constant__ ClipTable<N> c, double* sums) {
+__global__ void __launch_bounds__(kThreads, kCtas / kPlanSms) grad_squares_kernel(const __grid_constant__ ClipTable<N> c, double* sums) {
+    cudaTriggerProgrammaticLaunchCompletion();             // the scaling may come up meanwhile
     double s = 0.0;
-    for (uint32_t k = blockIdx.x; k < c.first[c.n]; k += gridDim.x) {
-        const Chunk u = find_chunk(c, k);
-        const int type = c.type[u.t];
-        const int64_t n = u.end - u.begin;
-        if (type == SWIGLU_FP32) s += chunk_squares(static_cast<const float*>(c.in[u.t]) + u.begin, n);
-        else if (type == SWIGLU_FP16) s += chunk_squares(static_cast<const __half*>(c.in[u.t]) + u.begin, n);
-        else s += chunk_squares(static_cast<const __nv_bfloat16*>(c.in[u.t]) + u.begin, n);
+    const uint2 share = share_of(c);
+    if (share.x < share.y) {
+        int t = tensor_of(c, share.x);
+        for (uint32_t g = share.x; g < share.y; ++t) {
+            const uint32_t end = min(share.y, c.first[t + 1]);
+            const int type = c.type[t];
+            const int64_t per = granule_elements(type), from = (int64_t)(g - c.first[t]) * per;
+            const int64_t n = min((int64_t)(end - c.first[t]) * per, c.count[t]) - from;
+            if (end > g) {
+                if (type == SWIGLU_FP32) s += squares(static_cast<const float*>(c.in[t]) + from, n);
+                else if (type == SWIGLU_FP16) s += squares(static_cast<const __half*>(c.in[t]) + from, n);
+                else s += squares(static_cast<const __nv_bfloat16*>(c.in[t]) + from, n);
+            }
+            g = end;
+        }
     }
     s = cta_sum(s);
     if (threadIdx.x == 0) sums[blockIdx.x] = s;
 }
 
 template <class T>
-__device__ __forceinline__ void scale_chunk(const T* p, T* o, int64_t n, float f) {
+__device__ __forceinline__ void scale(const T* p, T* o, int64_t n, float f) {
     constexpr int V = 16 / sizeof(T);
     if ((reinterpret_cast<uintptr_t>(p) & 15) != (reinterpret_cast<uintptr_t>(o) & 15)) {
         for (int64_t i = threadIdx.x; i < n; i += kThreads) o[i] = from_f32<T>(to_f32(p[i]) * f);
         return;
     }
     const int64_t head = head_of(p, n);
-    if (threadIdx.x < head) o[threadIdx.x] = from_f32<T>(to_f32(p[threadIdx.x]) * f);
     const int packs = (int)((n - head) / V);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < packs; i += kThreads) {
-        float v[V];
-        load_pack<T, V>(p + head + (int64_t)i * V).unpack(v);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] *= f;
-        store_pack<T, V>(o + head + (int64_t)i * V, v);
-    }
     const int64_t tail = head + (int64_t)packs * V;
+    if (threadIdx.x < head) o[threadIdx.x] = from_f32<T>(to_f32(p[threadIdx.x]) * f);
     if (tail + threadIdx.x < n) o[tail + threadIdx.x] = from_f32<T>(to_f32(p[tail + threadIdx.x]) * f);
+    const T* q = p + head;
+    uint4* to = reinterpret_cast<uint4*>(o + head);
+    constexpr int step = kBlock * kThreads;
+    const F2 f2x = f2(f);
+    for (int i = (packs + step - 1) / step * step - step; i >= 0; i -= step) {         // the last block first
+        uint4 b[kBlock];
+        load_block(b, q, i + threadIdx.x, packs);
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) {
+            const int k = i + threadIdx.x + j * kThreads;
+            F2 v[V / 2];
+            unpack16<T>(b[j], v);
+#pragma unroll
+            for (int x = 0; x < V / 2; ++x) v[x] = v[x] * f2x;
+            if (k < packs) __stcs(to + k, pack16<T>(v));
+        }
+    }
 }
 
 // The norm from all launches' sums (every CTA, in the same order), then this launch's tensors.
 template <int N>
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ ClipTable<N> c, const double* sums,
+__global__ void __launch_bounds__(kThreads, kCtas / kPlanSms) grad_scale_kernel(const __grid_constant__ ClipTable<N> c, const double* sums,
                                                               int num_sums, float max_norm, float eps, float* norm) {
     __shared__ float factor;
+    cudaGridDependencySynchronize();         // the sums
     double s = 0.0;
     for (int i = threadIdx.x; i < num_sums; i += kThreads) s += sums[i];
     s = cta_sum(s);
@@ -168,18 +207,20 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
     }
     __syncthreads();
     const float f = factor;
-    const uint32_t chunks = c.first[c.n];
-    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
-        const Chunk u = find_chunk(c, k);
-        const int type = c.type[u.t];
-        const int64_t n = u.end - u.begin;
-        if (type == SWIGLU_FP32)
-            scale_chunk(static_cast<const float*>(c.in[u.t]) + u.begin, static_cast<float*>(c.out[u.t]) + u.begin, n, f);
-        else if (type == SWIGLU_FP16)
-            scale_chunk(static_cast<const __half*>(c.in[u.t]) + u.begin, static_cast<__half*>(c.out[u.t]) + u.begin, n, f);
-        else
-            scale_chunk(static_cast<const __nv_bfloat16*>(c.in[u.t]) + u.begin,
-                        static_cast<__nv_bfloat16*>(c.out[u.t]) + u.begin, n, f);
+    const uint2 share = share_of(c);
+    if (share.x >= share.y) return;
+    int t = tensor_of(c, share.y - 1);
+    for (uint32_t end = share.y; end > share.x; --t) {
+        const uint32_t g = max(share.x, c.first[t]);
+        const int type = c.type[t];
+        const int64_t per = granule_elements(type), from = (int64_t)(g - c.first[t]) * per;
+        const int64_t n = min((int64_t)(end - c.first[t]) * per, c.count[t]) - from;
+        if (end > g && (f != 1.f || c.in[t] != c.out[t])) {        // times 1 in place changes nothing
+            if (type == SWIGLU_FP32) scale(static_cast<const float*>(c.in[t]) + from, static_cast<float*>(c.out[t]) + from, n, f);
+            else if (type == SWIGLU_FP16) scale(static_cast<const __half*>(c.in[t]) + from, static_cast<__half*>(c.out[t]) + from, n, f);
+            else scale(static_cast<const __nv_bfloat16*>(c.in[t]) + from, static_cast<__nv_bfloat16*>(c.out[t]) + from, n, f);
+        }
+        end = g;
     }
 }
 
@@ -197,36 +238,36 @@ struct ClipCall {
     cudaStream_t stream;
 };
 
-// Table of tensors base .. base + N - 1; returns its number of chunks.
+// Table of tensors base .. base + N - 1; returns its number of granules.
 template <int N>
 uint64_t fill_table(ClipTable<N>& c, const ClipCall& a, int64_t base) {
     c.n = (int)(a.n - base < N ? a.n - base : N);
-    uint64_t chunks = 0;
+    uint64_t granules = 0;
     for (int i = 0; i < c.n; ++i) {
         c.in[i] = a.in[base + i];
         c.out[i] = a.out ? a.out[base + i] : nullptr;
         c.count[i] = a.counts[base + i];
         c.type[i] = (uint8_t)a.types[base + i];
-        c.first[i] = (uint32_t)chunks;
-        const int64_t per = kChunkBytes / (c.type[i] == SWIGLU_FP32 ? 4 : 2);
-        chunks += (uint64_t)((c.count[i] + per - 1) / per);
+        c.first[i] = (uint32_t)granules;
+        const int64_t per = granule_elements(c.type[i]);
+        granules += (uint64_t)((c.count[i] + per - 1) / per);
     }
-    c.first[c.n] = (uint32_t)chunks;
-    return chunks;
+    c.first[c.n] = (uint32_t)granules;
+    return granules;
 }
 
-int grid_of(uint64_t chunks) { return (int)(chunks < (uint64_t)kCtas ? (chunks ? chunks : 1) : kCtas); }
+int grid_of(uint64_t granules) { return (int)(granules < (uint64_t)kCtas ? (granules ? granules : 1) : kCtas); }
 
 template <int N>
 swiglu_status run_clip(const ClipCall& a) {
     static thread_local ClipTable<N> c;
     const int64_t launches = a.n <= N ? 1 : (a.n + N - 1) / N;
-    uint64_t chunks = 0;
+    uint64_t granules = 0;
     int num_sums = 0;
     for (int64_t l = 0; l < launches; ++l) {
-        chunks = fill_table(c, a, l * N);
-        if (chunks > 0xffffffffull - kCtas) return fail(SWIGLU_ERR_UNSUPPORTED_SHAPE, "clip_grads: the tensors are too large");
-        const int grid = grid_of(chunks);
+        granules = fill_table(c, a, l * N);
+        if (granules > 0xffffffffull) return fail(SWIGLU_ERR_UNSUPPORTED_SHAPE, "clip_grads: the tensors are too large");
+        const int grid = grid_of(granules);
         const swiglu_status rc = launch_traced(SWIGLU_KERNEL_GRAD_NORM, a.stream, [&] {
             grad_squares_kernel<N><<<grid, kThreads, 0, a.stream>>>(c, a.sums + num_sums);
             return cudaGetLastError();
@@ -238,14 +279,23 @@ swiglu_status run_clip(const ClipCall& a) {
         if (!a.out) {                        // only the norm: one CTA, no tensors
             c.n = 0;
             c.first[0] = 0;
-            chunks = 0;
+            granules = 0;
         } else if (launches > 1) {
-            chunks = fill_table(c, a, l * N);
+            granules = fill_table(c, a, l * N);
         }
         const swiglu_status rc = launch_traced(SWIGLU_KERNEL_GRAD_SCALE, a.stream, [&] {
-            grad_scale_kernel<N><<<grid_of(chunks), kThreads, 0, a.stream>>>(c, a.sums, num_sums, a.max_norm, a.eps,
-                                                                            l == 0 ? a.norm : nullptr);
-            return cudaGetLastError();
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(grid_of(granules));
+            cfg.blockDim = dim3(kThreads);
+            cfg.stream = a.stream;
+            const double* sums = a.sums;
+            float* norm = l == 0 ? a.norm : nullptr;
+            return cudaLaunchKernelEx(&cfg, grad_scale_kernel<N>, c, sums, num_sums, a.max_norm, a.eps, norm);
         });
         if (rc != SWIGLU_OK) return rc;
     }

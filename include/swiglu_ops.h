@@ -75,9 +75,9 @@ size_t swiglu_mlp_clip_grads_workspace_size(int64_t n);
  *                            place); out NULL computes the norm alone.  The arrays are
  *                            read before the call returns.
  *   norm                     device fp32, may be NULL when out is given
- * Squares are fp32 products summed in fp32 over at most 32 KiB of a tensor, then in fp64
- * (a chunk whose fp32 squares overflow is summed again in fp64); squares below fp32's
- * range (elements under 1e-23) add nothing.  The sums' order depends on the counts and
+ * Squares are fp32 products summed in fp32 16 at a time, then in fp64 (where fp32 squares
+ * overflow they are summed again in fp64); squares below fp32's range (elements under
+ * 1e-23) add nothing.  The sums' order depends on the counts and
  * types only: the same call returns the same bits on every run.  A norm that is infinite
  * or NaN gives what the formulas give (factor 0, so finite elements become 0 and infinite
  * ones NaN; or NaN everywhere): read `norm` before using the result.  n = 0: norm 0.
