@@ -229,7 +229,7 @@ __device__ __forceinline__ void store_smem(uint32_t at, const uint4& v) {
 // the steps [s, end) of 64 k.  Its kWarps warps are kWarps / split row groups x split k groups; a
 // chunk is STEPS steps of each k group, that is split * STEPS * 64 consecutive k.
 struct Segment {
-    int entry, tile, s, end;
+    int entry, tile, s, end;                 // tile: the warp's 8 hidden units (up), the output tile (down)
 };
 
 // The weights of one warp, kStages chunks in flight.  A copy instruction takes runs of STEPS *
@@ -457,45 +457,45 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int groups = a.H / 8, units = chosen.count * groups, steps = (a.D + 63) / 64, ctas = gridDim.x;
     int split = 1;
-    if (KEPT) {
-        // The smallest split whose rounds, at about 6.8 KB/us that a warp's copies in flight
-        // bring, take no longer than the units at the HBM rate (in units of a unit's 32 D bytes)
-        float least = INFINITY;
-        for (int s = 1; s <= kWarps; s *= 2) {
-            const int per = ctas * (kWarps / s);
-            const float rounds = (float)((units + per - 1) / per) / (float)s;
+    float least = INFINITY;
+    for (int s = 1; s <= kWarps && (KEPT || s * chosen.most <= kRows); s *= 2) {
+        const int per = kWarps / s;
+        if (KEPT) {
+            // The smallest split whose rounds, at about 6.8 KB/us that a warp's copies in flight
+            // bring, take no longer than the units at the HBM rate (in units of a unit's 32 D bytes)
+            const float rounds = (float)((units + ctas * per - 1) / (ctas * per)) / (float)s;
             if (rounds < 0.95f * least) least = rounds, split = s;
             if (rounds <= 1.1e-3f * (float)units) break;
-        }
-    } else {
-        // the split whose last round of segments wastes least, among those whose chunk of tokens
-        // fits; every split costs an exchange of sums
-        float best = INFINITY;
-        for (int s = 1; s <= kWarps && s * chosen.most <= kRows; s *= 2) {
-            const int per = kWarps / s, all = chosen.count * ((groups + per - 1) / per);
-            const float cost = (float)((all + ctas - 1) / ctas) / (float)s * (1.f + 0.1f * s);
-            if (cost < best) best = cost, split = s;
+        } else {
+            // the split whose last round of a CTA's units wastes least (a segment's end costs
+            // about a chunk), among those whose chunk of tokens fits
+            const float mine = (float)units / (float)ctas;
+            const float cost = ceilf(mine / (float)per) / (float)s * (1.f + 2.f * (float)s / (float)steps);
+            if (cost < least) least = cost, split = s;
         }
     }
-    const int per = kWarps / split, tiles = (groups + per - 1) / per, row = warp / split, group = warp % split;
-    const int rounds = KEPT ? (units + ctas * per - 1) / (ctas * per)
-                            : (chosen.count * tiles - (int)blockIdx.x + ctas - 1) / ctas;
-    auto segment = [&](int j, Segment& f) {                // this warp's in round j
-        if (j >= rounds) return false;
+    const int per = kWarps / split, row = warp / split, group = warp % split;
+    // KEPT: round j of a warp is unit (j * per + row) * ctas + CTA.  Otherwise a CTA has an even,
+    // consecutive share of the units and takes up to `per` of one entry at a time.
+    const int begin = KEPT ? 0 : (int)((int64_t)units * blockIdx.x / ctas);
+    const int end = KEPT ? (units + ctas * per - 1) / (ctas * per) : (int)((int64_t)units * (blockIdx.x + 1) / ctas);
+    auto segment = [&](int& at, Segment& f) {
+        if (at >= end) return false;
         if (KEPT) {
-            const int u = (j * per + row) * ctas + blockIdx.x;
-            f = {u / groups, u % groups, 0, steps};
-            return u < units;
+            const int u = (at++ * per + row) * ctas + blockIdx.x;
+            f = {u / groups, u < units ? u % groups : groups, 0, steps};
+            return true;
         }
-        const int t = j * ctas + blockIdx.x;
-        f = {t / tiles, t % tiles * per + row, 0, steps};
+        const int entry = at / groups, first = at - entry * groups, n = min(per, min(groups - first, end - at));
+        f = {entry, row < n ? first + row : groups, 0, steps};
+        at += n;
         return true;
     };
-    int ahead_w = 0, ahead_t = 0;
-    auto next_w = [&](Segment& f) { return segment(ahead_w++, f); };
-    auto next_t = [&](Segment& f) { return segment(ahead_t++, f); };
+    int ahead_w = begin, ahead_t = begin;
+    auto next_w = [&](Segment& f) { return segment(ahead_w, f); };
+    auto next_t = [&](Segment& f) { return segment(ahead_t, f); };
     auto rows = [&](const Segment& f, const __nv_bfloat16*& w, int64_t& second) {
-        if (f.tile >= groups) return false;
+        if (f.tile >= groups) return false;  // this warp has no unit in the segment
         w = a.W1 + ((int64_t)chosen.expert[f.entry] * 2 * a.H + f.tile * 8) * a.D;
         second = (int64_t)a.H * a.D;
         return true;
@@ -503,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     float* part = reinterpret_cast<float*>(smem + ring_bytes(kSteps) + 2 * token_bytes(kSteps));       // [warp][value][lane]
     Weights<kSteps, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.D, a.D, group, split);
     auto run = [&](auto& tokens, auto bufs) {
-        for (int j = 0; j < rounds; ++j) {
-            Segment f;
-            const bool mine = segment(j, f) && f.tile < groups;
+        int at = begin;
+        for (Segment f; segment(at, f);) {
+            const bool mine = f.tile < groups;
             if (KEPT && !mine && split == 1) break;
             const int n = KEPT && !mine ? 0 : chosen.pairs[f.entry], unit = f.tile * 8 + g;
             float acc[4][4];
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
 // warp adds each segment's sums, times the gates, into its own fp32 tile [T][16]; at the end
 // of a tile (or of the CTA's steps) the warps' are added in order and stored as a part.
 // (Clusters whose CTAs shared a tile and added in distributed shared memory were tried: at
-// most 128 of the 152 SMs fit whole clusters, and 16 tokens took 154 us of @@.)
+// most 128 of the 152 SMs fit whole clusters, and 61 ragged tokens took 86 us instead of 70.)
 // BUFS 0: the hidden rows are kept in shared memory.
 template <int BUFS>
 __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, int split) {
