@@ -42,15 +42,15 @@ constexpr int kMaxTop = 16;
 constexpr int kMaxExperts = 682;
 constexpr int kWarps = 16, kThreads = kWarps * 32;          // one CTA an SM
 constexpr int kSteps = 2;                    // steps of 64 k of a chunk
-constexpr int kStages = 2;                   // chunks of weights a warp has in flight or in use
+constexpr int kStages = 4;                   // steps of weights a warp has in flight or in use
+constexpr int kStageBytes = 16 * 128;        // 16 rows x 64 k
 constexpr int kMaxPass = 32, kMinPass = 4;   // tokens of an expert taken at a time (64 / split, at most 32)
 constexpr int kEntries = kMaxExperts + kMaxTokens * kMaxTop / kMinPass;
 constexpr int kRows = 64;                    // tokens x split of a chunk of B
 
 // A chunk is STEPS * 64 k for each k group of the CTA's warps: 16 rows of weights a warp, kRows
 // rows of tokens (with 64 bytes between the rows of a token).
-__host__ __device__ constexpr int stage_bytes(int steps) { return 16 * steps * 128; }
-__host__ __device__ constexpr int ring_bytes(int steps) { return kWarps * kStages * stage_bytes(steps); }
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 __host__ __device__ constexpr int token_bytes(int steps) { return kRows * steps * 128 + kMaxPass * 64; }
 
 struct Routed {
@@ -232,31 +232,29 @@ struct Segment {
     int entry, tile, s, end;                 // tile: the warp's 8 hidden units (up), the output tile (down)
 };
 
-// The weights of one warp, kStages chunks in flight.  A copy instruction takes runs of STEPS *
-// 128 bytes of 4 / STEPS rows: of the run lengths tried on 1.9 GB, 64 bytes a row read at 6.4
-// TB/s and 256 at 6.8, and a run off a 32-byte boundary costs one sector more whatever its
-// length.  Stage: 16 rows of STEPS * 128 bytes; odd rows have the halves of each 128 bytes
-// exchanged, so that a quarter-warp's reads (2 rows x 64 bytes) touch every bank once.
-// `next(segment)` moves on and returns false at the end; `rows(segment, w, second)` gives the
-// warp's rows 0..7 (w) and 8..15 (w + second), `ld` apart, and returns false where it has none.
+// The weights of one warp, kStages steps in flight.  A copy instruction takes runs of 128 bytes
+// of 4 rows (with runs of 64 bytes the launch of 16 tokens took 352 us instead of 272, with 256
+// as long but fewer, larger stages 5 to 10 % longer where K is no multiple of 128).  Stage: 16
+// rows of 128 bytes; odd rows have the halves exchanged, so that a quarter-warp's reads (2 rows
+// x 64 bytes) touch every bank once.  `next(segment)` moves on and returns false at the end;
+// `rows(segment, w, second)` gives the warp's rows 0..7 (w) and 8..15 (w + second), `ld` apart,
+// and returns false where it has none.
 template <int STEPS, class Next, class RowsOf>
 struct Weights {
-    static constexpr int kLanes = STEPS * 8, kRun = 32 / kLanes;        // lanes of a row, rows of an instruction
     Segment g;
     const __nv_bfloat16* w = nullptr;        // this lane's row and column 0 of a run
     int64_t second = 0, ld;
-    int at = 0, K, group, hop;               // at: the first step of the chunk copied next
+    int at = 0, half = 0, K, group, hop;     // the step copied next, and which of its chunk's it is
     bool live, mine = false;
     uint32_t copy_to, read_from, wr = 0, rd = 0;
     Next next;
     RowsOf rows;
     __device__ __forceinline__ Weights(Next n, RowsOf r, uint32_t ring, int K_, int64_t ld_, int group_, int split)
         : ld(ld_), K(K_), group(group_), hop(STEPS * split), next(n), rows(r) {
-        const int lane = threadIdx.x & 31, run = lane / kLanes, line = lane % kLanes, g8 = lane >> 2;
-        ring += (threadIdx.x >> 5) * kStages * stage_bytes(STEPS);
-        // kRun is even or 1: a lane's rows are all odd or all even, or (1) the instruction's are
-        copy_to = ring + run * STEPS * 128 + line * 16;
-        read_from = ring + g8 * STEPS * 128 + (((lane & 3) * 16) ^ ((g8 & 1) * 64));
+        const int lane = threadIdx.x & 31, run = lane >> 3, g8 = lane >> 2;
+        ring += (threadIdx.x >> 5) * kStages * kStageBytes;
+        copy_to = ring + run * 128 + (((lane & 7) * 16) ^ ((run & 1) * 64));
+        read_from = ring + g8 * 128 + (((lane & 3) * 16) ^ ((g8 & 1) * 64));
         enter();
 #pragma unroll
         for (int d = 0; d < kStages; ++d) issue();
@@ -265,33 +263,34 @@ struct Weights {
         live = next(g);
         if (!live) return;
         mine = rows(g, w, second);
-        w += (int64_t)((threadIdx.x & 31) / kLanes) * ld + (threadIdx.x & 31) % kLanes * 8;
+        w += (int64_t)((threadIdx.x & 31) >> 3) * ld + (threadIdx.x & 7) * 8;
         at = g.s + STEPS * group;
     }
     __device__ __forceinline__ void issue() {
         if (live) {
             if (mine && at < g.end) {
-                const int c = at * 64, last = g.end * 64 < K ? g.end * 64 : K;
-                const int n = c + (int)(threadIdx.x & 31) % kLanes * 8 < last ? 16 : 0;        // past the row: zeros
-                const uint32_t to = copy_to + (wr & (kStages - 1)) * stage_bytes(STEPS);
-                const __nv_bfloat16* from = w + (n ? c : 0);
-#pragma unroll
-                for (int i = 0; i < 16 / kRun; ++i) {
-                    const int row = i * kRun;              // of the lanes with run 0
-                    const uint32_t odd = ((row + (threadIdx.x & 31) / kLanes) & 1) * 64;
-                    copy((to + row * STEPS * 128) ^ odd, from + (row & 7) * ld + (row < 8 ? 0 : second), n);
-                }
+                const int n = at * 64 + (int)(threadIdx.x & 7) * 8 < K ? 16 : 0;       // past the row: zeros
+                const uint32_t to = copy_to + (wr & (kStages - 1)) * kStageBytes;
+                const __nv_bfloat16* from = w + (n ? at * 64 : 0);
+                copy(to, from, n);
+                copy(to + 512, from + 4 * ld, n);
+                copy(to + 1024, from + second, n);
+                copy(to + 1536, from + second + 4 * ld, n);
             }
-            at += hop;
-            if (at - STEPS * group >= g.end) enter();
+            ++at;
+            if (++half == STEPS) {
+                half = 0;
+                at += hop - STEPS;
+                if (at - STEPS * group >= g.end) enter();
+            }
         }
         ++wr;
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    __device__ __forceinline__ uint32_t wait() {           // this lane's place in the chunk to compute
+    __device__ __forceinline__ uint32_t wait() {           // this lane's place in the step to compute
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncwarp();
-        return read_from + (rd++ & (kStages - 1)) * stage_bytes(STEPS);
+        return read_from + (rd++ & (kStages - 1)) * kStageBytes;
     }
     static __device__ __forceinline__ void copy(uint32_t to, const void* from, int bytes) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
@@ -402,26 +401,23 @@ __device__ __forceinline__ void products(float (*acc)[4], W& weights, B& tokens,
             if (BUFS == 1) __syncthreads();
             tokens.load();
         }
-        const uint32_t from = weights.wait();
-        if (mine) {
 #pragma unroll
-            for (int d = 0; d < STEPS; ++d) {
-                if (c + STEPS * group + d < g.end) {
-                    const uint32_t at = from + d * 128, rows8 = 8 * STEPS * 128;
-                    const uint4 w0 = load_smem(at), w1 = load_smem(at + rows8), w2 = load_smem(at ^ 64), w3 = load_smem((at + rows8) ^ 64);
+        for (int d = 0; d < STEPS; ++d) {
+            const uint32_t from = weights.wait();
+            if (mine && c + STEPS * group + d < g.end) {
+                const uint4 w0 = load_smem(from), w1 = load_smem(from + 1024), w2 = load_smem(from ^ 64), w3 = load_smem((from + 1024) ^ 64);
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const uint4 u = load_smem(row[i] + buffer + d * 128), v = load_smem(row[i] + buffer + d * 128 + 64);
-                        mma(acc[i], w0.x, w1.x, w0.y, w1.y, u.x, u.y);
-                        mma(acc[i], w0.z, w1.z, w0.w, w1.w, u.z, u.w);
-                        mma(acc[i], w2.x, w3.x, w2.y, w3.y, v.x, v.y);
-                        mma(acc[i], w2.z, w3.z, w2.w, w3.w, v.z, v.w);
-                    }
+                for (int i = 0; i < NT; ++i) {
+                    const uint4 u = load_smem(row[i] + buffer + d * 128), v = load_smem(row[i] + buffer + d * 128 + 64);
+                    mma(acc[i], w0.x, w1.x, w0.y, w1.y, u.x, u.y);
+                    mma(acc[i], w0.z, w1.z, w0.w, w1.w, u.z, u.w);
+                    mma(acc[i], w2.x, w3.x, w2.y, w3.y, v.x, v.y);
+                    mma(acc[i], w2.z, w3.z, w2.w, w3.w, v.z, v.w);
                 }
             }
+            __syncwarp();                    // every lane has read the stage that is filled next
+            weights.issue();
         }
-        __syncwarp();                        // every lane has read the stage that is filled next
-        weights.issue();
     }
 }
 
@@ -443,7 +439,7 @@ __device__ __forceinline__ void products_of(float (*acc)[4], W& weights, B& toke
 // lane ends with left and gate of its unit.  KEPT: the tokens stay in shared memory, and the
 // units of all entries are dealt to the warps one by one; otherwise a CTA's row groups take
 // neighbouring units of one entry, which share its chunks of tokens.
-constexpr int kUpSmem = ring_bytes(kSteps) + 2 * token_bytes(kSteps) + kWarps * 16 * 32 * 4;
+constexpr int kUpSmem = kRingBytes + 2 * token_bytes(kSteps) + kWarps * 16 * 32 * 4;
 
 template <bool KEPT>
 __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
@@ -452,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
     auto from = [&](int pair) { return pair / a.k; };
     // x is older than the launch ahead of this one
-    Kept<decltype(from)> kept(from, chosen, a.x, ring + ring_bytes(kSteps), KEPT ? a.T : 0, a.D);
+    Kept<decltype(from)> kept(from, chosen, a.x, ring + kRingBytes, KEPT ? a.T : 0, a.D);
     read_choice(chosen, a, kMaxPass, smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int groups = a.H / 8, units = chosen.count * groups, steps = (a.D + 63) / 64, ctas = gridDim.x;
@@ -500,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
         second = (int64_t)a.H * a.D;
         return true;
     };
-    float* part = reinterpret_cast<float*>(smem + ring_bytes(kSteps) + 2 * token_bytes(kSteps));       // [warp][value][lane]
+    float* part = reinterpret_cast<float*>(smem + kRingBytes + 2 * token_bytes(kSteps));       // [warp][value][lane]
     Weights<kSteps, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.D, a.D, group, split);
     auto run = [&](auto& tokens, auto bufs) {
         int at = begin;
@@ -549,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     if constexpr (KEPT) {
         run(kept, std::integral_constant<int, 0>{});       // read_choice's barriers have published the rows
     } else {
-        Tokens<kSteps, 2, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.x, ring + ring_bytes(kSteps), a.D, split);
+        Tokens<kSteps, 2, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.x, ring + kRingBytes, a.D, split);
         run(tokens, std::integral_constant<int, 2>{});
     }
 }
@@ -594,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, i
     };
     auto from = [&](int pair) { return pair; };
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem);
-    float* sums = reinterpret_cast<float*>(smem + ring_bytes(kSteps) + (BUFS == 1 ? 1 : 2) * token_bytes(kSteps));      // [kWarps][T][16]
+    float* sums = reinterpret_cast<float*>(smem + kRingBytes + (BUFS == 1 ? 1 : 2) * token_bytes(kSteps));      // [kWarps][T][16]
     float* tile = sums + warp * a.T * 16;
     Weights<kSteps, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.H, a.H, group, split);
     for (int i = lane; i < a.T * 16; i += 32) tile[i] = 0.f;
@@ -643,11 +639,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, i
         if (open >= 0) finish(open);
     };
     if constexpr (BUFS == 0) {
-        Kept<decltype(from)> kept(from, chosen, a.h, ring + ring_bytes(kSteps), a.T * a.k, a.H);
+        Kept<decltype(from)> kept(from, chosen, a.h, ring + kRingBytes, a.T * a.k, a.H);
         __syncthreads();
         run(kept);
     } else {
-        Tokens<kSteps, BUFS, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.h, ring + ring_bytes(kSteps), a.H, split);
+        Tokens<kSteps, BUFS, decltype(next_t), decltype(from)> tokens(next_t, from, chosen, a.h, ring + kRingBytes, a.H, split);
         run(tokens);
     }
 }
@@ -702,7 +698,7 @@ cudaError_t launch_clusters(void (*kernel)(Args...), int clusters, int size, int
 }
 
 int down_smem(int bufs, int64_t T) {
-    return ring_bytes(kSteps) + bufs * token_bytes(kSteps) + (int)(kWarps * T * 16 * sizeof(float));
+    return kRingBytes + bufs * token_bytes(kSteps) + (int)(kWarps * T * 16 * sizeof(float));
 }
 
 // Output columns of a tile: as many as leave 12 tiles (wide tiles share the tokens' chunks among
