@@ -11,7 +11,9 @@ library raises ``RuntimeError`` (there is no fallback path).
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 import threading
 
@@ -618,6 +620,7 @@ def swiglu_moe_routed_fwd(x, Wr, W1, W2, top_k: int, renormalize: bool = True, r
 # ---------------------------------------------------------------------------- layer norm
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}      # swiglu_dtype
+_dtype_of = operator.attrgetter("dtype")
 
 
 # The calls below are short on the device (a few microseconds for a decode step's tokens), so
@@ -812,19 +815,21 @@ def swiglu_mlp_clip_grads_workspace_size(n: int) -> int:
 
 
 def _grad_arrays(tensors, name: str):
-    """(pointers, counts, type codes) of contiguous tensors on one device, and the device."""
-    device = tensors[0].device
-    for i, t in enumerate(tensors):
-        if t.device != device:
-            raise ValueError(f"{name}[{i}]: on {t.device}, the call's other tensors are on {device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{i}]: tensor must be contiguous")
+    """Host arrays (pointers, counts, type codes) of contiguous tensors on one device, and the
+    device.  A model's gradients are many: one pass in C for each property."""
+    device, of = tensors[0].device, torch.Tensor
+    if len(set(map(of.get_device, tensors))) > 1 or not all(map(of.is_contiguous, tensors)):
+        for i, t in enumerate(tensors):
+            if t.device != device:
+                raise ValueError(f"{name}[{i}]: on {t.device}, the call's other tensors are on {device}")
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}]: tensor must be contiguous")
     try:
-        codes = [_DTYPES[t.dtype] for t in tensors]
+        codes = array.array("i", map(_DTYPES.__getitem__, map(_dtype_of, tensors)))
     except KeyError:
         i = next(i for i, t in enumerate(tensors) if t.dtype not in _DTYPES)
         raise TypeError(f"{name}[{i}]: {tensors[i].dtype}, expected bf16, fp16 or fp32") from None
-    return [t.data_ptr() for t in tensors], [t.numel() for t in tensors], codes, device
+    return array.array("Q", map(of.data_ptr, tensors)), array.array("q", map(of.numel, tensors)), codes, device
 
 
 def _clip_call(grads, max_norm, eps, out, norm, workspace):
@@ -832,8 +837,6 @@ def _clip_call(grads, max_norm, eps, out, norm, workspace):
         raise ValueError("grads: empty")
     n = len(grads)
     ptrs, counts, codes, device = _grad_arrays(grads, "grads")
-    pointers = ctypes.c_void_p * n
-    ptrs = pointers(*ptrs)
     outs = None
     if out is grads:
         outs = ptrs
@@ -841,12 +844,12 @@ def _clip_call(grads, max_norm, eps, out, norm, workspace):
         outs, ocounts, ocodes, odevice = _grad_arrays(out, "out") if out else (None,) * 4
         if odevice != device or ocounts != counts or ocodes != codes:
             raise ValueError("out: one tensor of the same type, element count and device for each gradient")
-        outs = pointers(*outs)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=device)
     if workspace is None:
         workspace = torch.empty(swiglu_mlp_clip_grads_workspace_size(n), dtype=torch.uint8, device=device)
-    st = lib().swiglu_mlp_clip_grads(ptrs, outs, (_i64 * n)(*counts), (_i32 * n)(*codes), n, max_norm, eps,
+    st = lib().swiglu_mlp_clip_grads(ptrs.buffer_info()[0], None if outs is None else outs.buffer_info()[0],
+                                     counts.buffer_info()[0], codes.buffer_info()[0], n, max_norm, eps,
                                      _vector(norm, "norm", (), torch.float32, device),
                                      _workspace_ptr(workspace, device), _nbytes(workspace), _device_stream(device))
     if st:
