@@ -160,16 +160,19 @@ struct Chosen {
 
 // `scratch`: kMaxExperts x 10 bytes.  Tokens choose an expert at most once, so a bit for each
 // of the 64 tokens is an expert's list, and the list's order does not depend on timing.
+// The up kernel comes up while the router runs and waits for it here; only then may the down
+// kernel come up, which therefore finds the router's results in place (L2) and can start on its
+// weights while the last hidden units are computed.
+template <bool WAIT>
 __device__ __forceinline__ void read_choice(Chosen& c, const Routed& a, int pass, void* scratch) {
     unsigned long long* tokens = static_cast<unsigned long long*>(scratch);
     short* start = reinterpret_cast<short*>(tokens + kMaxExperts);
     const int pairs = a.T * a.k;
     for (int e = threadIdx.x; e < a.E; e += kThreads) tokens[e] = 0;
-    // each launch may come up while the one before it runs, whose results it waits for here
+    if (WAIT) cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
-    cudaGridDependencySynchronize();
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += kThreads) atomicOr(&tokens[a.ids[p]], 1ull << (p / a.k));
+    for (int p = threadIdx.x; p < pairs; p += kThreads) atomicOr(&tokens[__ldcg(a.ids + p)], 1ull << (p / a.k));
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
@@ -198,7 +201,7 @@ __device__ __forceinline__ void read_choice(Chosen& c, const Routed& a, int pass
     }
     __syncthreads();
     for (int p = threadIdx.x; p < pairs; p += kThreads) {
-        const int e = a.ids[p], t = p / a.k;
+        const int e = __ldcg(a.ids + p), t = p / a.k;
         c.order[start[e] + __popcll(tokens[e] & ((1ull << t) - 1))] = (short)p;
     }
     __syncthreads();
@@ -311,37 +314,44 @@ struct Tokens {
     int at = 0, K, hop, lines, pitch;        // hop: steps of a chunk; lines: log2 of its 16-byte pieces a token
     bool live;
     uint32_t buffers, put = 0;
+    uint32_t start[kPieces];                 // the first element of a piece's row in `base`; kNoRow: none
     uint4 piece[kPieces];
     Next next;
     From from;
+    static constexpr uint32_t kNoRow = ~0u;  // rows x K stays below 2^31
     __device__ __forceinline__ Tokens(Next n, From f, const Chosen& c, const __nv_bfloat16* b, uint32_t smem, int K_, int split)
         : chosen(c), base(b), K(K_), buffers(smem), next(n), from(f) {
         hop = STEPS * split;
         lines = (STEPS == 2 ? 4 : 3) + (31 - __clz(split));
         pitch = (16 << lines) + 64;
-        live = next(g);
-        at = live ? g.s : 0;
+        enter();
         load();
         if (BUFS == 2) {
             store();
             load();
         }
     }
-    __device__ __forceinline__ void load() {
+    __device__ __forceinline__ void enter() {
+        live = next(g);
         if (!live) return;
+        at = g.s;
         const int first = chosen.first[g.entry], n = chosen.pairs[g.entry];
-        const int end = g.end * 64 < K ? g.end * 64 : K;
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            const int i = threadIdx.x + j * kThreads, row = i >> lines, col = at * 64 + (i & ((1 << lines) - 1)) * 8;
+            const int i = threadIdx.x + j * kThreads, row = i >> lines;
+            start[j] = row < n ? (uint32_t)from(chosen.order[first + row]) * (uint32_t)K : kNoRow;
+        }
+    }
+    __device__ __forceinline__ void load() {
+        if (!live) return;
+        const int end = g.end * 64 < K ? g.end * 64 : K, col = at * 64 + (int)(threadIdx.x & ((1 << lines) - 1)) * 8;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
             piece[j] = make_uint4(0, 0, 0, 0);
-            if (row < n && col < end) piece[j] = *reinterpret_cast<const uint4*>(base + from(chosen.order[first + row]) * K + col);
+            if (start[j] != kNoRow && col < end) piece[j] = *reinterpret_cast<const uint4*>(base + (start[j] + (uint32_t)col));
         }
         at += hop;
-        if (at >= g.end) {
-            live = next(g);
-            at = live ? g.s : 0;
-        }
+        if (at >= g.end) enter();
     }
     __device__ __forceinline__ void store() {
         const uint32_t to = buffers + (put++ & (BUFS - 1)) * token_bytes(STEPS);
@@ -449,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     auto from = [&](int pair) { return pair / a.k; };
     // x is older than the launch ahead of this one
     Kept<decltype(from)> kept(from, chosen, a.x, ring + kRingBytes, KEPT ? a.T : 0, a.D);
-    read_choice(chosen, a, kMaxPass, smem);
+    read_choice<true>(chosen, a, kMaxPass, smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int groups = a.H / 8, units = chosen.count * groups, steps = (a.D + 63) / 64, ctas = gridDim.x;
     int split = 1;
@@ -561,7 +571,7 @@ template <int BUFS>
 __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, int split) {
     __shared__ Chosen chosen;
     extern __shared__ __align__(128) unsigned char smem[];
-    read_choice(chosen, a, min(kMaxPass, kRows / split), smem);
+    read_choice<false>(chosen, a, min(kMaxPass, kRows / split), smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int steps = (a.H + 63) / 64, row = warp / split, group = warp % split;
     const long long span = (long long)chosen.count * steps;
@@ -594,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, i
     float* tile = sums + warp * a.T * 16;
     Weights<kSteps, decltype(next_w), decltype(rows)> weights(next_w, rows, ring, a.H, a.H, group, split);
     for (int i = lane; i < a.T * 16; i += 32) tile[i] = 0.f;
-    __syncwarp();
+    cudaGridDependencySynchronize();         // h is complete; the first weights are on their way
     auto finish = [&](int t) {               // tile t's part, and zeros for the next
         __syncthreads();
         float* part = a.parts + (int64_t)(blockIdx.x + t) * a.T * a.width;
@@ -627,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, i
                     const int col = i * 8 + 2 * q + v;
                     if (col < n) {
                         const int p = chosen.order[first + col];
-                        const float gate = a.gates[p];
+                        const float gate = __ldcg(a.gates + p);
                         float* o = tile + p / a.k * 16 + g;
                         o[0] += gate * acc[i][v];
                         o[8] += gate * acc[i][2 + v];
