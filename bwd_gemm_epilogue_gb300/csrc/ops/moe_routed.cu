@@ -61,7 +61,7 @@ struct Routed {
     float* gates;
     int T, E, D, H, Dout, k, renorm, wr32;
     float* parts;                            // [CTA + tile][T][width]: a CTA's part of a tile
-    long long* steps;                        // the span of a tile, then every CTA's first step: for the join kernel
+    int* span;                               // the down kernel's steps of a tile, for the join kernel
     int width, tiles, ctas;                  // output columns of a tile; tiles; CTAs of the down kernel
 };
 
@@ -560,6 +560,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     }
 }
 
+// CTAs of the down kernel that have steps: CTA c has [all * c / n, all * (c + 1) / n) of all =
+// tiles * span steps, at least one each.
+__device__ __forceinline__ int down_sharers(int ctas, int tiles, int span) {
+    return (int)min((long long)ctas, (long long)tiles * span);
+}
+
 // A tile is `width` = 16 * (kWarps / split) output columns, and its span the steps of all
 // entries, one after the other; the spans of all tiles are divided evenly over the CTAs.  A
 // warp adds each segment's sums, times the gates, into its own fp32 tile [T][16]; at the end
@@ -574,13 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, i
     read_choice<false>(chosen, a, min(kMaxPass, kRows / split), smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int steps = (a.H + 63) / 64, row = warp / split, group = warp % split;
-    const long long span = (long long)chosen.count * steps;
-    const long long begin = a.tiles * span * blockIdx.x / a.ctas, end = a.tiles * span * (blockIdx.x + 1) / a.ctas;
-    if (threadIdx.x == 0) {
-        if (blockIdx.x == 0) a.steps[0] = span;
-        a.steps[1 + blockIdx.x] = begin;
-        if (blockIdx.x == a.ctas - 1) a.steps[2 + blockIdx.x] = end;
-    }
+    const int span = chosen.count * steps, sharers = down_sharers(a.ctas, a.tiles, span);
+    const long long all = (long long)a.tiles * span;
+    const long long begin = (int)blockIdx.x < sharers ? all * blockIdx.x / sharers : 0;
+    const long long end = (int)blockIdx.x < sharers ? all * (blockIdx.x + 1) / sharers : 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.span = span;
     long long ahead_w = begin, ahead_t = begin;
     auto segment = [&](long long& ahead, Segment& f) {
         if (ahead >= end) return false;
@@ -658,22 +662,25 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, i
     }
 }
 
-// y: the parts of a tile, from the CTAs whose steps meet its span, in order.
+// y: the parts of a tile, in the order of the CTAs whose steps meet its span, that is
+// first <= c <= last with first = floor((tile * span * n + n - 1) / (tiles * span)) and
+// last = ceil((tile + 1) * n / tiles) - 1.  Grid (blocks of columns, tokens).
 __global__ void __launch_bounds__(256) moe_join_kernel(const Routed a) {
+    const int col = blockIdx.x * 256 + threadIdx.x, tile = col / a.width, in = col - tile * a.width;
+    const int64_t i = (int64_t)blockIdx.y * a.Dout + col;
+    const float* part = a.parts + (int64_t)blockIdx.y * a.width + in;
+    const float v = a.r && col < a.Dout ? to_f32(a.r[i]) : 0.f;            // older than the call
     cudaGridDependencySynchronize();
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= a.T * a.Dout) return;
-    const int t = i / a.Dout, col = i - t * a.Dout, tile = col / a.width;
-    const long long lo = tile * a.steps[0], hi = lo + a.steps[0];
-    const float* part = a.parts + (int64_t)t * a.width + (col - tile * a.width);
-    const float v = a.r ? to_f32(a.r[i]) : 0.f;
+    if (col >= a.Dout) return;
+    const int span = *a.span, n = down_sharers(a.ctas, a.tiles, span);
+    const int first = (tile * n + (n - 1) / span) / a.tiles, last = ((tile + 1) * n - 1) / a.tiles;
     float sum = 0.f;
-    int c = tile * a.ctas / a.tiles;         // the first CTA that has steps of the tile, or the one before it
-    long long end = a.steps[1 + c];
-    for (; c < a.ctas && end < hi; ++c) {
-        const long long begin = end;
-        end = a.steps[2 + c];
-        if (end > lo && end > begin) sum += part[(int64_t)(c + tile) * a.T * a.width];
+    for (int c = first; c <= last; c += 8) {               // 8 loads in flight
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = c + j <= last ? part[(int64_t)(c + j + tile) * a.T * a.width] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += p[j];
     }
     a.y[i] = __float2bfloat16_rn(v + sum);
 }
@@ -682,9 +689,9 @@ __global__ void __launch_bounds__(256) moe_join_kernel(const Routed a) {
 
 bool width_ok(int64_t v) { return v > 0 && v % 8 == 0 && v < (int64_t(1) << 24); }
 
-// `clusters` clusters of `size` CTAs; early: the launch may start before the one ahead of it ends.
+// A grid of clusters of `size` CTAs along x; early: the launch may start before the one ahead of it ends.
 template <class... Args>
-cudaError_t launch_clusters(void (*kernel)(Args...), int clusters, int size, int threads, size_t smem, cudaStream_t s,
+cudaError_t launch_clusters(void (*kernel)(Args...), dim3 clusters, int size, int threads, size_t smem, cudaStream_t s,
                             bool early, Args... args) {
     cudaError_t e = smem <= 48 * 1024
                         ? cudaSuccess
@@ -700,7 +707,7 @@ cudaError_t launch_clusters(void (*kernel)(Args...), int clusters, int size, int
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = early ? 2 : 1;
-    cfg.gridDim = dim3(clusters * size);
+    cfg.gridDim = dim3(clusters.x * size, clusters.y);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -722,8 +729,7 @@ int down_tiles(int64_t Dout) { return (int)((Dout + down_width(Dout) - 1) / down
 int down_ctas(int64_t Dout) { return std::min(kPlanSms, 16 * down_tiles(Dout)); }
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
-constexpr size_t kStepsBytes = 1536;         // the join kernel's table: kPlanSms + 2 entries
-static_assert((kPlanSms + 2) * sizeof(long long) <= kStepsBytes, "the table fits");
+constexpr size_t kSpanBytes = 256;           // the join kernel's span
 size_t h_bytes(int64_t T, int64_t H, int64_t k) { return round256((size_t)T * (size_t)k * (size_t)H * 2); }
 size_t part_bytes(int64_t T, int64_t Dout) {
     return (size_t)(down_ctas(Dout) + down_tiles(Dout)) * (size_t)T * (size_t)down_width(Dout) * sizeof(float);
@@ -738,7 +744,7 @@ extern "C" {
 
 size_t swiglu_moe_routed_fwd_workspace_size(int64_t T, int64_t H, int64_t Dout, int64_t top_k) {
     if (T <= 0 || H <= 0 || Dout <= 0 || top_k <= 0) return 0;
-    return h_bytes(T, H, top_k) + kStepsBytes + round256(part_bytes(T, Dout));
+    return h_bytes(T, H, top_k) + kSpanBytes + round256(part_bytes(T, Dout));
 }
 
 swiglu_status swiglu_moe_routed_fwd(const void* x, const void* Wr, const void* W1, const void* W2,
@@ -766,7 +772,7 @@ swiglu_status swiglu_moe_routed_fwd(const void* x, const void* Wr, const void* W
     uint8_t* ws = static_cast<uint8_t*>(workspace) + h_bytes(T, H, top_k);
     const Routed a{(In)x, (In)W1, (In)W2, (In)residual, Wr, (__nv_bfloat16*)y, (__nv_bfloat16*)workspace, ids, gates,
                    (int)T, (int)E, (int)D, (int)H, (int)Dout, (int)top_k, renormalize != 0, router_fp32 != 0,
-                   reinterpret_cast<float*>(ws + kStepsBytes), reinterpret_cast<long long*>(ws), down_width(Dout), down_tiles(Dout),
+                   reinterpret_cast<float*>(ws + kSpanBytes), reinterpret_cast<int*>(ws), down_width(Dout), down_tiles(Dout),
                    down_ctas(Dout)};
     // route: up to 8 CTAs of 8 warps share a token's experts
     const int route_ctas = E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8;
@@ -790,7 +796,7 @@ swiglu_status swiglu_moe_routed_fwd(const void* x, const void* Wr, const void* W
     });
     if (rc != SWIGLU_OK) return rc;
     return launch_traced(SWIGLU_KERNEL_MOE_JOIN, s, [&] {
-        return launch_clusters(moe_join_kernel, (int)((T * Dout + 255) / 256), 1, 256, 0, s, true, a);
+        return launch_clusters(moe_join_kernel, dim3((unsigned)((Dout + 255) / 256), (unsigned)T), 1, 256, 0, s, true, a);
     });
 }
 
