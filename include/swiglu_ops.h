@@ -4,8 +4,9 @@
  * backward, and the clipping of many gradients by their global norm.
  *
  * Unlike the block's GEMMs these take bf16, fp16 or fp32 tensors of any width, and rows
- * at any stride: a pointer needs only its element's alignment (16-byte aligned rows are
- * read in 16-byte pieces and run fastest).
+ * at any stride: a pointer needs only its element's alignment.  Rows on 16-byte boundaries
+ * run fastest, then rows off them that start alike in every tensor of a call (contiguous
+ * tensors of one odd width do), then others.
  */
 #ifndef SWIGLU_OPS_H
 #define SWIGLU_OPS_H
