@@ -11,10 +11,10 @@ library raises ``RuntimeError`` (there is no fallback path).
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import operator
 import os
+import struct
 import threading
 
 import torch
@@ -814,9 +814,9 @@ def swiglu_mlp_clip_grads_workspace_size(n: int) -> int:
     return int(lib().swiglu_mlp_clip_grads_workspace_size(n))
 
 
-def _grad_arrays(tensors, name: str):
-    """Host arrays (pointers, counts, type codes) of contiguous tensors on one device, and the
-    device.  A model's gradients are many: one pass in C for each property."""
+def _grad_lists(tensors, name: str):
+    """Device, types, element counts and pointers of contiguous tensors on one device.  A
+    model's gradients are many: one pass in C for each property."""
     device, of = tensors[0].device, torch.Tensor
     if len(set(map(of.get_device, tensors))) > 1 or not all(map(of.is_contiguous, tensors)):
         for i, t in enumerate(tensors):
@@ -824,32 +824,33 @@ def _grad_arrays(tensors, name: str):
                 raise ValueError(f"{name}[{i}]: on {t.device}, the call's other tensors are on {device}")
             if not t.is_contiguous():
                 raise ValueError(f"{name}[{i}]: tensor must be contiguous")
-    try:
-        codes = array.array("i", map(_DTYPES.__getitem__, map(_dtype_of, tensors)))
-    except KeyError:
-        i = next(i for i, t in enumerate(tensors) if t.dtype not in _DTYPES)
-        raise TypeError(f"{name}[{i}]: {tensors[i].dtype}, expected bf16, fp16 or fp32") from None
-    return array.array("Q", map(of.data_ptr, tensors)), array.array("q", map(of.numel, tensors)), codes, device
+    return device, list(map(_dtype_of, tensors)), list(map(of.numel, tensors)), list(map(of.data_ptr, tensors))
 
 
 def _clip_call(grads, max_norm, eps, out, norm, workspace):
     if not grads:
         raise ValueError("grads: empty")
     n = len(grads)
-    ptrs, counts, codes, device = _grad_arrays(grads, "grads")
-    outs = None
+    device, types, counts, ptrs = _grad_lists(grads, "grads")
+    try:
+        codes = list(map(_DTYPES.__getitem__, types))
+    except KeyError:
+        i = next(i for i, t in enumerate(types) if t not in _DTYPES)
+        raise TypeError(f"grads[{i}]: {types[i]}, expected bf16, fp16 or fp32") from None
+    pack = struct.Struct(f"{n}Q").pack
+    ins, outs = pack(*ptrs), None
     if out is grads:
-        outs = ptrs
+        outs = ins
     elif out is not None:
-        outs, ocounts, ocodes, odevice = _grad_arrays(out, "out") if out else (None,) * 4
-        if odevice != device or ocounts != counts or ocodes != codes:
+        odevice, otypes, ocounts, optrs = _grad_lists(out, "out") if out else (None,) * 4
+        if odevice != device or ocounts != counts or otypes != types:
             raise ValueError("out: one tensor of the same type, element count and device for each gradient")
+        outs = pack(*optrs)
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=device)
     if workspace is None:
         workspace = torch.empty(swiglu_mlp_clip_grads_workspace_size(n), dtype=torch.uint8, device=device)
-    st = lib().swiglu_mlp_clip_grads(ptrs.buffer_info()[0], None if outs is None else outs.buffer_info()[0],
-                                     counts.buffer_info()[0], codes.buffer_info()[0], n, max_norm, eps,
+    st = lib().swiglu_mlp_clip_grads(ins, outs, pack(*counts), struct.pack(f"{n}i", *codes), n, max_norm, eps,
                                      _vector(norm, "norm", (), torch.float32, device),
                                      _workspace_ptr(workspace, device), _nbytes(workspace), _device_stream(device))
     if st:
