@@ -596,22 +596,16 @@ def swiglu_moe_routed_fwd(x, Wr, W1, W2, top_k: int, renormalize: bool = True, r
     if W1.shape != (E, 2 * H, D):
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, W1 {tuple(W1.shape)}, W2 {tuple(W2.shape)}")
     fp32 = Wr.dtype == torch.float32
-    if y is None:
-        y = torch.empty((T, Dout), dtype=bf, device=device)
-    if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=device)
-    if gates is None:
-        gates = torch.empty((T, top_k), dtype=torch.float32, device=device)
-    if workspace is None:
-        workspace = torch.empty(max(16, swiglu_moe_routed_fwd_workspace_size(T, H, Dout, top_k)), dtype=torch.uint8,
-                                device=device)
-    st = lib().swiglu_moe_routed_fwd(
-        _vector(x, "x", (T, D), bf, device), _vector(Wr, "Wr", (E, D), torch.float32 if fp32 else bf, device),
-        _vector(W1, "W1", W1.shape, bf, device), _vector(W2, "W2", W2.shape, bf, device),
-        _vector(residual, "residual", (T, Dout), bf, device), _vector(y, "y", (T, Dout), bf, device),
-        _vector(ids, "ids", (T, top_k), torch.int32, device),
-        _vector(gates, "gates", (T, top_k), torch.float32, device), T, E, D, H, Dout, top_k, bool(renormalize), fp32,
-        _workspace_ptr(workspace, device), _nbytes(workspace), _device_stream(device))
+    px, pr = _vector(x, "x", (T, D), bf, device), _vector(Wr, "Wr", (E, D), torch.float32 if fp32 else bf, device)
+    p1, p2 = _vector(W1, "W1", W1.shape, bf, device), _vector(W2, "W2", W2.shape, bf, device)
+    pres = _vector(residual, "residual", (T, Dout), bf, device)
+    y, py = _out_vector(y, "y", (T, Dout), bf, device)
+    ids, pids = _out_vector(ids, "ids", (T, top_k), torch.int32, device)
+    gates, pgates = _out_vector(gates, "gates", (T, top_k), torch.float32, device)
+    need = lib().swiglu_moe_routed_fwd_workspace_size(T, H, Dout, top_k) if workspace is None else 0
+    workspace, pw, nw = _workspace(workspace, need, device)
+    st = lib().swiglu_moe_routed_fwd(px, pr, p1, p2, pres, py, pids, pgates, T, E, D, H, Dout, top_k,
+                                     bool(renormalize), fp32, pw, nw, _device_stream(device))
     if st:
         _check(st, "swiglu_moe_routed_fwd")
     return y, ids, gates
@@ -670,9 +664,28 @@ def _vector(t, name: str, shape, dtype, device):
     return t.data_ptr()
 
 
-def _new_rows(like: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype,
-                                                                          device=like.device)
+def _out_rows(t, name: str, shape, dtype, device):
+    """(tensor, pointer, row stride) of a [M, D] output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr(), shape[1]
+    return (t, *_rows(t, name, shape, dtype, device))
+
+
+def _out_vector(t, name: str, shape, dtype, device):
+    """(tensor, pointer) of a contiguous output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _vector(t, name, shape, dtype, device)
+
+
+def _workspace(t, need: int, device):
+    """(tensor, pointer, bytes) of a workspace: the caller's, or a new one of `need` bytes."""
+    if t is None:
+        t = torch.empty(max(16, need), dtype=torch.uint8, device=device)
+        return t, t.data_ptr(), max(16, need)
+    return t, _workspace_ptr(t, device), _nbytes(t)
 
 
 def _workspace_ptr(t: torch.Tensor, device):
@@ -701,25 +714,19 @@ def swiglu_mlp_layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, resid
     shape, dtype, device = x.shape, x.dtype, x.device
     M, D = shape
     code, wdtype = _dtype(x, "x"), _norm_params(x, gamma, beta)
-    if y is None:
-        y = _new_rows(x)
-    if residual is None:
-        if s is not None:
-            raise ValueError("s: only written with a residual")
-    elif s is None:
-        s = _new_rows(x)
-    if mean is None:
-        mean = torch.empty(M, dtype=torch.float32, device=device)
-    if rstd is None:
-        rstd = torch.empty(M, dtype=torch.float32, device=device)
     px, ldx = _rows(x, "x", shape, dtype, device)
     pr, ldr = _rows(residual, "residual", shape, dtype, device)
-    py, ldy = _rows(y, "y", shape, dtype, device)
-    ps, lds = _rows(s, "s", shape, dtype, device)
-    st = lib().swiglu_mlp_layer_norm_fwd(
-        px, ldx, pr, ldr, _vector(gamma, "gamma", (D,), wdtype, device), _vector(beta, "beta", (D,), wdtype, device),
-        py, ldy, ps, lds, _vector(mean, "mean", (M,), torch.float32, device),
-        _vector(rstd, "rstd", (M,), torch.float32, device), M, D, eps, code, _DTYPES[wdtype], _device_stream(device))
+    pgamma, pbeta = _vector(gamma, "gamma", (D,), wdtype, device), _vector(beta, "beta", (D,), wdtype, device)
+    y, py, ldy = _out_rows(y, "y", shape, dtype, device)
+    ps, lds = None, 0
+    if residual is not None:
+        s, ps, lds = _out_rows(s, "s", shape, dtype, device)
+    elif s is not None:
+        raise ValueError("s: only written with a residual")
+    mean, pmean = _out_vector(mean, "mean", (M,), torch.float32, device)
+    rstd, prstd = _out_vector(rstd, "rstd", (M,), torch.float32, device)
+    st = lib().swiglu_mlp_layer_norm_fwd(px, ldx, pr, ldr, pgamma, pbeta, py, ldy, ps, lds, pmean, prstd, M, D, eps,
+                                         code, _DTYPES[wdtype], _device_stream(device))
     if st:
         _check(st, "swiglu_mlp_layer_norm_fwd")
     return y, (x if s is None else s), mean, rstd
@@ -740,29 +747,23 @@ def swiglu_mlp_layer_norm_bwd(dy, s, gamma, mean, rstd, dskip=None, dx=None, dga
     shape, dtype, device = s.shape, s.dtype, s.device
     M, D = shape
     code, wdtype = _dtype(s, "s"), _norm_params(s, gamma, dbeta)
-    if dx is None:
-        dx = _new_rows(s)
-    if not param_grads:
-        if dgamma is not None or dbeta is not None:
-            raise ValueError("dgamma, dbeta: not computed with param_grads=False")
-    else:
-        if dgamma is None:
-            dgamma = torch.empty(D, dtype=wdtype, device=device)
-        if dbeta is None:
-            dbeta = torch.empty(D, dtype=wdtype, device=device)
-    if workspace is None:
-        workspace = torch.empty(max(16, swiglu_mlp_layer_norm_bwd_workspace_size(M, D)), dtype=torch.uint8,
-                                device=device)
     pdy, lddy = _rows(dy, "dy", shape, dtype, device)
     ps, lds = _rows(s, "s", shape, dtype, device)
     pk, ldk = _rows(dskip, "dskip", shape, dtype, device)
-    pdx, lddx = _rows(dx, "dx", shape, dtype, device)
-    st = lib().swiglu_mlp_layer_norm_bwd(
-        pdy, lddy, ps, lds, _vector(gamma, "gamma", (D,), wdtype, device),
-        _vector(mean, "mean", (M,), torch.float32, device), _vector(rstd, "rstd", (M,), torch.float32, device),
-        pk, ldk, pdx, lddx, _vector(dgamma, "dgamma", (D,), wdtype, device),
-        _vector(dbeta, "dbeta", (D,), wdtype, device), M, D, code, _DTYPES[wdtype],
-        _workspace_ptr(workspace, device), _nbytes(workspace), _device_stream(device))
+    pgamma = _vector(gamma, "gamma", (D,), wdtype, device)
+    pmean = _vector(mean, "mean", (M,), torch.float32, device)
+    prstd = _vector(rstd, "rstd", (M,), torch.float32, device)
+    dx, pdx, lddx = _out_rows(dx, "dx", shape, dtype, device)
+    pdgamma = pdbeta = None
+    if param_grads:
+        dgamma, pdgamma = _out_vector(dgamma, "dgamma", (D,), wdtype, device)
+        dbeta, pdbeta = _out_vector(dbeta, "dbeta", (D,), wdtype, device)
+    elif dgamma is not None or dbeta is not None:
+        raise ValueError("dgamma, dbeta: not computed with param_grads=False")
+    need = lib().swiglu_mlp_layer_norm_bwd_workspace_size(M, D) if workspace is None else 0
+    workspace, pw, nw = _workspace(workspace, need, device)
+    st = lib().swiglu_mlp_layer_norm_bwd(pdy, lddy, ps, lds, pgamma, pmean, prstd, pk, ldk, pdx, lddx, pdgamma, pdbeta,
+                                         M, D, code, _DTYPES[wdtype], pw, nw, _device_stream(device))
     if st:
         _check(st, "swiglu_mlp_layer_norm_bwd")
     return dx, dgamma, dbeta
@@ -846,13 +847,11 @@ def _clip_call(grads, max_norm, eps, out, norm, workspace):
         if odevice != device or ocounts != counts or otypes != types:
             raise ValueError("out: one tensor of the same type, element count and device for each gradient")
         outs = pack(*optrs)
-    if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=device)
-    if workspace is None:
-        workspace = torch.empty(swiglu_mlp_clip_grads_workspace_size(n), dtype=torch.uint8, device=device)
+    norm, pnorm = _out_vector(norm, "norm", (), torch.float32, device)
+    need = lib().swiglu_mlp_clip_grads_workspace_size(n) if workspace is None else 0
+    workspace, pw, nw = _workspace(workspace, need, device)
     st = lib().swiglu_mlp_clip_grads(ins, outs, pack(*counts), struct.pack(f"{n}i", *codes), n, max_norm, eps,
-                                     _vector(norm, "norm", (), torch.float32, device),
-                                     _workspace_ptr(workspace, device), _nbytes(workspace), _device_stream(device))
+                                     pnorm, pw, nw, _device_stream(device))
     if st:
         _check(st, "swiglu_mlp_clip_grads")
     return norm
