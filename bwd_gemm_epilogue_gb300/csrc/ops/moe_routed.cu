@@ -78,11 +78,53 @@ __device__ __forceinline__ void load8(float* o, const float* p) {
     load_pack<float, 4>(p + 4).unpack(o + 4);
 }
 
-// Order-preserving key of a logit: larger logit, larger key; NaN lowest.
+// Order-preserving key of a logit: larger logit, larger key; NaN lowest, but above 0 (none).
 __device__ __forceinline__ uint32_t logit_key(float v) {
-    if (isnan(v)) return 0;
+    if (isnan(v)) return 1;
     const uint32_t u = __float_as_uint(v + 0.f);           // -0 counts as 0
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// Top k of a token's logits by one warp, lane's own of them in registers: lane j < k has the j-th
+// choice and its gate.
+template <int OWN>
+__device__ __forceinline__ void choose(const Routed& a, const float* logits, int& mine, float& gate) {
+    const int lane = threadIdx.x & 31;
+    uint32_t key[OWN];
+    float v[OWN], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const bool in = lane + 32 * i < a.E;
+        v[i] = in ? logits[lane + 32 * i] : -INFINITY;
+        key[i] = in ? logit_key(v[i]) : 0;
+        top = fmaxf(top, v[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+    for (int i = 0; i < OWN; ++i)
+        if (lane + 32 * i < a.E) sum += expf(v[i] - top);  // a NaN logit makes every gate NaN
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    mine = 0;
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < OWN; ++i)
+            if (key[i] > best) best = key[i], at = i;
+        const uint32_t high = __reduce_max_sync(0xffffffffu, best);
+        const int e = __reduce_min_sync(0xffffffffu, best == high ? lane + 32 * at : kMaxExperts);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i)
+            if (e == lane + 32 * i) key[i] = 0;
+        if (lane == j) mine = e;
+    }
+    const float p = lane < a.k ? expf(logits[mine] - top) : 0.f;
+    float chosen = p;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) chosen += __shfl_xor_sync(0xffffffffu, chosen, o);
+    gate = (isnan(sum) ? sum : p) / (a.renorm ? chosen : sum);
 }
 
 constexpr int kRouteWarps = 8;
@@ -116,35 +158,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
     cluster.sync();
     if (rank != 0 || warp != 0) return;
 
-    float top = -INFINITY, sum = 0.f;
-    for (int e = lane; e < a.E; e += 32) top = fmaxf(top, logits[e]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int e = lane; e < a.E; e += 32) sum += expf(logits[e] - top);      // a NaN logit makes every gate NaN
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    uint32_t taken = 0;                                    // bit i: expert lane + 32 i
-    int mine = 0;
-    float weight = 0.f, chosen = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t key = 0;
-        int best = kMaxExperts;
-        for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
-            if (taken >> i & 1) continue;
-            const uint32_t q = logit_key(logits[e]);
-            if (best == kMaxExperts || q > key) key = q, best = e;
-        }
-        const uint32_t high = __reduce_max_sync(0xffffffffu, best < kMaxExperts ? key : 0);
-        const int e = __reduce_min_sync(0xffffffffu, best < kMaxExperts && key == high ? best : kMaxExperts);
-        if ((e & 31) == lane) taken |= 1u << (e >> 5);
-        const float p = expf(logits[e] - top);
-        chosen += p;
-        if (lane == j) mine = e, weight = p;
-    }
-    if (isnan(sum)) weight = sum;
+    int mine;
+    float gate;
+    if (a.E <= 128) choose<4>(a, logits, mine, gate);
+    else choose<(kMaxExperts + 31) / 32>(a, logits, mine, gate);
     if (lane < a.k) {
         a.ids[t * a.k + lane] = mine;
-        a.gates[t * a.k + lane] = weight / (a.renorm ? chosen : sum);
+        a.gates[t * a.k + lane] = gate;
     }
 }
 
@@ -233,6 +253,8 @@ __device__ __forceinline__ void store_smem(uint32_t at, const uint4& v) {
 // chunk is STEPS steps of each k group, that is split * STEPS * 64 consecutive k.
 struct Segment {
     int entry, tile, s, end;                 // tile: the warp's 8 hidden units (up), the output tile (down)
+    int first, rows;                         // of chosen.order: the pairs whose tokens are the chunk's rows
+    int lead, most;                          // those before this entry's; the most pairs of one entry among them
 };
 
 // The weights of one warp, kStages steps in flight.  A copy instruction takes runs of 128 bytes
@@ -335,11 +357,10 @@ struct Tokens {
         live = next(g);
         if (!live) return;
         at = g.s;
-        const int first = chosen.first[g.entry], n = chosen.pairs[g.entry];
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
             const int i = threadIdx.x + j * kThreads, row = i >> lines;
-            start[j] = row < n ? (uint32_t)from(chosen.order[first + row]) * (uint32_t)K : kNoRow;
+            start[j] = row < g.rows ? (uint32_t)from(chosen.order[g.first + row]) * (uint32_t)K : kNoRow;
         }
     }
     __device__ __forceinline__ void load() {
@@ -361,7 +382,7 @@ struct Tokens {
             if (row < kMaxPass) store_smem(to + row * pitch + (i & ((1 << lines) - 1)) * 16, piece[j]);
         }
     }
-    __device__ __forceinline__ uint32_t row(const Segment&, int i) const { return buffers + i * pitch; }
+    __device__ __forceinline__ uint32_t row(const Segment& f, int i) const { return buffers + (f.lead + i) * pitch; }
 };
 
 // All rows that any pair reads, kept in the buffers' place for the whole launch where they fit:
@@ -431,7 +452,8 @@ __device__ __forceinline__ void products(float (*acc)[4], W& weights, B& tokens,
     }
 }
 
-// products() over the number of 8-token tiles that n <= kMaxPass tokens take.
+// products() over the number of 8-token tiles that the most tokens of one of the chunk's entries
+// take (the same for all warps, which meet at its barriers).
 template <int STEPS, int BUFS, class W, class B>
 __device__ __forceinline__ void products_of(float (*acc)[4], W& weights, B& tokens, const Segment& g, int n, bool mine,
                                             int group, int split) {
@@ -439,8 +461,8 @@ __device__ __forceinline__ void products_of(float (*acc)[4], W& weights, B& toke
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    if (n <= 8) products<STEPS, BUFS, 1>(acc, weights, tokens, g, n, mine, group, split);
-    else if (n <= 16) products<STEPS, BUFS, 2>(acc, weights, tokens, g, n, mine, group, split);
+    if (g.most <= 8) products<STEPS, BUFS, 1>(acc, weights, tokens, g, n, mine, group, split);
+    else if (g.most <= 16) products<STEPS, BUFS, 2>(acc, weights, tokens, g, n, mine, group, split);
     else products<STEPS, BUFS, 4>(acc, weights, tokens, g, n, mine, group, split);
 }
 
@@ -482,18 +504,32 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     }
     const int per = kWarps / split, row = warp / split, group = warp % split;
     // KEPT: round j of a warp is unit (j * per + row) * ctas + CTA.  Otherwise a CTA has an even,
-    // consecutive share of the units and takes up to `per` of one entry at a time.
+    // consecutive share of the units and takes `per` at a time, of more than one entry where their
+    // tokens, which follow one another in the list, fit a chunk together (cut at every entry's end,
+    // the CTAs with such an end took a round more: 61 ragged tokens 171 us instead of 165).
     const int begin = KEPT ? 0 : (int)((int64_t)units * blockIdx.x / ctas);
     const int end = KEPT ? (units + ctas * per - 1) / (ctas * per) : (int)((int64_t)units * (blockIdx.x + 1) / ctas);
     auto segment = [&](int& at, Segment& f) {
         if (at >= end) return false;
         if (KEPT) {
-            const int u = (at++ * per + row) * ctas + blockIdx.x;
-            f = {u / groups, u < units ? u % groups : groups, 0, steps};
+            const int u = (at++ * per + row) * ctas + blockIdx.x, entry = u / groups;
+            f = {entry, u < units ? u % groups : groups, 0, steps, 0, 0, 0, u < units ? chosen.pairs[entry] : 0};
             return true;
         }
-        const int entry = at / groups, first = at - entry * groups, n = min(per, min(groups - first, end - at));
-        f = {entry, row < n ? first + row : groups, 0, steps};
+        const int entry0 = at / groups, u = at + row;
+        int n = min(per, end - at), rows = 0, most = 0, entry = entry0, lead = 0;
+        for (int e = entry0, next = (entry0 + 1) * groups;; ++e, next += groups) {
+            const int pairs = chosen.pairs[e];
+            if (e > entry0 && rows + pairs > min(kMaxPass, kRows / split)) {
+                n = min(n, next - groups - at);            // its units are another chunk's
+                break;
+            }
+            if (u >= next - groups) entry = e, lead = rows;
+            rows += pairs;
+            most = max(most, pairs);
+            if (next >= at + n) break;
+        }
+        f = {entry, row < n ? u - entry * groups : groups, 0, steps, chosen.first[entry0], rows, lead, most};
         at += n;
         return true;
     };
@@ -585,12 +621,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, i
     const long long begin = (int)blockIdx.x < sharers ? all * blockIdx.x / sharers : 0;
     const long long end = (int)blockIdx.x < sharers ? all * (blockIdx.x + 1) / sharers : 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.span = span;
-    long long ahead_w = begin, ahead_t = begin;
-    auto segment = [&](long long& ahead, Segment& f) {
-        if (ahead >= end) return false;
-        const int tile = (int)(ahead / span), in = (int)(ahead - tile * span), entry = in / steps, first = in - entry * steps;
-        f = {entry, tile, first, (int)min((long long)steps, first + end - ahead)};
-        ahead += f.end - first;
+    struct Cursor {
+        int left, tile, entry, step;         // steps left to the CTA; the next one
+    };
+    const int tile0 = (int)(begin / span), in0 = (int)(begin - (long long)tile0 * span), entry0 = in0 / steps;
+    const Cursor start{(int)(end - begin), tile0, entry0, in0 - entry0 * steps};
+    Cursor ahead_w = start, ahead_t = start;
+    auto segment = [&](Cursor& c, Segment& f) {
+        if (c.left == 0) return false;
+        const int n = min(steps - c.step, c.left);
+        f = {c.entry, c.tile, c.step, c.step + n, chosen.first[c.entry], chosen.pairs[c.entry], 0, chosen.pairs[c.entry]};
+        c.left -= n;
+        c.step += n;
+        if (c.step == steps) {
+            c.step = 0;
+            if (++c.entry == chosen.count) c.entry = 0, ++c.tile;
+        }
         return true;
     };
     auto next_w = [&](Segment& f) { return segment(ahead_w, f); };
@@ -625,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const Routed a, i
         __syncthreads();
     };
     auto run = [&](auto& tokens) {
-        long long at = begin;
+        Cursor at = start;
         int open = -1;
         for (Segment f; segment(at, f);) {
             if (open >= 0 && f.tile != open) finish(open);
