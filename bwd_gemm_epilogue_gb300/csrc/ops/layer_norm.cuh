@@ -169,7 +169,8 @@ __device__ __forceinline__ void group_sync(int group, int lanes) {
 constexpr int kRed = 24;
 
 
-// Rows off 16-byte boundaries (odd widths, strides, bases), element by element: thread t of a
+// Rows off 16-byte boundaries, element by element (those that lie differently in the call's tensors,
+// and those that shifted packs do not pay for): thread t of a
 // row's THREADS has columns t + i * THREADS, i < kCols, whose offsets are constants; kCols
 // loads a thread keep enough bytes in flight, and a warp still reads 64 or 128 bytes in a row.
 constexpr int kCols = 16;
