@@ -588,6 +588,10 @@ def swiglu_moe_routed_fwd(x, Wr, W1, W2, top_k: int, renormalize: bool = True, r
     """A whole MoE layer for up to 64 tokens, routed on the device: returns (y [T,Dout] bf16,
     ids [T,top_k] int32, gates [T,top_k] fp32).  Wr [E,D] bf16 or fp32; residual [T,Dout] is
     added to y; renormalize: the chosen gates sum to one."""
+    if y is None and ids is None and gates is None and workspace is None:
+        done = _short().moe_routed_fwd(x, Wr, W1, W2, top_k, renormalize, residual)
+        if done is not None:
+            return done if done.__class__ is tuple else _check(done, "swiglu_moe_routed_fwd")
     if x.dim() != 2 or W1.dim() != 3 or W2.dim() != 3:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, W1 {tuple(W1.shape)}, W2 {tuple(W2.shape)}")
     T, D = x.shape
@@ -618,8 +622,21 @@ _dtype_of = operator.attrgetter("dtype")
 
 
 # The calls below are short on the device (a few microseconds for a decode step's tokens), so
-# their checks compare first and explain (in _expect) only on a mismatch, and the stream comes
-# from torch's raw accessor.
+# the usual ones, every output new, are made by a compiled module (csrc/ops/short_calls.cpp), which
+# returns None for any other and for anything unexpected.  Here the checks compare first and
+# explain (in _expect) only on a mismatch, and the stream comes from torch's raw accessor.
+_short_calls = None
+
+
+def _short():
+    global _short_calls
+    if _short_calls is None:
+        lib()                              # says what to do where it has not been built
+        from . import _short_calls as module
+        _short_calls = module
+    return _short_calls
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
@@ -709,6 +726,10 @@ def swiglu_mlp_layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, resid
     """Layer norm of x (+ residual); returns (y, s, mean, rstd): s is x + residual, or x itself
     without a residual; mean, rstd [M] fp32 are what the backward takes.  x, residual, y, s
     [M, D] bf16, fp16 or fp32, rows at any stride; gamma, beta [D] of x's type or fp32."""
+    if y is None and s is None and mean is None and rstd is None:
+        done = _short().layer_norm_fwd(x, gamma, beta, eps, residual)
+        if done is not None:
+            return done if done.__class__ is tuple else _check(done, "swiglu_mlp_layer_norm_fwd")
     if x.dim() != 2:
         raise ValueError(f"x: shape {tuple(x.shape)}, expected two dimensions")
     shape, dtype, device = x.shape, x.dtype, x.device
@@ -742,6 +763,10 @@ def swiglu_mlp_layer_norm_bwd(dy, s, gamma, mean, rstd, dskip=None, dx=None, dga
     input; dskip: a gradient added to dx (the residual stream's).  gamma None (= 1): dgamma
     and dbeta have the type of the dbeta passed in, or s's.  param_grads False: neither is
     computed and both are None."""
+    if dx is None and dgamma is None and dbeta is None and workspace is None and param_grads:
+        done = _short().layer_norm_bwd(dy, s, gamma, mean, rstd, dskip)
+        if done is not None:
+            return done if done.__class__ is tuple else _check(done, "swiglu_mlp_layer_norm_bwd")
     if s.dim() != 2:
         raise ValueError(f"s: shape {tuple(s.shape)}, expected two dimensions")
     shape, dtype, device = s.shape, s.dtype, s.device
@@ -831,6 +856,10 @@ def _grad_lists(tensors, name: str):
 def _clip_call(grads, max_norm, eps, out, norm, workspace):
     if not grads:
         raise ValueError("grads: empty")
+    if norm is None and workspace is None:
+        done = _short().clip_grads(grads, out, max_norm, eps)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_mlp_clip_grads")
     n = len(grads)
     device, types, counts, ptrs = _grad_lists(grads, "grads")
     try:

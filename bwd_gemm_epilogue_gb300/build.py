@@ -1,8 +1,9 @@
 """Compile the CUDA library (``libswiglu_mlp.so``) in-tree for sm_103a with nvcc.
 
 One translation unit per file of ``csrc/*.cu`` and ``csrc/ops/*.cu``, compiled in parallel and linked
-into one shared library with the CUDA runtime linked statically.  Rebuilds only
-when a source or header is newer than the library.
+into one shared library with the CUDA runtime linked statically; beside it a Python module
+(``_short_calls.so``, from ``csrc/ops/short_calls.cpp`` with g++ and torch's headers) that makes the
+usual calls of the short operators.  Rebuilds only when a source or header is newer than the library.
 """
 from __future__ import annotations
 
@@ -11,12 +12,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libswiglu_mlp.so")
+MODULE = os.path.join(HERE, "_short_calls.so")
 OBJDIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -30,11 +33,32 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MODULE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
     deps = glob.glob(os.path.join(CSRC, "*.*")) + glob.glob(os.path.join(CSRC, "ops", "*.*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _compile_module(cuda_home: str) -> str:
+    """The object of the Python module, against the torch that imports it."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OBJDIR, "short_calls.o")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    f"-I{INCLUDE}", f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+                    f"-I{os.path.join(cuda_home, 'include')}", f"-I{sysconfig.get_paths()['include']}", "-c",
+                    os.path.join(CSRC, "ops", "short_calls.cpp"), "-o", obj], check=True)
+    return obj
+
+
+def _link_module(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MODULE + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:" + os.path.basename(LIB), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+                    "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(tmp, MODULE)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -52,11 +76,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         subprocess.run(cmd, check=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        module = ex.submit(_compile_module, os.path.dirname(os.path.dirname(os.path.realpath(nvcc))))
         objs = list(ex.map(compile_one, srcs))
+        module_obj = module.result()
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static"], check=True)
     os.replace(tmp, LIB)
+    _link_module(module_obj)
     return LIB
 
 
