@@ -131,7 +131,7 @@ __device__ __forceinline__ void load_staged(F2* o, uint32_t p, int k, int width)
 // One value of gamma or beta.
 template <class T>
 __device__ __forceinline__ float param(const void* p, int gf32, int col, float none, T*) {
-    return p == nullptr ? none : gf32 ? static_cast<const float*>(p)[col] : to_f32(static_cast<const T*>(p)[col]);
+    return p == nullptr ? none : gf32 && sizeof(T) != 4 ? static_cast<const float*>(p)[col] : to_f32(static_cast<const T*>(p)[col]);
 }
 
 // Whether pack k = q * lanes + lane is the row's, which ends at element `end` of its packs: the

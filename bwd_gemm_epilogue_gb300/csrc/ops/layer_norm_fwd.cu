@@ -213,8 +213,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) layer_norm_fwd_kernel(const Nor
     } while (EDGE && row < a.M);
 }
 
-// Bound by instructions, 53 a column: 4099 x 1021 fp32 9.5 us, 3.5 TB/s; 40000 x 257 bf16 22.6 us, 1.8 TB/s.
-template <class T, bool RES, int THREADS>
+// Bound by instructions: 4099 x 1021 fp32 9.3 us, 3.6 TB/s (with twice the columns a thread, half of them
+// past the row, 11.5); 40000 x 257 bf16 22.3 us, 1.8 TB/s.
+template <class T, bool RES, int THREADS, int COLS>
 __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS, THREADS > 128 ? 2 : 8)
     layer_norm_fwd_narrow_kernel(const NormFwd a) {
     __shared__ __align__(16) float red[2 * kRed];
@@ -227,34 +228,34 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS, THREADS > 128 ?
     if (row >= a.M) return;
     const T* x = static_cast<const T*>(a.x) + row * a.ldx + t;
     const T* r = static_cast<const T*>(a.r) + row * a.ldr + t;
-    float v[kCols];
+    float v[COLS];
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
+    for (int i = 0; i < COLS; ++i) {
         v[i] = 0.f;
         if (t + i * THREADS < D) v[i] = to_f32(x[i * THREADS]);
     }
     if (RES) {
         T* s = static_cast<T*>(a.s) + row * a.lds + t;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i)
+        for (int i = 0; i < COLS; ++i)
             if (t + i * THREADS < D) v[i] += to_f32(r[i * THREADS]);
 #pragma unroll
-        for (int i = 0; i < kCols; ++i)
+        for (int i = 0; i < COLS; ++i)
             if (t + i * THREADS < D) s[i * THREADS] = from_f32<T>(v[i]);
     }
     float sum = 0.f, sq = 0.f;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) sum += v[i];
+    for (int i = 0; i < COLS; ++i) sum += v[i];
     const float mean = row_sum(sum, 0, THREADS, red, 0) / (float)D;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
+    for (int i = 0; i < COLS; ++i) {
         v[i] -= mean;
         if (t + i * THREADS < D) sq += v[i] * v[i];
     }
     const float rstd = __frsqrt_rn(row_sum(sq, 0, THREADS, red, 1) / (float)D + a.eps);
     T* y = static_cast<T*>(a.y) + row * a.ldy + t;
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) {
+    for (int i = 0; i < COLS; ++i) {
         if (t + i * THREADS < D) {
             const float g = param(a.gamma, a.gf32, t + i * THREADS, 1.f, (T*)nullptr);
             const float b = param(a.beta, a.gf32, t + i * THREADS, 0.f, (T*)nullptr);
@@ -362,12 +363,16 @@ struct LaunchFwd {
         if (lie == kEdge) return a.r ? go<T, NV, true, true>() : go<T, NV, false, true>();
         return a.r ? go<T, NV, true, false>() : go<T, NV, false, false>();
     }
-    template <class T, int THREADS>
+    template <class T, int THREADS, int COLS>
     cudaError_t narrow() const {
         constexpr int rows = THREADS == 32 ? 4 : 1;
-        auto kern = a.r ? layer_norm_fwd_narrow_kernel<T, true, THREADS> : layer_norm_fwd_narrow_kernel<T, false, THREADS>;
+        auto kern = a.r ? layer_norm_fwd_narrow_kernel<T, true, THREADS, COLS> : layer_norm_fwd_narrow_kernel<T, false, THREADS, COLS>;
         kern<<<(unsigned)((a.M + rows - 1) / rows), THREADS * rows, 0, s>>>(a);
         return cudaGetLastError();
+    }
+    template <class T, int THREADS>
+    cudaError_t narrow() const {           // half as many columns a thread where they are enough
+        return a.D <= THREADS * kCols / 2 ? narrow<T, THREADS, kCols / 2>() : narrow<T, THREADS, kCols>();
     }
     template <class T>
     cudaError_t run() const {
