@@ -502,16 +502,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     for (int s = 1; s <= kWarps && (KEPT || s * chosen.most <= kRows); s *= 2) {
         const int per = kWarps / s;
         if (KEPT) {
-            // The smallest split whose rounds, at about 6.8 KB/us that a warp's copies in flight
-            // bring, take no longer than the units at the HBM rate (in units of a unit's 32 D bytes)
-            const float rounds = (float)((units + ctas * per - 1) / (ctas * per)) / (float)s;
-            if (rounds < 0.95f * least) least = rounds, split = s;
-            if (rounds <= 1.1e-3f * (float)units) break;
+            // In units of a warp's time for a unit of 32 D bytes, at the 6.8 KB/us its copies in flight
+            // bring: all full rounds at the HBM rate, the last, partial one at that or at a warp's
+            // (4 tokens, 30 of 64 experts of 2048 x 1408: split 1 99.5 us, 2 94.6; one token, 8 of
+            // them: 41.8, 47.0), and 0.5 us a round for adding the k groups' sums.  (With the
+            // compiler's exact divisions, finding this out took 1.2 us.)
+            const float warps = (float)(ctas * kWarps), hbm = 1.015e-3f * (float)units, inv = __fdividef(1.f, (float)s);
+            const float rounds = __fdividef((float)units * (float)s, warps), full = floorf(rounds);
+            // hbm / rounds: a round of all warps at the HBM rate
+            const float each = 1.015e-3f * warps * inv, part = rounds - full;
+            const float cost = each * full + (part > 0.f ? fmaxf(inv, each * part) : 0.f) +
+                               (s > 1 ? __fdividef(106.f * (full + 1.f), (float)a.D) : 0.f);
+            if (cost < least) least = cost, split = s;
+            if (rounds <= 1.f && hbm * (float)s >= 1.f) break;             // one round, at the HBM rate
         } else {
             // the split whose last round of a CTA's units wastes least (a segment's end costs
             // about a chunk), among those whose chunk of tokens fits
-            const float mine = (float)units / (float)ctas;
-            const float cost = ceilf(mine / (float)per) / (float)s * (1.f + 2.f * (float)s / (float)steps);
+            const float mine = __fdividef((float)units * (float)s, (float)(ctas * kWarps));
+            const float cost = ceilf(mine) * (__fdividef(1.f, (float)s) + __fdividef(2.f, (float)steps));
             if (cost < least) least = cost, split = s;
         }
     }
