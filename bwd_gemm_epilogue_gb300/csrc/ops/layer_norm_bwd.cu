@@ -248,15 +248,27 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
     __syncthreads();
     auto place = [&](int c) { return sizeof(T) == 4 ? c : (c & 4 ? half : 0) + (c >> 3) * 4 + (c & 3); };
     const int first = EDGE ? into_pack<T>(a.s, (int64_t)blockIdx.x * rows, a.lds) : 0;
-    for (int c = threadIdx.x; c < D; c += blockDim.x) {
-        const float* p = acc + place(c);
-        float g = 0.f, b = 0.f;
-        for (int w = 0; w < rows; ++w, p += 2 * width) {
-            if (EDGE) p = acc + w * 2 * width + place(c + ((first + w * (int)(a.lds & (V - 1))) & (V - 1)));
-            g += p[0], b += p[width];
+    constexpr int kAtOnce = 4;             // columns a thread adds at a time
+    for (int c0 = threadIdx.x; c0 < D; c0 += kAtOnce * blockDim.x) {
+        float g[kAtOnce], b[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) g[j] = b[j] = 0.f;
+        for (int w = 0; w < rows; ++w) {
+            const float* p = acc + w * 2 * width;
+            const int at = EDGE ? (first + w * (int)(a.lds & (V - 1))) & (V - 1) : 0;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int c = c0 + j * blockDim.x;
+                if (c < D) g[j] += p[place(c + at)], b[j] += p[width + place(c + at)];
+            }
         }
-        if (a.pg) a.pg[(int64_t)blockIdx.x * D + c] = g;
-        if (a.pb) a.pb[(int64_t)blockIdx.x * D + c] = b;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int c = c0 + j * blockDim.x;
+            if (c >= D) continue;
+            if (a.pg) a.pg[(int64_t)blockIdx.x * D + c] = g[j];
+            if (a.pb) a.pb[(int64_t)blockIdx.x * D + c] = b[j];
+        }
     }
 }
 
