@@ -500,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const Routed a) {
     int split = 1;
     float least = INFINITY;
     for (int s = 1; s <= kWarps && (KEPT || s * chosen.most <= kRows); s *= 2) {
-        const int per = kWarps / s;
         if (KEPT) {
             // In units of a warp's time for a unit of 32 D bytes, at the 6.8 KB/us its copies in flight
             // bring: all full rounds at the HBM rate, the last, partial one at that or at a warp's
