@@ -139,17 +139,20 @@ constexpr int kRouteWarps = 8;
 // l = x Wr^T, fp32 products and sums; p = softmax(l); the top k, ties to the lowest index.  Bound by
 // latencies (5.5 us alone for one token of 64 experts, of which about 2.5 are the launch).
 // One cluster per token; CTA rank c computes the logits of experts c * kRouteWarps + warp,
-// + cluster size * kRouteWarps, ...; the first CTA's first warp chooses.
+// + cluster size * kRouteWarps, ...; the first CTA's first warp chooses.  A CTA may write another's
+// shared memory only once that one is known to run: the cluster's barrier, at which all arrive first
+// and wait after their first logit, which hides it.
 template <class W>
 __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Routed a) {
     __shared__ float logits[kMaxExperts];
     cudaTriggerProgrammaticLaunchCompletion();
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();              // this CTA runs
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
     const int t = blockIdx.x / ctas, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* all = cluster.map_shared_rank(logits, 0);
     const __nv_bfloat16* x = a.x + (int64_t)t * a.D;
-    for (int e = rank * kRouteWarps + warp; e < a.E; e += ctas * kRouteWarps) {
+    auto logit = [&](int e) {
         const W* w = static_cast<const W*>(a.Wr) + (int64_t)e * a.D;
         float s = 0.f;
 #pragma unroll 4
@@ -162,7 +165,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    };
+    int e = rank * kRouteWarps + warp;
+    float s = e < a.E ? logit(e) : 0.f;
+    cluster.barrier_wait();                // every CTA runs: rank 0's shared memory may be written
+    while (e < a.E) {
         if (lane == 0) all[e] = s;
+        e += ctas * kRouteWarps;
+        if (e < a.E) s = logit(e);
     }
     cluster.sync();
     if (rank != 0 || warp != 0) return;
