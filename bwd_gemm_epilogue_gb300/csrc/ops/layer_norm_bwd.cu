@@ -113,8 +113,9 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int group, int lanes, float
 // this CTA's partial planes.  A row is read from the ring twice, before and after the
 // reduction, which costs less than keeping xh and g beside the column sums.  (With one row
 // ahead in registers instead of the ring it took 92 us of 11136 x 3584 bf16.)
-// xh = s * rstd - mean * rstd, and
-// dx = g * rstd + s * A + B with A = -c2 * rstd^2, B = c2 * mean * rstd^2 - c1 * rstd.
+// xh = (s - mean) * rstd, whose difference loses nothing however far the mean is from 0 (a product
+// -mean * rstd rounded on its own would put |mean| * rstd * 2^-24 into every xh of the row), and
+// dx = g * rstd + xh * A + B with A = -c2 * rstd, B = -c1 * rstd.
 // Shared memory: red [groups][2][kRed] pairs, gamma (whole packs, fp32), then the rows in
 // flight, and after them the groups' column sums in their place.
 template <class T, int NV, bool SKIP, bool EDGE>
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
                 }
             }
         }
-        const F2 rs2 = f2(rs), shift = f2(-mu * rs);
+        const F2 rs2 = f2(rs), centre = f2(-mu);
         F2 c1 = f2(0.f), c2 = f2(0.f);
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
                 unpack16<T>(s.get(stage, q), xs);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
-                    const F2 xh = fma(xs[i], rs2, shift), g = d[i] * w[i];
+                    const F2 xh = (xs[i] + centre) * rs2, g = d[i] * w[i];
                     dg[q * P + i] = fma(d[i], xh, dg[q * P + i]);
                     db[q * P + i] = db[q * P + i] + d[i];
                     c1 = c1 + g;
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
         float2 c = row_sum2(make_float2(p1.x + p1.y, p2.x + p2.y), group, lanes, red, stage);
         c.x *= inv * rs;
         c.y *= inv * rs;
-        const F2 A = f2(-c.y * rs), B = f2(c.y * mu * rs - c.x);
+        const F2 A = f2(-c.y), B = f2(-c.x);
         T* o = static_cast<T*>(a.dx) + row * a.lddx - m;
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kBwdThreads) layer_norm_bwd_kernel(const NormB
                 unpack16<T>(dy.get(stage, q), d);
                 unpack16<T>(s.get(stage, q), xs);
 #pragma unroll
-                for (int i = 0; i < P; ++i) w[i] = fma(d[i] * w[i], rs2, fma(xs[i], A, B));
+                for (int i = 0; i < P; ++i) w[i] = fma(d[i] * w[i], rs2, fma((xs[i] + centre) * rs2, A, B));
                 if (SKIP) {
                     unpack16<T>(skip.get(stage, q), d);
 #pragma unroll
