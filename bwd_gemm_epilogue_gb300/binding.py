@@ -725,7 +725,8 @@ def swiglu_mlp_layer_norm_fwd(x, gamma=None, beta=None, eps: float = 1e-5, resid
                               rstd=None):
     """Layer norm of x (+ residual); returns (y, s, mean, rstd): s is x + residual, or x itself
     without a residual; mean, rstd [M] fp32 are what the backward takes.  x, residual, y, s
-    [M, D] bf16, fp16 or fp32, rows at any stride; gamma, beta [D] of x's type or fp32."""
+    [M, D] bf16, fp16 or fp32, rows at any stride; gamma, beta [D] of x's type or fp32.  y and s
+    may each be x or residual (in place), but not both the same."""
     if y is None and s is None and mean is None and rstd is None:
         done = _short().layer_norm_fwd(x, gamma, beta, eps, residual)
         if done is not None:
@@ -762,7 +763,7 @@ def swiglu_mlp_layer_norm_bwd(dy, s, gamma, mean, rstd, dskip=None, dx=None, dga
     """Backward of the layer norm; returns (dx, dgamma, dbeta).  s: the forward's normalised
     input; dskip: a gradient added to dx (the residual stream's).  gamma None (= 1): dgamma
     and dbeta have the type of the dbeta passed in, or s's.  param_grads False: neither is
-    computed and both are None."""
+    computed and both are None.  dx may be dy, s or dskip (in place)."""
     if dx is None and dgamma is None and dbeta is None and workspace is None and param_grads:
         done = _short().layer_norm_bwd(dy, s, gamma, mean, rstd, dskip)
         if done is not None:

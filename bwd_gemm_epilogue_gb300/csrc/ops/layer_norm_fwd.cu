@@ -295,7 +295,6 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_wide_kernel(const 
             load((int)c, v);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) sum += v[j];
-            if (r) store_pack<T, VEC>(static_cast<T*>(a.s) + row * a.lds + c, v);
         }
         const float mean = row_sum(sum, 0, blockDim.x, red, 0) * inv;
         for (int64_t c = first; c < a.D; c += hop) {
@@ -307,6 +306,8 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_fwd_wide_kernel(const 
         for (int64_t c = first; c < a.D; c += hop) {
             float g[VEC], b[VEC];
             load((int)c, v);
+            // not before the last pass over x and the residual, in whose place s may be
+            if (r) store_pack<T, VEC>(static_cast<T*>(a.s) + row * a.lds + c, v);
             load_param<T, VEC>(g, a.gamma, a.gf32, (int)c, 1.f);
             load_param<T, VEC>(b, a.beta, a.gf32, (int)c, 0.f);
 #pragma unroll
@@ -408,6 +409,7 @@ swiglu_status swiglu_mlp_layer_norm_fwd(const void* x, int64_t ldx, const void* 
     if (!x || !y) return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: a required pointer is null");
     if ((residual == nullptr) != (s == nullptr) || (mean == nullptr) != (rstd == nullptr))
         return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: residual and s, and mean and rstd, go together");
+    if (y == s) return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: y and s are the same");
     if (ldx < D || ldy < D || (residual && (ldr < D || lds < D)))
         return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: a row stride is smaller than the width");
     const size_t n = type_bytes(type), np = type_bytes(param_type);
