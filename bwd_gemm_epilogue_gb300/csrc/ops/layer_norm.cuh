@@ -168,6 +168,23 @@ __device__ __forceinline__ void group_sync(int group, int lanes) {
 // has passed.  The entries past the group's warps hold zeros.
 constexpr int kRed = 24;
 
+// A thread's sum over a row wider than the registers hold, up to half a million elements: runs of a
+// pack or of kRun single elements in fp32, whose sums are added with the rounding error of each
+// addition kept (Knuth's two-sum), so it is off by one run's roundings however long the row.  (A plain
+// running sum of 2^24 columns of 1.1 put the mean off by 1e-4, and with it every difference from it.)
+constexpr int kRun = 32;
+struct LongSum {
+    float sum = 0.f, lost = 0.f;
+    __device__ __forceinline__ void add(float v) {
+        const float t = sum + v, z = t - sum;
+        lost += (sum - (t - z)) + (v - z);
+        sum = t;
+    }
+    __device__ __forceinline__ float value() const {       // infinite sums have no error to speak of
+        const float v = sum + lost;
+        return v == v ? v : sum;
+    }
+};
 
 // Rows off 16-byte boundaries, element by element (those that lie differently in the call's tensors,
 // and those that shifted packs do not pay for): thread t of a

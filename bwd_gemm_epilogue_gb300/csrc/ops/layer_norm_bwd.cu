@@ -379,8 +379,8 @@ __global__ void __launch_bounds__(THREADS < 128 ? 128 : THREADS, THREADS > 128 ?
 
 // Rows wider than the registers hold, in two passes: the two sums of every row, then dx
 // and the column sums of a block of columns over a range of rows.  Bound by HBM, which reads dy and
-// s twice: 3000 x 16384 bf16 with the residual stream's gradient 138 us, 590 MB at 4.3 TB/s; single
-// elements, for rows off 16-byte boundaries, 3000 x 14001: 227 us.
+// s twice: 3000 x 16384 bf16 with the residual stream's gradient 137 us, 590 MB at 4.3 TB/s; single
+// elements, for rows off 16-byte boundaries, 3000 x 14001: 240 us.
 template <class T, int VEC>
 __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_wide_sums_kernel(const NormBwd a, float2* sums) {
     __shared__ __align__(16) float2 red[2 * kRed];
@@ -391,20 +391,28 @@ __global__ void __launch_bounds__(kMaxThreads) layer_norm_bwd_wide_sums_kernel(c
         const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
         const T* s = static_cast<const T*>(a.s) + row * a.lds;
         const float mean = a.mean[row], rstd = a.rstd[row];
-        float2 c = make_float2(0.f, 0.f);
-        for (int64_t col = threadIdx.x * VEC; col < a.D; col += blockDim.x * VEC) {
-            float w[VEC], d[VEC], xs[VEC];
-            load_pack<T, VEC>(dy + col).unpack(d);
-            load_pack<T, VEC>(s + col).unpack(xs);
-            load_param<T, VEC>(w, a.gamma, a.gf32, (int)col, 1.f);
+        LongSum sum_g, sum_gx;
+        constexpr int run = VEC > 1 ? 1 : kRun;
+        const int64_t hop = blockDim.x * VEC;
+        for (int64_t col = threadIdx.x * VEC; col < a.D;) {
+            float2 part = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int i = 0; i < run && col < a.D; ++i, col += hop) {
+                float w[VEC], d[VEC], xs[VEC];
+                load_pack<T, VEC>(dy + col).unpack(d);
+                load_pack<T, VEC>(s + col).unpack(xs);
+                load_param<T, VEC>(w, a.gamma, a.gf32, (int)col, 1.f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float g = d[j] * w[j];
-                c.x += g;
-                c.y += g * ((xs[j] - mean) * rstd);
+                for (int j = 0; j < VEC; ++j) {
+                    const float g = d[j] * w[j];
+                    part.x += g;
+                    part.y += g * ((xs[j] - mean) * rstd);
+                }
             }
+            sum_g.add(part.x);
+            sum_gx.add(part.y);
         }
-        c = row_sum2(c, 0, blockDim.x, red, buf);
+        const float2 c = row_sum2(make_float2(sum_g.value(), sum_gx.value()), 0, blockDim.x, red, buf);
         if (threadIdx.x == 0) sums[row] = make_float2(c.x / (float)a.D, c.y / (float)a.D);
     }
 }

@@ -30,8 +30,11 @@ typedef enum { SWIGLU_BF16 = 0, SWIGLU_FP16 = 1, SWIGLU_FP32 = 2 } swiglu_dtype;
  *                              together: both NULL or neither.
  *   gamma, beta [D]            `param_type`: `type` or SWIGLU_FP32; NULL = 1 and 0
  *   mean, rstd [M] fp32        saved for the backward; both may be NULL
- * The statistics and y are taken from the unrounded fp32 sum, in two passes over the row
- * held in registers; each output is rounded once.  1 <= D < 2^28, 0 <= M < 2^31, eps >= 0.
+ * The statistics and y are taken from the unrounded fp32 sum, the deviations in a pass of
+ * their own about the mean; rows are held in registers for it, or, past 64 KB (where tensors
+ * lie differently, 8192 columns), read three times.  A row's sums are off by at most 53 x 2^-24
+ * of the sum of magnitudes at every width; each output is rounded once.
+ * 1 <= D < 2^28, 0 <= M < 2^31, eps >= 0.
  * In place: s and y may each be x or residual itself (the same pointer and row stride; then
  * that input is overwritten), but not both the same.  No other outputs may overlap inputs or
  * one another.
@@ -57,8 +60,9 @@ size_t swiglu_mlp_layer_norm_bwd_workspace_size(int64_t M, int64_t D);
  *   mean, rstd [M] fp32       from the forward
  *   gamma, dgamma, dbeta [D]  `param_type`; gamma NULL = 1; dgamma and dbeta may each be
  *                             NULL (not computed)
- * dgamma and dbeta are summed in fp32 in an order that depends on M, D and the alignment
- * only: the same call returns the same bits on every run.  M = 0 zeroes them.
+ * dgamma and dbeta are summed in fp32 in an order that depends on M, D, the type, dskip's
+ * presence and the alignment only: the same call returns the same bits on every run.  M = 0
+ * zeroes them.
  * In place: dx may be dy, s or dskip itself (the same pointer and row stride).
  */
 swiglu_status swiglu_mlp_layer_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const void* gamma,
