@@ -73,31 +73,46 @@ __device__ __forceinline__ void load_block(uint4* b, const T* q, int from, int p
     }
 }
 
-// Sum of a block's squares, 16 to each of two sums.
-template <class T, class Acc>
-__device__ __forceinline__ Acc block_squares(const uint4* b) {
+// Sum of the squares of a block's elements times `scale`, 16 to each of two sums.
+template <class T, bool SCALED>
+__device__ __forceinline__ float block_squares(const uint4* b, float scale) {
     constexpr int V = 16 / sizeof(T);
-    Acc s0 = 0, s1 = 0;
+    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int j = 0; j < kBlock; ++j) {
         F2 v[V / 2];
         unpack16<T>(b[j], v);
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-            const float2 f = split(v[i]);
-            s0 += (Acc)f.x * (Acc)f.x;
-            s1 += (Acc)f.y * (Acc)f.y;
+            const float2 f = split(SCALED ? v[i] * f2(scale) : v[i]);
+            s0 += f.x * f.x;
+            s1 += f.y * f.y;
         }
     }
     return s0 + s1;
 }
 
-// In fp32, and once more in fp64 where that overflowed (finite elements above 1.8e19 do).
+// It is taken in fp32 as the elements are, and once more of their scaled values where that overflowed
+// (finite elements above 1.8e19 do) or came out below kLeastSquares (elements below 1e-18 can): fp32
+// squares under 1.2e-38 are off by up to 2^-150 each, 32 of them by 2e-44, which is 2^-28 of that least
+// sum.  Times 2^100 (2^-100) every element that such a block can have, down to 2^-149 (up to 2^128),
+// has a square in the normal range or one that does not count beside the block's largest.
+constexpr float kLeastSquares = 1e-35f;
+
 template <class T>
-__device__ __noinline__ double block_squares_f64(const T* q, int from, int packs) {
+__device__ __noinline__ double block_squares_scaled(const T* q, int from, int packs, bool up) {
     uint4 b[kBlock];
     load_block(b, q, from, packs);
-    return block_squares<T, double>(b);
+    const float f = block_squares<T, true>(b, up ? 0x1p100f : 0x1p-100f);
+    return (double)f * (up ? 0x1p-200 : 0x1p200);
+}
+// Whether a block has an element other than 0 and -0, which whole gradients can consist of.
+template <class T>
+__device__ __forceinline__ bool any_element(const uint4* b) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) any |= b[j].x | b[j].y | b[j].z | b[j].w;
+    return (any & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) != 0;
 }
 template <class T>
 __device__ __forceinline__ double squares(const T* p, int64_t n) {
@@ -118,8 +133,9 @@ __device__ __forceinline__ double squares(const T* p, int64_t n) {
     for (int i = threadIdx.x; i < packs; i += kBlock * kThreads) {
         uint4 b[kBlock];
         load_block(b, q, i, packs);
-        const float f = block_squares<T, float>(b);
-        s += isinf(f) ? block_squares_f64(q, i, packs) : (double)f;
+        const float f = block_squares<T, false>(b, 1.f);
+        const bool small = f < kLeastSquares && any_element<T>(b);
+        s += small || isinf(f) ? block_squares_scaled(q, i, packs, small) : (double)f;
     }
     return s;
 }

@@ -84,12 +84,13 @@ size_t swiglu_mlp_clip_grads_workspace_size(int64_t n);
  *                            place); out NULL computes the norm alone.  The arrays are
  *                            read before the call returns.
  *   norm                     device fp32, may be NULL when out is given
- * Squares are fp32 products summed in fp32 16 at a time, then in fp64 (where fp32 squares
- * overflow they are summed again in fp64); squares below fp32's range (elements under
- * 1e-23) add nothing.  The sums' order depends on the counts and
- * types only: the same call returns the same bits on every run.  A norm that is infinite
- * or NaN gives what the formulas give (factor 0, so finite elements become 0 and infinite
- * ones NaN; or NaN everywhere): read `norm` before using the result.  n = 0: norm 0.
+ * Squares are fp32 products summed in fp32 16 at a time, then in fp64; where fp32 squares
+ * overflow or fall below its normal range they are summed again of scaled elements, so the
+ * norm is as precise for the largest and the smallest elements of a type as for others.
+ * The sums' order depends on the counts, types and alignment only: the same call returns the
+ * same bits on every run.  A norm that is infinite or NaN gives what the formulas give
+ * (factor 0, so finite elements become 0 and infinite ones NaN; or NaN everywhere): read
+ * `norm` before using the result.  n = 0: norm 0.
  */
 swiglu_status swiglu_mlp_clip_grads(const void* const* in, void* const* out, const int64_t* counts, const int* types,
                                     int64_t n, float max_norm, float eps, float* norm, void* workspace,
