@@ -4,12 +4,12 @@
 // add those sums in the same order, so every one of them holds the same norm and no CTA
 // waits for another.  The tensors' table travels in the kernels' parameters (no copy, no
 // allocation, fit for stream capture).  All tensors, in granules of kGranule bytes, are
-// divided evenly over the CTAs; a CTA walks its share tensor by tensor with the next 32 KB in
-// flight, and the scaling walks it backwards, so that what the norm read last is still in L2.
+// divided evenly over the CTAs; a CTA walks its share tensor by tensor, 32 KB at a time,
+// and the scaling walks it backwards, so that what the norm read last is still in L2.
 //
 // Bound by HBM: gradients larger than L2 are read twice (the factor needs all of them first) and
 // written once.  Measured, 616.6 M bf16: 570 us, 3.7 GB at 6.5 TB/s of the 6.78 TB/s of a copy.
-// Few and small gradients: two launches and one sum of the norm, 8 us.
+// Few and small gradients: two launches and one sum of the norm, 8.5 us.
 #include "../host.h"
 #include "convert.cuh"
 #include "swiglu_ops.h"
@@ -19,7 +19,11 @@ namespace {
 
 constexpr int kPlanSms = 152;
 constexpr int kThreads = 512;
-constexpr int kCtas = kPlanSms * 3;          // CTAs = fp64 sums of one launch; 3 an SM (4: 568 us, 2: 559, 3: 561 for 616.6 M bf16)
+// CTAs = fp64 sums of one launch, 2 an SM: fewer sums to add and fewer first loads than with more (2, 3
+// and 4 an SM, us: 616.6 M bf16 574, 577, 584; 48 mixed tensors of 19 M elements 25.6, 27.1, 28.6; 51 of
+// up to 0.5 M each 13.9, 17.3, 19.7; but 3 tensors of 0.4 M in all 8.6, 8.4, 8.4, and the norm alone of
+// the first 180, 174).
+constexpr int kCtas = kPlanSms * 2;
 constexpr int kMaxTensors = 768;             // per launch: 22 KB of parameters
 constexpr int kFewTensors = 64;              // a second, 2 KB table for the usual few (shorter launches)
 constexpr int64_t kGranule = 16384;
@@ -156,7 +160,7 @@ __device__ __forceinline__ double cta_sum(double v) {
 }
 
 // Sum of g^2 over this CTA's share: fp32 products and sums of 64 bytes a thread, then fp64.  Bound by
-// HBM (1.23 GB of bf16 in 195 us, 6.3 TB/s); what hides the latency is 48 warps an SM with 64 bytes a
+// HBM (1.23 GB of bf16 in 195 us, 6.3 TB/s); what hides the latency is 32 warps an SM with 64 bytes a
 // thread in flight (two such blocks a thread, at 24 warps: 698 us with the scaling instead of 561).
 template <int N>
 __global__ void __launch_bounds__(kThreads, kCtas / kPlanSms) grad_squares_kernel(const __grid_constant__ ClipTable<N> c, double* sums) {
