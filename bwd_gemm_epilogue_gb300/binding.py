@@ -12,10 +12,12 @@ library raises ``RuntimeError`` (there is no fallback path).
 from __future__ import annotations
 
 import ctypes
+import importlib
 import operator
 import os
 import struct
 import threading
+import warnings
 
 import torch
 
@@ -628,11 +630,24 @@ _dtype_of = operator.attrgetter("dtype")
 _short_calls = None
 
 
+class _NoShortCalls:
+    """In the module's place where it was not built or is another torch's: every call is made below."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _short():
     global _short_calls
     if _short_calls is None:
         lib()                              # says what to do where it has not been built
-        from . import _short_calls as module
+        try:
+            module = importlib.import_module("._short_calls", __package__)
+            if module.torch_version != str(torch.__version__):
+                raise ImportError(f"it was built for torch {module.torch_version}, not {torch.__version__}")
+        except ImportError as e:
+            warnings.warn(f"the short operators' calls go through ctypes: {e}")
+            module = _NoShortCalls()
         _short_calls = module
     return _short_calls
 

@@ -232,4 +232,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_short_calls", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__short_calls() { return PyModule_Create(&module); }
+// torch_version: the torch whose headers this was compiled with, which has to be the one that runs.
+PyMODINIT_FUNC PyInit__short_calls() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", SWIGLU_TORCH) < 0) Py_CLEAR(m);
+    return m;
+}
