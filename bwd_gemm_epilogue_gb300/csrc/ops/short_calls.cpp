@@ -158,6 +158,7 @@ PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
         if (n != 4 || !PyList_Check(args[0]) || !(PyList_Check(args[1]) || args[1] == Py_None)) Py_RETURN_NONE;
         const double max_norm = PyFloat_AsDouble(args[2]), eps = PyFloat_AsDouble(args[3]);
+        if (PyErr_Occurred()) return nullptr;
         const Py_ssize_t count = PyList_GET_SIZE(args[0]);
         const bool write = args[1] != Py_None;
         if (count == 0 || (write && PyList_GET_SIZE(args[1]) != count) || (write && (!(max_norm >= 0.0) || !(eps >= 0.0)))) Py_RETURN_NONE;
@@ -201,7 +202,8 @@ PyObject* moe_routed_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
         int over = 0;
         const int64_t k = PyLong_AsLongLongAndOverflow(args[4], &over);
         const int renorm = PyObject_IsTrue(args[5]);
-        if (!x.ok || !wr.ok || !w1.ok || !w2.ok || !r.ok || over || k <= 0 || renorm < 0 || x.t->dim() != 2 || w2.t->dim() != 3) Py_RETURN_NONE;
+        if (renorm < 0) return nullptr;    // a value without a truth: its own error
+        if (!x.ok || !wr.ok || !w1.ok || !w2.ok || !r.ok || over || k <= 0 || x.t->dim() != 2 || w2.t->dim() != 3) Py_RETURN_NONE;
         const at::Device device = x.t->device();
         const at::ScalarType bf = at::kBFloat16, rtype = wr.t->scalar_type();
         const int64_t T = x.t->size(0), D = x.t->size(1), E = w2.t->size(0), Dout = w2.t->size(1), H = w2.t->size(2);
