@@ -11,6 +11,7 @@
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -86,14 +87,12 @@ int released(const F& f) {
     return f();
 }
 
+// A C++ exception (no memory for an output, say) as the Python exception that torch makes of it.
 template <class F>
 PyObject* guarded(const F& f) {
-    try {
-        return f();
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+    HANDLE_TH_ERRORS
+    return f();
+    END_HANDLE_TH_ERRORS
 }
 
 // (x, gamma, beta, eps, residual) -> (y, s, mean, rstd)
