@@ -486,25 +486,50 @@ def swiglu_mlp_gemm_bf16(A, B, M: int, N: int, K: int, a_mn_major: bool, b_mn_ma
     return C
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """A backward kernel's results (the first n tensors), as functions of all that they were computed
+    from (the rest): to differentiate them again raises, where it would else lose their terms."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the backward kernels are not differentiable: no second derivative passes through them")
+
+
+def _once(outputs, *inputs):
+    """A backward's outputs (None among them), guarded when a graph of it is wanted (create_graph)."""
+    if not torch.is_grad_enabled():
+        return outputs
+    own = [t for t in outputs if t is not None]
+    guarded = iter(_NoSecondDerivative.apply(len(own), *own, *(t for t in inputs if t is not None)))
+    return tuple(None if t is None else next(guarded) for t in outputs)
+
+
 class SwiGLUMLP(torch.autograd.Function):
     """autograd wrapper: forward saves (x, W1, W2, preact) and drops h; backward
     calls swiglu_mlp_bwd.  Leading dimensions of x are flattened.  With residual
-    set it is the block y = x + MLP(x) (the residual entry points)."""
+    set it is the block y = x + MLP(x) (the residual entry points).  Differentiable once."""
 
     @staticmethod
     def forward(ctx, x, W1, W2, residual=False):
         x2 = x.reshape(-1, x.shape[-1]).contiguous()
         preact, y = swiglu_mlp_fwd(x2, W1.contiguous(), W2.contiguous(), residual=residual)
-        ctx.save_for_backward(x2, W1, W2, preact)
+        ctx.save_for_backward(x, W1, W2, preact)
         ctx.residual = residual
         return y.reshape(*x.shape[:-1], y.shape[-1])
 
     @staticmethod
     def backward(ctx, grad_y):
-        x2, W1, W2, preact = ctx.saved_tensors
-        dy = grad_y.reshape(-1, grad_y.shape[-1]).contiguous()
-        dx, dW1, dW2 = swiglu_mlp_bwd(x2, W1.contiguous(), W2.contiguous(), preact, dy, residual=ctx.residual)
-        return dx.reshape(*grad_y.shape[:-1], dx.shape[-1]), dW1, dW2, None
+        x, W1, W2, preact = ctx.saved_tensors
+        with torch.no_grad():
+            x2 = x.reshape(-1, x.shape[-1]).contiguous()
+            dy = grad_y.reshape(-1, grad_y.shape[-1]).contiguous()
+            dx, dW1, dW2 = swiglu_mlp_bwd(x2, W1.contiguous(), W2.contiguous(), preact, dy, residual=ctx.residual)
+            dx = dx.reshape(*grad_y.shape[:-1], dx.shape[-1])
+        return *_once((dx, dW1, dW2), grad_y, x, W1, W2), None
 
 
 def swiglu_mlp(x, W1, W2, residual: bool = False):
@@ -812,30 +837,35 @@ def swiglu_mlp_layer_norm_bwd(dy, s, gamma, mean, rstd, dskip=None, dx=None, dga
 
 class LayerNorm(torch.autograd.Function):
     """autograd wrapper: y without a residual, (y, s) with one; the gradient reaching s past
-    the norm is then added to dx in the backward kernel.  Leading dimensions are flattened."""
+    the norm is then added to dx in the backward kernel.  Leading dimensions are flattened.
+    Differentiable once."""
 
     @staticmethod
     def forward(ctx, x, gamma, beta, eps, residual):
         y, s, mean, rstd = swiglu_mlp_layer_norm_fwd(_flat_rows(x), gamma, beta, eps,
                                                      None if residual is None else _flat_rows(residual))
+        ctx.residual = residual is not None
+        s = s.reshape(x.shape) if ctx.residual else x
         ctx.save_for_backward(s, gamma, mean, rstd)
         ctx.beta_dtype = None if beta is None else beta.dtype
-        ctx.residual = residual is not None
         ctx.set_materialize_grads(False)
-        return (y.reshape(x.shape), s.reshape(x.shape)) if ctx.residual else y.reshape(x.shape)
+        return (y.reshape(x.shape), s) if ctx.residual else y.reshape(x.shape)
 
     @staticmethod
     def backward(ctx, dy, ds=None):
         s, gamma, mean, rstd = ctx.saved_tensors
         if dy is None:
             return ds, None, None, None, ds
-        dbeta = None if ctx.beta_dtype is None else torch.empty(s.shape[1], dtype=ctx.beta_dtype, device=s.device)
-        want = gamma is not None or dbeta is not None
-        dx, dgamma, _ = swiglu_mlp_layer_norm_bwd(_flat_rows(dy), s, gamma, mean, rstd,
-                                                  None if ds is None else _flat_rows(ds), dbeta=dbeta,
-                                                  param_grads=want)
-        dx = dx.reshape(dy.shape)
-        return dx, None if gamma is None else dgamma, dbeta, None, dx if ctx.residual else None
+        with torch.no_grad():
+            rows = _flat_rows(s)
+            dbeta = None if ctx.beta_dtype is None else torch.empty(rows.shape[1], dtype=ctx.beta_dtype, device=s.device)
+            want = gamma is not None or dbeta is not None
+            dx, dgamma, _ = swiglu_mlp_layer_norm_bwd(_flat_rows(dy), rows, gamma, mean, rstd,
+                                                      None if ds is None else _flat_rows(ds), dbeta=dbeta,
+                                                      param_grads=want)
+            dx = dx.reshape(dy.shape)
+        dx, dgamma, dbeta = _once((dx, None if gamma is None else dgamma, dbeta), dy, ds, s, gamma)
+        return dx, dgamma, dbeta, None, dx if ctx.residual else None
 
 
 def _flat_rows(t):
