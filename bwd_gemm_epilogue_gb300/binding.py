@@ -844,18 +844,18 @@ class LayerNorm(torch.autograd.Function):
     def forward(ctx, x, gamma, beta, eps, residual):
         y, s, mean, rstd = swiglu_mlp_layer_norm_fwd(_flat_rows(x), gamma, beta, eps,
                                                      None if residual is None else _flat_rows(residual))
-        ctx.residual = residual is not None
-        s = s.reshape(x.shape) if ctx.residual else x
+        ctx.residual = None if residual is None else residual.shape
+        s = x if residual is None else s.reshape(x.shape)
         ctx.save_for_backward(s, gamma, mean, rstd)
         ctx.beta_dtype = None if beta is None else beta.dtype
         ctx.set_materialize_grads(False)
-        return (y.reshape(x.shape), s) if ctx.residual else y.reshape(x.shape)
+        return y.reshape(x.shape) if residual is None else (y.reshape(x.shape), s)
 
     @staticmethod
     def backward(ctx, dy, ds=None):
         s, gamma, mean, rstd = ctx.saved_tensors
         if dy is None:
-            return ds, None, None, None, ds
+            return ds, None, None, None, _residual_grad(ds, ctx.residual)
         with torch.no_grad():
             rows = _flat_rows(s)
             dbeta = None if ctx.beta_dtype is None else torch.empty(rows.shape[1], dtype=ctx.beta_dtype, device=s.device)
@@ -865,7 +865,16 @@ class LayerNorm(torch.autograd.Function):
                                                       param_grads=want)
             dx = dx.reshape(dy.shape)
         dx, dgamma, dbeta = _once((dx, None if gamma is None else dgamma, dbeta), dy, ds, s, gamma)
-        return dx, dgamma, dbeta, None, dx if ctx.residual else None
+        return dx, dgamma, dbeta, None, _residual_grad(dx, ctx.residual)
+
+
+def _residual_grad(dx, shape):
+    """dx for a residual of `shape`, whose leading dimensions may be others than x's: the same tensor,
+    which autograd copies where it keeps both, or a copy (a view would be kept as it is, and x's
+    gradient and the residual's would share their memory)."""
+    if dx is None or shape is None:
+        return None
+    return dx if dx.shape == shape else dx.reshape(shape).clone()
 
 
 def _flat_rows(t):
