@@ -17,7 +17,8 @@ from . import binding
 
 
 class PreNormMoE:
-    """gamma, beta [D], router [E, D] (fp32 or bf16), W1 [E, 2H, D], W2 [E, D, H] bf16 CUDA tensors."""
+    """gamma, beta [D], router [E, D] (fp32 or bf16), W1 [E, 2H, D], W2 [E, D, H] bf16 CUDA tensors or
+    Parameters; the block has a backward of its own, and autograd sees nothing of it."""
 
     def __init__(self, gamma, beta, router, W1, W2, top_k: int, eps: float = 1e-5):
         E, H2, D = W1.shape
@@ -31,6 +32,7 @@ class PreNormMoE:
         self.grads = None
         self._saved = None
 
+    @torch.no_grad()
     def forward(self, x):
         """x [T, D] bf16 -> y [T, D]; keeps what the backward needs."""
         gamma, beta, router, W1, W2 = self.params
@@ -50,6 +52,7 @@ class PreNormMoE:
         self._saved = (x, xn, mean, rstd, ids, gates, order, counts, xg, preact, out)
         return y
 
+    @torch.no_grad()
     def backward(self, dy):
         """dy [T, D] bf16 -> dx; leaves the parameters' gradients in self.grads."""
         gamma, _, router, W1, W2 = self.params
@@ -68,6 +71,7 @@ class PreNormMoE:
         self.grads = [dgamma, dbeta, drouter, dW1, dW2]
         return dx
 
+    @torch.no_grad()
     def step(self, lr: float, max_norm: float):
         """Clip the gradients in place by their global norm and take a plain descent step;
         returns the norm before clipping (on the device)."""
@@ -76,6 +80,7 @@ class PreNormMoE:
             p.add_(g, alpha=-lr)
         return norm
 
+    @torch.no_grad()
     def decode(self, x):
         """y of forward for up to 64 tokens, nothing kept."""
         gamma, beta, router, W1, W2 = self.params
