@@ -944,7 +944,8 @@ def _clip_call(grads, max_norm, eps, out, norm, workspace):
 def swiglu_mlp_clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, norm=None, workspace=None):
     """Clip gradients by their global norm; returns (norm, clipped gradients).  The result
     goes to `out` (a list like grads), or into grads themselves when out is None.  norm: fp32
-    scalar on the device, of the gradients before clipping (no host synchronisation)."""
+    scalar on the device, of the gradients before clipping (no host synchronisation).  Outputs
+    that overlap, such as one gradient listed twice, are refused."""
     grads = list(grads)
     dst = grads if out is None else list(out)
     return _clip_call(grads, float(max_norm), float(eps), dst, norm, workspace), dst

@@ -10,6 +10,10 @@
 // Bound by HBM: gradients larger than L2 are read twice (the factor needs all of them first) and
 // written once.  Measured, 616.6 M bf16: 570 us, 3.7 GB at 6.5 TB/s of the 6.78 TB/s of a copy.
 // Few and small gradients: two launches and one sum of the norm, 8.5 us.
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "../host.h"
 #include "convert.cuh"
 #include "swiglu_ops.h"
@@ -267,6 +271,31 @@ struct ClipCall {
     cudaStream_t stream;
 };
 
+// Whether an output shares memory with another one, or with an input that is not its own: the scaling's
+// CTAs would race on it.  `outs`: room for the n outputs' ranges.
+struct Range {
+    uintptr_t begin, end;
+};
+bool outputs_overlap(const ClipCall& a, Range* outs) {
+    auto range = [&](const void* p, int64_t i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        return Range{at, at + (uintptr_t)a.counts[i] * (a.types[i] == SWIGLU_FP32 ? 4 : 2)};
+    };
+    Range* last = outs;
+    for (int64_t i = 0; i < a.n; ++i)
+        if (a.counts[i] > 0) *last++ = range(a.out[i], i);
+    std::sort(outs, last, [](const Range& p, const Range& q) { return p.begin < q.begin; });
+    for (Range* r = outs; r + 1 < last; ++r)
+        if (r->end > r[1].begin) return true;
+    for (int64_t i = 0; i < a.n; ++i) {
+        if (a.counts[i] == 0 || a.in[i] == a.out[i]) continue;
+        const Range in = range(a.in[i], i);  // the first output that ends past its begin
+        const Range* r = std::partition_point(outs, last, [&](const Range& p) { return p.end <= in.begin; });
+        if (r != last && r->begin < in.end) return true;
+    }
+    return false;
+}
+
 // Table of tensors base .. base + N - 1; returns its number of granules.
 template <int N>
 uint64_t fill_table(ClipTable<N>& c, const ClipCall& a, int64_t base) {
@@ -364,11 +393,18 @@ swiglu_status swiglu_mlp_clip_grads(const void* const* in, void* const* out, con
         return fail(SWIGLU_ERR_MISALIGNED, "clip_grads: the workspace is not 16-byte aligned, or norm not 4-byte aligned");
     if (workspace_bytes < swiglu_mlp_clip_grads_workspace_size(n))
         return fail(SWIGLU_ERR_WORKSPACE_TOO_SMALL, "clip_grads: workspace smaller than the size query returns");
+    const ClipCall a{in, out, counts, types, n, max_norm, eps, norm, static_cast<double*>(workspace),
+                     static_cast<cudaStream_t>(stream)};
+    if (out) {
+        Range few[kFewTensors];
+        const std::unique_ptr<Range[]> many(n > kFewTensors ? new (std::nothrow) Range[n] : nullptr);
+        if (n > kFewTensors && !many) return fail(SWIGLU_ERR_CUDA, "clip_grads: no host memory for the tensors' ranges");
+        if (outputs_overlap(a, many ? many.get() : few))
+            return fail(SWIGLU_ERR_INVALID_ARG, "clip_grads: an output overlaps another one, or an input that is not its own");
+    }
     int sms;
     swiglu_status rc = device_sms(&sms);
     if (rc != SWIGLU_OK) return rc;
-    const ClipCall a{in, out, counts, types, n, max_norm, eps, norm, static_cast<double*>(workspace),
-                     static_cast<cudaStream_t>(stream)};
     return n <= kFewTensors ? run_clip<kFewTensors>(a) : run_clip<kMaxTensors>(a);
 }
 

@@ -81,8 +81,10 @@ size_t swiglu_mlp_clip_grads_workspace_size(int64_t n);
  *   in, out, counts, types   host arrays of n entries: device pointers (each aligned to
  *                            its element), element counts (0 allowed), swiglu_dtype.
  *                            out_i has in_i's type and count and may be in_i itself (in
- *                            place); out NULL computes the norm alone.  The arrays are
- *                            read before the call returns.
+ *                            place), but share no memory with another entry's tensors
+ *                            (SWIGLU_ERR_INVALID_ARG: one gradient twice in a list would be
+ *                            scaled twice); out NULL computes the norm alone.  The arrays
+ *                            are read before the call returns.
  *   norm                     device fp32, may be NULL when out is given
  * Squares are fp32 products summed in fp32 16 at a time, then in fp64; where fp32 squares
  * overflow or fall below its normal range they are summed again of scaled elements, so the
