@@ -52,20 +52,16 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// VEC elements of T as one load moves them: 4 or 16 bytes kept as 32-bit words (the compiler
-// would otherwise give each 16-bit element a register of its own), or a single element.
+// VEC elements of T as one load moves them: 16 bytes kept as 32-bit words (the compiler would
+// otherwise give each 16-bit element a register of its own), or a single element.
 template <class T, int VEC>
 struct Pack {
-    static constexpr int kWords = VEC * (int)sizeof(T) / 4;
+    static constexpr int kWords = 4;
+    static_assert(VEC * (int)sizeof(T) == 16, "packs are 16 bytes");
     uint32_t w[kWords];
     __device__ __forceinline__ void load(const T* p) {
-        if constexpr (kWords == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
-            static_assert(kWords == 1, "packs are 16 or 4 bytes");
-            w[0] = *reinterpret_cast<const uint32_t*>(p);
-        }
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     }
     __device__ __forceinline__ void unpack(float* o) const {
 #pragma unroll
@@ -99,15 +95,14 @@ __device__ __forceinline__ void store_pack(T* p, const float* v) {
     if constexpr (VEC == 1) {
         *p = from_f32<T>(v[0]);
     } else {
-        constexpr int words = VEC * (int)sizeof(T) / 4;
-        uint32_t w[words];
+        static_assert(VEC * (int)sizeof(T) == 16, "packs are 16 bytes");
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < words; ++i) {
+        for (int i = 0; i < 4; ++i) {
             if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
             else w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
         }
-        if constexpr (words == 4) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        else *reinterpret_cast<uint32_t*>(p) = w[0];
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
