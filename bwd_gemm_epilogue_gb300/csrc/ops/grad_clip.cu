@@ -8,7 +8,7 @@
 // and the scaling walks it backwards, so that what the norm read last is still in L2.
 //
 // Bound by HBM: gradients larger than L2 are read twice (the factor needs all of them first) and
-// written once.  Measured, 616.6 M bf16: 570 us, 3.7 GB at 6.5 TB/s of the 6.78 TB/s of a copy.
+// written once.  Measured, 616.6 M bf16: 574 us, 3.7 GB at 6.4 TB/s of the 6.78 TB/s of a copy.
 // Few and small gradients: two launches and one sum of the norm, 8.5 us.
 #include <algorithm>
 #include <memory>
@@ -164,8 +164,8 @@ __device__ __forceinline__ double cta_sum(double v) {
 }
 
 // Sum of g^2 over this CTA's share: fp32 products and sums of 64 bytes a thread, then fp64.  Bound by
-// HBM (1.23 GB of bf16 in 195 us, 6.3 TB/s); what hides the latency is 32 warps an SM with 64 bytes a
-// thread in flight (two such blocks a thread, at 24 warps: 698 us with the scaling instead of 561).
+// HBM (1.23 GB of bf16 in 203 us, 6.1 TB/s); what hides the latency is 32 warps an SM with 64 bytes a
+// thread in flight (two such blocks a thread, at 24 warps: 698 us with the scaling where one took 561).
 template <int N>
 __global__ void __launch_bounds__(kThreads, kCtas / kPlanSms) grad_squares_kernel(const __grid_constant__ ClipTable<N> c, double* sums) {
     cudaTriggerProgrammaticLaunchCompletion();             // the scaling may come up meanwhile
@@ -222,8 +222,8 @@ __device__ __forceinline__ void scale(const T* p, T* o, int64_t n, float f) {
 }
 
 // The norm from all launches' sums (every CTA, in the same order), then this launch's tensors:
-// out = g * min(1, max_norm / (norm + eps)).  Bound by HBM (1.23 GB of bf16 read and written in 372
-// us, 6.6 TB/s); from the end of the share, it finds up to an L2's worth of what the norm read last.
+// out = g * min(1, max_norm / (norm + eps)).  Bound by HBM (1.23 GB of bf16 read and written in 381
+// us, 6.5 TB/s); from the end of the share, it finds up to an L2's worth of what the norm read last.
 template <int N>
 __global__ void __launch_bounds__(kThreads, kCtas / kPlanSms) grad_scale_kernel(const __grid_constant__ ClipTable<N> c, const double* sums,
                                                               int num_sums, float max_norm, float eps, float* norm) {
