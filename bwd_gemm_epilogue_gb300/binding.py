@@ -1,9 +1,9 @@
-"""ctypes binding of the C ABI in ``include/swiglu_mlp.h``, ``include/swiglu_moe.h`` and
-``include/swiglu_ops.h`` -- argument marshalling only.
+"""ctypes binding of the C ABI in ``include/swiglu_mlp.h``, ``include/swiglu_moe.h``,
+``include/swiglu_ops.h`` and ``include/swiglu_tokens.h`` -- argument marshalling only.
 
 Each function has the name of the C entry point it calls and takes torch CUDA
-tensors for the pointer arguments (bf16, contiguous; the operators of
-``swiglu_ops.h`` also take fp16 and fp32, and rows at a stride); torch supplies device
+tensors for the pointer arguments (bf16, contiguous; the operators of ``swiglu_ops.h``
+and ``swiglu_tokens.h`` also take fp16 and fp32, and rows at a stride); torch supplies device
 memory and the current stream, every step of the computation runs in the
 library's kernels.  Outputs and workspaces the caller does not pass are
 allocated with torch.  A non-OK status raises ``SwigluError``; a missing
@@ -36,7 +36,7 @@ STATUS_NAMES = {
 }
 
 # Every symbol the headers under include/ declare: name -> (restype, argtypes)
-_f32 = ctypes.c_float
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 _vp, _i64, _i32, _u64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64, ctypes.c_size_t
 SIGNATURES = {
     "swiglu_mlp_fwd_workspace_size": (_sz, [_i64, _i64, _i64, _i64]),
@@ -82,11 +82,22 @@ SIGNATURES = {
                                          _i64, _i32, _i32, _vp, _sz, _vp]),
     "swiglu_mlp_clip_grads_workspace_size": (_sz, [_i64]),
     "swiglu_mlp_clip_grads": (_i32, [_vp, _vp, _vp, _vp, _i64, _f32, _f32, _vp, _vp, _sz, _vp]),
+    "swiglu_moe_gate_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp]),
+    "swiglu_moe_gate_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _i32, _vp]),
+    "swiglu_moe_sort": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp]),
+    "swiglu_moe_dispatch_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _vp]),
+    "swiglu_moe_dispatch_bwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _i32, _vp]),
+    "swiglu_moe_combine_fwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _i32, _f64, _u64,
+                                      _u64, _vp, _vp]),
+    "swiglu_moe_combine_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i32, _f64,
+                                      _u64, _u64, _vp, _vp]),
+    "swiglu_mlp_dropout": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _f64, _u64, _u64, _vp, _vp]),
 }
 
 KERNEL_KINDS = {1: "fwd_preact", 2: "fwd_down", 3: "bwd_grad_h", 4: "bwd_dW2", 5: "bwd_dx", 6: "bwd_dW1", 7: "gemm",
                 8: "bwd_gemms", 9: "elementwise", 10: "norm_fwd", 11: "norm_bwd", 12: "norm_params", 13: "grad_norm",
-                14: "grad_scale", 15: "moe_route", 16: "moe_up", 17: "moe_down", 18: "moe_join"}
+                14: "grad_scale", 15: "moe_route", 16: "moe_up", 17: "moe_down", 18: "moe_join",
+                19: "moe_gate", 20: "moe_sort", 21: "moe_scatter", 22: "moe_gather", 23: "dropout"}
 
 
 class SwigluError(RuntimeError):
@@ -954,3 +965,285 @@ def swiglu_mlp_clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, n
 def swiglu_mlp_grad_norm(grads, norm=None, workspace=None):
     """Global norm of gradients alone (swiglu_mlp_clip_grads without outputs)."""
     return _clip_call(list(grads), 0.0, 0.0, None, norm, workspace)
+
+
+# ---------------------------------------------------------------------------- tokens to experts and back
+
+def _rows_of(t: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
+    return t
+
+
+def swiglu_moe_gate_fwd(logits, top_k: int, renormalize: bool = True, ids=None, gates=None):
+    """The experts with the top_k largest softmax probabilities of each token; returns
+    (ids [T,top_k] int32, gates [T,top_k] fp32).  logits [T,E] bf16, fp16 or fp32, rows at any
+    stride; minus infinity switches an expert off, and a choice without an expert has id -1 and
+    gate 0.  renormalize: the chosen gates sum to one."""
+    T, E = _rows_of(logits, "logits").shape
+    code, device = _dtype(logits, "logits"), logits.device
+    p, ld = _rows(logits, "logits", (T, E), logits.dtype, device)
+    _top_k(top_k, E)
+    ids, pids = _out_vector(ids, "ids", (T, top_k), torch.int32, device)
+    gates, pgates = _out_vector(gates, "gates", (T, top_k), torch.float32, device)
+    st = lib().swiglu_moe_gate_fwd(p, ld, pids, pgates, T, E, top_k, bool(renormalize), code, _device_stream(device))
+    if st:
+        _check(st, "swiglu_moe_gate_fwd")
+    return ids, gates
+
+
+def _top_k(k, E):
+    if not 1 <= k <= E:
+        raise ValueError(f"top_k: {k}, expected 1 .. {E}")
+
+
+def swiglu_moe_gate_bwd(logits, ids, gates, dgates, renormalize: bool = True, dlogits=None):
+    """Gradient of the gates with respect to the logits: dlogits [T,E] of the logits' type.  ids,
+    gates: the forward's; dgates [T,top_k] fp32.  dlogits may be logits (in place)."""
+    T, E = _rows_of(logits, "logits").shape
+    code, device = _dtype(logits, "logits"), logits.device
+    p, ld = _rows(logits, "logits", (T, E), logits.dtype, device)
+    k = _rows_of(ids, "ids").shape[1]
+    _top_k(k, E)
+    pids = _vector(ids, "ids", (T, k), torch.int32, device)
+    pq = _vector(gates, "gates", (T, k), torch.float32, device)
+    pdq = _vector(dgates, "dgates", (T, k), torch.float32, device)
+    dlogits, pd, ldd = _out_rows(dlogits, "dlogits", (T, E), logits.dtype, device)
+    st = lib().swiglu_moe_gate_bwd(p, ld, pids, pq, pdq, pd, ldd, T, E, k, bool(renormalize), code, _device_stream(device))
+    if st:
+        _check(st, "swiglu_moe_gate_bwd")
+    return dlogits
+
+
+def swiglu_moe_sort(ids, E: int, counts=None, pos=None):
+    """(token, choice) pairs by expert, in their order; returns (counts [E] int32: rows of each
+    expert, pos: the pair's row, of ids' shape, int32, -1 where ids is outside 0 .. E - 1)."""
+    device = ids.device
+    pids = _vector(ids, "ids", ids.shape, torch.int32, device)
+    counts, pc = _out_vector(counts, "counts", (E,), torch.int32, device)
+    pos, pp = _out_vector(pos, "pos", ids.shape, torch.int32, device)
+    st = lib().swiglu_moe_sort(pids, pc, pp, ids.numel(), E, _device_stream(device))
+    if st:
+        _check(st, "swiglu_moe_sort")
+    return counts, pos
+
+
+def swiglu_moe_dispatch_fwd(x, pos, n_rows: int | None = None, rows=None):
+    """Tokens to their experts' rows: rows[pos[t,j]] = x[t].  x [T,D] bf16, fp16 or fp32; n_rows:
+    rows of a new output (all pairs' by default; the sum of the counts leaves none unwritten).
+    Rows that no pair has, and pairs with pos outside the rows, are left alone."""
+    T, D = _rows_of(x, "x").shape
+    k = _rows_of(pos, "pos").shape[1]
+    code, device = _dtype(x, "x"), x.device
+    px, ldx = _rows(x, "x", (T, D), x.dtype, device)
+    ppos = _vector(pos, "pos", (T, k), torch.int32, device)
+    if rows is None:
+        n_rows = T * k if n_rows is None else n_rows
+        if n_rows < 0:
+            raise ValueError(f"n_rows: {n_rows} is negative")
+    elif n_rows is not None and n_rows != rows.shape[0]:
+        raise ValueError(f"n_rows: {n_rows}, but rows has {rows.shape[0]}")
+    else:
+        n_rows = _rows_of(rows, "rows").shape[0]
+    rows, pr, ldr = _out_rows(rows, "rows", (n_rows, D), x.dtype, device)
+    st = lib().swiglu_moe_dispatch_fwd(px, ldx, ppos, pr, ldr, T, D, k, n_rows, code, _device_stream(device))
+    if st:
+        _check(st, "swiglu_moe_dispatch_fwd")
+    return rows
+
+
+def swiglu_moe_dispatch_bwd(drows, pos, add=None, dx=None):
+    """Gradient of the dispatch: dx [T,D], dx[t] = add[t] + sum_j drows[pos[t,j]].  add: of drows'
+    type or fp32 (the router's part of the gradient, say); dx may be add (in place)."""
+    n_rows, D = _rows_of(drows, "drows").shape
+    T, k = _rows_of(pos, "pos").shape
+    code, device = _dtype(drows, "drows"), drows.device
+    pd, ldd = _rows(drows, "drows", (n_rows, D), drows.dtype, device)
+    ppos = _vector(pos, "pos", (T, k), torch.int32, device)
+    atype = drows.dtype if add is None or add.dtype != torch.float32 else torch.float32
+    pa, lda = _rows(add, "add", (T, D), atype, device)
+    dx, px, ldx = _out_rows(dx, "dx", (T, D), drows.dtype, device)
+    st = lib().swiglu_moe_dispatch_bwd(pd, ldd, ppos, pa, lda, px, ldx, T, D, k, n_rows, code, _DTYPES[atype],
+                                       _device_stream(device))
+    if st:
+        _check(st, "swiglu_moe_dispatch_bwd")
+    return dx
+
+
+def _mask(seed, offset, step, device):
+    """seed, offset and the pointer of step, of a dropout."""
+    seed, offset = operator.index(seed), operator.index(offset)
+    for name, v in (("seed", seed), ("offset", offset)):
+        if not 0 <= v < 1 << 64:
+            raise ValueError(f"{name}: {v}, expected 0 .. 2**64 - 1")
+    return seed, offset, _vector(step, "step", (), torch.int64, device)
+
+
+def swiglu_moe_combine_fwd(rows, pos, gates, residual=None, p: float = 0.0, seed: int = 0, offset: int = 0, step=None,
+                           y=None):
+    """The experts' rows back to their tokens: y[t] = residual[t] + dropout(sum_j gates[t,j] *
+    rows[pos[t,j]]).  rows [n,D] bf16, fp16 or fp32, residual of the same type; y may be residual
+    (in place).  p, seed, offset, step: the dropout's, as in swiglu_mlp_dropout."""
+    n_rows, D = _rows_of(rows, "rows").shape
+    T, k = _rows_of(pos, "pos").shape
+    code, device = _dtype(rows, "rows"), rows.device
+    pr, ldr = _rows(rows, "rows", (n_rows, D), rows.dtype, device)
+    ppos = _vector(pos, "pos", (T, k), torch.int32, device)
+    pg = _vector(gates, "gates", (T, k), torch.float32, device)
+    pres, ldres = _rows(residual, "residual", (T, D), rows.dtype, device)
+    seed, offset, pstep = _mask(seed, offset, step, device)
+    y, py, ldy = _out_rows(y, "y", (T, D), rows.dtype, device)
+    st = lib().swiglu_moe_combine_fwd(pr, ldr, ppos, pg, pres, ldres, py, ldy, T, D, k, n_rows, code, p, seed, offset,
+                                      pstep, _device_stream(device))
+    if st:
+        _check(st, "swiglu_moe_combine_fwd")
+    return y
+
+
+def swiglu_moe_combine_bwd(dy, rows, pos, gates, p: float = 0.0, seed: int = 0, offset: int = 0, step=None, drows=None,
+                           dgates=None):
+    """Gradient of the combine; returns (drows, dgates [T,k] fp32).  The residual's gradient is dy.
+    dgates is 0 where a pair has no row; rows that no pair has are left alone in drows."""
+    n_rows, D = _rows_of(rows, "rows").shape
+    T, k = _rows_of(pos, "pos").shape
+    code, device = _dtype(rows, "rows"), rows.device
+    pdy, lddy = _rows(dy, "dy", (T, D), rows.dtype, device)
+    pr, ldr = _rows(rows, "rows", (n_rows, D), rows.dtype, device)
+    ppos = _vector(pos, "pos", (T, k), torch.int32, device)
+    pg = _vector(gates, "gates", (T, k), torch.float32, device)
+    seed, offset, pstep = _mask(seed, offset, step, device)
+    drows, pd, ldd = _out_rows(drows, "drows", (n_rows, D), rows.dtype, device)
+    dgates, pdg = _out_vector(dgates, "dgates", (T, k), torch.float32, device)
+    st = lib().swiglu_moe_combine_bwd(pdy, lddy, pr, ldr, ppos, pg, pd, ldd, pdg, T, D, k, n_rows, code, p, seed, offset,
+                                      pstep, _device_stream(device))
+    if st:
+        _check(st, "swiglu_moe_combine_bwd")
+    return drows, dgates
+
+
+class MoEGate(torch.autograd.Function):
+    """autograd wrapper of the gate.  Differentiable once."""
+
+    @staticmethod
+    def forward(ctx, logits, top_k, renormalize):
+        rows = _flat_rows(logits)
+        ids, gates = swiglu_moe_gate_fwd(rows, top_k, renormalize)
+        ctx.save_for_backward(logits, ids, gates)
+        ctx.renormalize = renormalize
+        ctx.mark_non_differentiable(ids)
+        ctx.set_materialize_grads(False)
+        lead = logits.shape[:-1]
+        return ids.reshape(*lead, top_k), gates.reshape(*lead, top_k)
+
+    @staticmethod
+    def backward(ctx, _, dgates):
+        if dgates is None:
+            return None, None, None
+        logits, ids, gates = ctx.saved_tensors
+        with torch.no_grad():
+            d = swiglu_moe_gate_bwd(_flat_rows(logits), ids, gates, dgates.reshape(gates.shape).contiguous(), ctx.renormalize)
+            d = d.reshape(logits.shape)
+        return *_once((d,), dgates, logits), None, None
+
+
+def moe_gate(logits, top_k: int, renormalize: bool = True):
+    """(ids int32, gates fp32) of shape [..., top_k]; gradients reach the logits through the gates."""
+    return MoEGate.apply(logits, top_k, renormalize)
+
+
+class MoEDispatch(torch.autograd.Function):
+    """autograd wrapper of the dispatch (rows that no pair has, if any, are zeros).  Differentiable once."""
+
+    @staticmethod
+    def forward(ctx, x, pos, n_rows):
+        flat, p2 = _flat_rows(x), pos.reshape(-1, pos.shape[-1]).contiguous()
+        rows = torch.zeros(p2.numel() if n_rows is None else n_rows, flat.shape[1], dtype=x.dtype, device=x.device)
+        swiglu_moe_dispatch_fwd(flat, p2, rows=rows)
+        ctx.save_for_backward(p2)
+        ctx.shape = x.shape
+        return rows
+
+    @staticmethod
+    def backward(ctx, drows):
+        p2, = ctx.saved_tensors
+        with torch.no_grad():
+            dx = swiglu_moe_dispatch_bwd(_flat_rows(drows), p2).reshape(ctx.shape)
+        return *_once((dx,), drows), None, None
+
+
+def moe_dispatch(x, pos, n_rows: int | None = None):
+    """rows [n_rows, D] of x [..., D] by pos [..., top_k] (swiglu_moe_sort)."""
+    return MoEDispatch.apply(x, pos, n_rows)
+
+
+class MoECombine(torch.autograd.Function):
+    """autograd wrapper of the combine.  Differentiable once."""
+
+    @staticmethod
+    def forward(ctx, rows, pos, gates, residual, p, seed, offset, step):
+        lead, k = pos.shape[:-1], pos.shape[-1]
+        r2, p2, g2 = _flat_rows(rows), pos.reshape(-1, k).contiguous(), gates.reshape(-1, k).contiguous()
+        y = swiglu_moe_combine_fwd(r2, p2, g2, None if residual is None else _flat_rows(residual), p, seed, offset, step)
+        ctx.save_for_backward(rows, p2, gates, step)
+        ctx.mask = p, seed, offset
+        ctx.residual = None if residual is None else residual.shape
+        return y.reshape(*lead, y.shape[1])
+
+    @staticmethod
+    def backward(ctx, dy):
+        rows, p2, gates, step = ctx.saved_tensors
+        with torch.no_grad():
+            r2 = _flat_rows(rows)
+            drows, dgates = swiglu_moe_combine_bwd(_flat_rows(dy), r2, p2, gates.reshape(p2.shape).contiguous(), *ctx.mask, step,
+                                                   drows=torch.zeros_like(r2, memory_format=torch.contiguous_format))
+            drows, dgates = drows.reshape(rows.shape), dgates.reshape(gates.shape)
+        drows, dgates = _once((drows, dgates), dy, rows, gates)
+        return drows, None, dgates, _residual_grad(dy, ctx.residual), None, None, None, None
+
+
+def moe_combine(rows, pos, gates, residual=None, p: float = 0.0, seed: int = 0, offset: int = 0, step=None):
+    """y [..., D] = residual + dropout(sum_j gates_j rows[pos_j]) for pos, gates [..., top_k]."""
+    return MoECombine.apply(rows, pos, gates, residual, p, seed, offset, step)
+
+
+# ---------------------------------------------------------------------------- dropout
+
+def swiglu_mlp_dropout(x, p: float, seed: int, offset: int = 0, step=None, residual=None, y=None):
+    """y = residual + dropout(x): each element kept with probability 1 - p (to the nearest 1/65536) and
+    divided by it.  The mask follows from (seed, offset + step) and the element's row and column and
+    is never stored: the gradient is the same call on dy.  x, residual [M,D] bf16, fp16 or fp32; y may
+    be x or residual (in place).  step: an int64 scalar on the device, so that a captured graph has
+    another mask on every replay; leave it alone between a forward and its backward."""
+    M, D = _rows_of(x, "x").shape
+    code, device = _dtype(x, "x"), x.device
+    px, ldx = _rows(x, "x", (M, D), x.dtype, device)
+    pr, ldr = _rows(residual, "residual", (M, D), x.dtype, device)
+    seed, offset, pstep = _mask(seed, offset, step, device)
+    y, py, ldy = _out_rows(y, "y", (M, D), x.dtype, device)
+    st = lib().swiglu_mlp_dropout(px, ldx, pr, ldr, py, ldy, M, D, code, p, seed, offset, pstep, _device_stream(device))
+    if st:
+        _check(st, "swiglu_mlp_dropout")
+    return y
+
+
+class Dropout(torch.autograd.Function):
+    """autograd wrapper: the backward computes the mask again.  Leading dimensions are flattened."""
+
+    @staticmethod
+    def forward(ctx, x, p, seed, offset, step, residual):
+        y = swiglu_mlp_dropout(_flat_rows(x), p, seed, offset, step, None if residual is None else _flat_rows(residual))
+        ctx.save_for_backward(step)
+        ctx.mask = p, seed, offset
+        ctx.residual = None if residual is None else residual.shape
+        return y.reshape(x.shape)
+
+    @staticmethod
+    def backward(ctx, dy):
+        step, = ctx.saved_tensors
+        dx = Dropout.apply(dy, *ctx.mask, step, None)      # linear: its own gradient is itself
+        return dx, None, None, None, None, _residual_grad(dy, ctx.residual)
+
+
+def dropout(x, p: float, seed: int, offset: int = 0, step=None, residual=None):
+    """residual + dropout(x) for x [..., D], as swiglu_mlp_dropout."""
+    return Dropout.apply(x, p, seed, offset, step, residual)

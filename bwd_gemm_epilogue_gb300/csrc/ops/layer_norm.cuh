@@ -2,21 +2,15 @@
 // gamma and beta in shared memory, sums over a row, and the plan of a launch.
 #pragma once
 
-#include "../host.h"
-#include "convert.cuh"
-#include "swiglu_ops.h"
+#include "rows.cuh"
 
 namespace swiglu {
 namespace {
 
-constexpr int kPlanSms = 152;      // grids are planned for the GB300, so that the workspace query sees no device
 constexpr int kMaxThreads = 512;   // the forms for rows too wide for registers
 constexpr size_t kSmem = 227 * 1024;
 
 // ---------------------------------------------------------------- 16-byte packs of a row
-
-template <class T>
-constexpr int kVec = 16 / (int)sizeof(T);
 
 // Rows that do not start on 16-byte boundaries, or end off them, but lie alike in every tensor:
 // pack k is then the aligned 16 bytes with the columns k * kVec - m ... of the row, where the row
@@ -39,32 +33,6 @@ __device__ __forceinline__ uint4 row_elements(uint4 v, int first, int D) {
         if ((unsigned)(first + j) >= (unsigned)D) w[j / per] &= ~bits;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// They alone, loaded and stored one by one; `row`: column 0.
-template <class T>
-__device__ __forceinline__ uint4 load_edge(const T* row, int first, int D) {
-    uint32_t w[4] = {0, 0, 0, 0};
-    constexpr int per = 4 / (int)sizeof(T);
-#pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) {
-        if ((unsigned)(first + j) < (unsigned)D) {
-            if constexpr (sizeof(T) == 4) w[j] = *reinterpret_cast<const uint32_t*>(row + first + j);
-            else w[j / per] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + first + j) << (j % per * 16);
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <class T>
-__device__ __forceinline__ void store_edge(T* row, int first, int D, const uint4& v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    constexpr int per = 4 / (int)sizeof(T);
-#pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) {
-        if ((unsigned)(first + j) < (unsigned)D) {
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(row + first + j) = w[j];
-            else *reinterpret_cast<uint16_t*>(row + first + j) = (uint16_t)(w[j / per] >> (j % per * 16));
-        }
-    }
 }
 
 __device__ __forceinline__ uint4 load_smem(uint32_t at) {
@@ -150,12 +118,6 @@ __device__ __forceinline__ bool on_edge(int q, int k, int m, int end) {
 
 // ---------------------------------------------------------------- sums over a row
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 // Barrier of a group of threads (barrier 0 is __syncthreads').
 __device__ __forceinline__ void group_sync(int group, int lanes) {
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
@@ -233,11 +195,6 @@ inline NormPlan norm_plan(int64_t width, int size, int packs, int threads) {
 // worker has a partial plane, so the wider the row, the fewer.  Wider than 8192: two passes.
 inline int narrow_threads(int64_t D) { return D <= 32 * kCols ? 32 : D <= 128 * kCols ? 128 : 512; }
 constexpr int64_t kNarrowWidth = 512 * kCols;
-// Bytes an element of `type` takes; 0 for an unknown type.
-inline int type_bytes(int type) { return type == SWIGLU_FP32 ? 4 : type == SWIGLU_BF16 || type == SWIGLU_FP16 ? 2 : 0; }
-
-inline bool misaligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
-
 // How a call's rows lie: every base, row stride and the width on 16-byte boundaries (kWhole), or
 // off them but each row alike in all tensors (kEdge), or neither (kApart).  A row of less than
 // kLeastEdge bytes counts as kApart: most of its packs would be edges.
@@ -258,14 +215,6 @@ struct Rows16 {
         return alike && D * size >= kLeastEdge ? kEdge : kApart;
     }
 };
-
-// f.run<T>() for the run-time type.
-template <class F>
-cudaError_t with_type(int type, const F& f) {
-    if (type == SWIGLU_FP32) return f.template run<float>();
-    if (type == SWIGLU_FP16) return f.template run<__half>();
-    return f.template run<__nv_bfloat16>();
-}
 
 // Past 48 KB, of which the kernels' own arrays take less than 1 KB, a launch has to be allowed.
 template <class K>

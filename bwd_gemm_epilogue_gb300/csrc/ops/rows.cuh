@@ -1,0 +1,127 @@
+// rows.cuh -- rows of a tensor in 16-byte packs, what the operators on rows of bf16, fp16 and fp32
+// have in common.
+#pragma once
+
+#include "../host.h"
+#include "convert.cuh"
+#include "swiglu_ops.h"
+
+namespace swiglu {
+namespace {
+
+constexpr int kPlanSms = 152;      // grids are planned for the GB300, so that the workspace query sees no device
+
+template <class T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+// The elements of the pack that starts at column `first` which are the row's, loaded and stored one
+// by one (others are loaded as 0); `row`: column 0.
+template <class T>
+__device__ __forceinline__ uint4 load_edge(const T* row, int first, int D) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    constexpr int per = 4 / (int)sizeof(T);
+#pragma unroll
+    for (int j = 0; j < kVec<T>; ++j) {
+        if ((unsigned)(first + j) < (unsigned)D) {
+            if constexpr (sizeof(T) == 4) w[j] = *reinterpret_cast<const uint32_t*>(row + first + j);
+            else w[j / per] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + first + j) << (j % per * 16);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <class T>
+__device__ __forceinline__ void store_edge(T* row, int first, int D, const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    constexpr int per = 4 / (int)sizeof(T);
+#pragma unroll
+    for (int j = 0; j < kVec<T>; ++j) {
+        if ((unsigned)(first + j) < (unsigned)D) {
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t*>(row + first + j) = w[j];
+            else *reinterpret_cast<uint16_t*>(row + first + j) = (uint16_t)(w[j / per] >> (j % per * 16));
+        }
+    }
+}
+
+// The 16 bytes that start m bytes (even, below 16) into the 32 of lo and hi.
+__device__ __forceinline__ uint4 shift_right(const uint4& lo, const uint4& hi, unsigned m) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
+    const unsigned bits = (m & 2) * 8;
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// 16 bytes of a row that need not start on a 16-byte boundary: columns c .. c + kVec - 1, those past the
+// row's ends as 0.  Whole ones come out of the two aligned packs that hold them (each has at least one
+// element of this row, so nothing outside the tensor's own 16-byte granules is read).
+template <class T>
+__device__ __forceinline__ uint4 load_shifted(const T* row, int c, int D) {
+    if (c < 0 || c + kVec<T> > D) return load_edge(row, c, D);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+    const uint4* p = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+    const unsigned m = (unsigned)(at & 15);
+    const uint4 lo = p[0];
+    if (m == 0) return lo;
+    const uint4 hi = p[1];
+    return shift_right(lo, hi, m);
+}
+
+// Columns c .. c + kVec - 1 of a row; EDGE: whether rows may lie off 16-byte boundaries or end off them.
+template <class T, bool EDGE>
+__device__ __forceinline__ uint4 load_cols(const T* row, int c, int D) {
+    if constexpr (EDGE) return load_shifted(row, c, D);
+    else return *reinterpret_cast<const uint4*>(row + c);
+}
+// The same of an output, whose packs are taken on its 16-byte boundaries (first_col).
+template <class T, bool EDGE>
+__device__ __forceinline__ void store_cols(T* row, int c, int D, const uint4& v) {
+    if (EDGE && (c < 0 || c + kVec<T> > D)) store_edge(row, c, D, v);
+    else *reinterpret_cast<uint4*>(row + c) = v;
+}
+// First column of pack k of an output row (up to kVec - 1 before the row).
+template <class T, bool EDGE>
+__device__ __forceinline__ int first_col(const T* row, int k) {
+    return k * kVec<T> - (EDGE ? (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)) : 0);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// ---------------------------------------------------------------- host side
+
+// Bytes an element of `type` takes; 0 for an unknown type.
+inline int type_bytes(int type) { return type == SWIGLU_FP32 ? 4 : type == SWIGLU_BF16 || type == SWIGLU_FP16 ? 2 : 0; }
+
+inline bool misaligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
+
+// f.run<T>() for the run-time type.
+template <class F>
+cudaError_t with_type(int type, const F& f) {
+    if (type == SWIGLU_FP32) return f.template run<float>();
+    if (type == SWIGLU_FP16) return f.template run<__half>();
+    return f.template run<__nv_bfloat16>();
+}
+
+// x / d for 0 <= x < 2^31 and 1 <= d < 2^31 by a product: with 2^(l - 1) < d <= 2^l and
+// m = floor(2^(31 + l) / d) + 1, m d exceeds 2^(31 + l) by at most d <= 2^l, so x m / 2^(31 + l)
+// exceeds x / d by less than 1 / d.
+struct Divisor {
+    uint32_t m, shift, d;
+    static Divisor of(uint32_t d) {
+        uint32_t l = 0;
+        while ((uint64_t(1) << l) < d) ++l;
+        return {(uint32_t)((uint64_t(1) << (31 + l)) / d + 1), 31 + l, d};
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t x) const { return (uint32_t)(((uint64_t)x * m) >> shift); }
+};
+
+}  // namespace
+}  // namespace swiglu

@@ -338,7 +338,12 @@ typedef enum {
     SWIGLU_KERNEL_MOE_ROUTE = 15,   /* routed MoE layer (swiglu_moe.h): router and choice of experts */
     SWIGLU_KERNEL_MOE_UP = 16,      /* routed MoE layer: x @ W1^T and SwiGLU of the chosen experts */
     SWIGLU_KERNEL_MOE_DOWN = 17,    /* routed MoE layer: parts of h @ W2^T, weighted per token */
-    SWIGLU_KERNEL_MOE_JOIN = 18     /* routed MoE layer: the parts added */
+    SWIGLU_KERNEL_MOE_JOIN = 18,    /* routed MoE layer: the parts added */
+    SWIGLU_KERNEL_MOE_GATE = 19,    /* choice of experts from logits, or its gradient (swiglu_tokens.h) */
+    SWIGLU_KERNEL_MOE_SORT = 20,    /* (token, choice) pairs by expert */
+    SWIGLU_KERNEL_MOE_SCATTER = 21, /* tokens to their experts' rows, or the combine's gradient */
+    SWIGLU_KERNEL_MOE_GATHER = 22,  /* experts' rows back to their tokens, or the dispatch's gradient */
+    SWIGLU_KERNEL_DROPOUT = 23      /* dropout without experts */
 } swiglu_kernel_kind;
 
 /*
