@@ -2,12 +2,14 @@
 
     y = x + sum_j gate_j * expert_{e_j}(LayerNorm(x)),   gates = softmax over the top_k logits
 
-``forward`` / ``backward`` / ``step`` train it on batches: layer norm forward and backward with
-the residual stream's gradient fused in, the grouped experts (``swiglu_moe_fwd`` / ``_bwd``) on
-rows sorted by expert, and gradients clipped by their global norm before the update.  The
-routing between them (a [T, E] product, a sort, gathers) is plain torch, and the grouped
-launches take their row counts from the host.  ``decode`` answers for up to 64 tokens with the
-same weights in a handful of launches and no host synchronisation (``swiglu_moe_routed_fwd``).
+``forward`` / ``backward`` / ``step`` train it on batches, in the library's kernels but for the
+router's two products with torch: layer norm forward and backward with the residual stream's gradient fused
+in, the gate (softmax and top k), the rows sorted by expert, the grouped experts
+(``swiglu_moe_fwd`` / ``_bwd``) and their rows back to the tokens with the gates, dropout and the
+residual stream, each with its gradient, and gradients clipped by their global norm before the
+update.  The grouped launches take their row counts from the host, the one synchronisation of a
+step.  ``decode`` answers for up to 64 tokens with the same weights in a handful of launches and no
+host synchronisation (``swiglu_moe_routed_fwd``).
 """
 from __future__ import annotations
 
@@ -20,15 +22,20 @@ class PreNormMoE:
     """gamma, beta [D], router [E, D] (fp32 or bf16), W1 [E, 2H, D], W2 [E, D, H] bf16 CUDA tensors or
     Parameters; the block has a backward of its own, and autograd sees nothing of it."""
 
-    def __init__(self, gamma, beta, router, W1, W2, top_k: int, eps: float = 1e-5):
+    def __init__(self, gamma, beta, router, W1, W2, top_k: int, eps: float = 1e-5, dropout: float = 0.0, seed: int = 0):
+        """dropout: probability of dropping an element of the experts' sum in training (not in
+        decode); the masks follow from seed and the number of the forward call."""
         E, H2, D = W1.shape
         if W2.shape != (E, D, H2 // 2) or router.shape != (E, D) or gamma.shape != (D,) or beta.shape != (D,):
             raise ValueError(f"shape mismatch: gamma {tuple(gamma.shape)}, beta {tuple(beta.shape)}, router "
                              f"{tuple(router.shape)}, W1 {tuple(W1.shape)}, W2 {tuple(W2.shape)}")
         if not 1 <= top_k <= E:
             raise ValueError(f"top_k: {top_k}, expected 1 .. {E}")
+        if not 0 <= dropout <= 1:
+            raise ValueError(f"dropout: {dropout}, expected 0 .. 1")
         self.params = [gamma, beta, router, W1, W2]
         self.top_k, self.eps = top_k, eps
+        self.dropout, self.seed, self.calls = dropout, seed, 0
         self.grads = None
         self._saved = None
 
@@ -36,38 +43,30 @@ class PreNormMoE:
     def forward(self, x):
         """x [T, D] bf16 -> y [T, D]; keeps what the backward needs."""
         gamma, beta, router, W1, W2 = self.params
-        T, k = x.shape[0], self.top_k
         xn, _, mean, rstd = binding.swiglu_mlp_layer_norm_fwd(x, gamma, beta, self.eps)
         logits = xn.float() @ router.float().T
-        picked, ids = (v[:, :k] for v in torch.sort(logits, dim=1, descending=True, stable=True))
-        gates = torch.softmax(picked, dim=1)
-        order = torch.argsort(ids.reshape(-1), stable=True)              # (token, choice) pairs by expert
-        counts = torch.bincount(ids.reshape(-1), minlength=router.shape[0]).tolist()
-        xg = xn[order // k]
+        ids, gates = binding.swiglu_moe_gate_fwd(logits, self.top_k)
+        counts, pos = binding.swiglu_moe_sort(ids, router.shape[0])
+        counts = counts.tolist()
+        xg = binding.swiglu_moe_dispatch_fwd(xn, pos, sum(counts))
         preact, rows = binding.swiglu_moe_fwd(xg, W1, W2, counts)
-        out = torch.empty_like(rows)
-        out[order] = rows
-        out = out.reshape(T, k, -1)
-        y = (x.float() + (out.float() * gates[:, :, None]).sum(1)).to(x.dtype)
-        self._saved = (x, xn, mean, rstd, ids, gates, order, counts, xg, preact, out)
+        mask = dict(p=self.dropout, seed=self.seed, offset=self.calls)
+        y = binding.swiglu_moe_combine_fwd(rows, pos, gates, residual=x, **mask)
+        self.calls += 1
+        self._saved = (x, xn, mean, rstd, ids.long(), gates, logits, counts, xg, preact, rows, ids, pos, mask)
         return y
 
     @torch.no_grad()
     def backward(self, dy):
         """dy [T, D] bf16 -> dx; leaves the parameters' gradients in self.grads."""
         gamma, _, router, W1, W2 = self.params
-        x, xn, mean, rstd, ids, gates, order, counts, xg, preact, out = self._saved
-        T, k = x.shape[0], self.top_k
-        dgates = (dy.float()[:, None] * out.float()).sum(2)
-        drows = (dy.float()[:, None] * gates[:, :, None]).to(dy.dtype).reshape(T * k, -1)[order]
+        x, xn, mean, rstd, _, gates, logits, counts, xg, preact, rows, ids, pos, mask = self._saved
+        drows, dgates = binding.swiglu_moe_combine_bwd(dy, rows, pos, gates, **mask)
         dxg, dW1, dW2 = binding.swiglu_moe_bwd(xg, W1, W2, preact, drows, counts)
-        back = torch.empty_like(dxg)
-        back[order] = dxg
-        dpicked = gates * (dgates - (gates * dgates).sum(1, keepdim=True))
-        dlogits = torch.zeros(T, router.shape[0], device=x.device).scatter(1, ids, dpicked)
-        dxn = back.reshape(T, k, -1).float().sum(1) + dlogits @ router.float()
+        dlogits = binding.swiglu_moe_gate_bwd(logits, ids, gates, dgates)
+        dxn = binding.swiglu_moe_dispatch_bwd(dxg, pos, add=dlogits @ router.float())
         drouter = (dlogits.T @ xn.float()).to(router.dtype)
-        dx, dgamma, dbeta = binding.swiglu_mlp_layer_norm_bwd(dxn.to(x.dtype), x, gamma, mean, rstd, dskip=dy)
+        dx, dgamma, dbeta = binding.swiglu_mlp_layer_norm_bwd(dxn, x, gamma, mean, rstd, dskip=dy)
         self.grads = [dgamma, dbeta, drouter, dW1, dW2]
         return dx
 

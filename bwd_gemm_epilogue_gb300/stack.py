@@ -5,7 +5,8 @@ weights: the layer input x_l (which is the previous layer's output, already
 kept) and preact_l -- the drop-h saved-tensor policy applied to every layer
 ("SwiGLU MLP Drop-H technical report", 4-layer stack memory table).  Backward
 walks the layers in reverse; each layer's dx is the next (lower) layer's dy.
-Every product runs in the library's kernels through the C ABI.
+Every product runs in the library's kernels through the C ABI.  With dropout, y_l =
+dropout(block_l(y_{l-1})) in place, and the backward computes each layer's mask again.
 """
 from __future__ import annotations
 
@@ -15,8 +16,13 @@ from . import binding
 
 
 class SwiGLUStack:
-    def __init__(self, layers, M: int, device=None):
-        """layers: list of (W1 [2H,D], W2 [Dout,H]) CUDA bf16 tensors with D == Dout."""
+    def __init__(self, layers, M: int, device=None, dropout: float = 0.0, seed: int = 0):
+        """layers: list of (W1 [2H,D], W2 [Dout,H]) CUDA bf16 tensors with D == Dout.  dropout:
+        probability of dropping an element of a layer's output; the masks follow from seed, the number of the
+        forward call and the layer."""
+        if not 0 <= dropout <= 1:
+            raise ValueError(f"dropout: {dropout}, expected 0 .. 1")
+        self.dropout, self.seed, self.calls = dropout, seed, 0
         self.layers = layers
         self.M = M
         W1, W2 = layers[0]
@@ -39,9 +45,15 @@ class SwiGLUStack:
 
     def forward(self, x):
         self.acts[0].copy_(x)
+        self.calls += 1
         for l, (W1, W2) in enumerate(self.layers):
             binding.swiglu_mlp_fwd(self.acts[l], W1, W2, self.preacts[l], self.acts[l + 1], self.ws_f)
+            if self.dropout:
+                binding.swiglu_mlp_dropout(self.acts[l + 1], self.dropout, self.seed, self._mask(l), y=self.acts[l + 1])
         return self.acts[-1]
+
+    def _mask(self, l: int) -> int:
+        return self.calls * len(self.layers) + l
 
     def backward(self, dy):
         """Returns (dx of the stack input, [(dW1_l, dW2_l) for each layer])."""
@@ -50,6 +62,9 @@ class SwiGLUStack:
             W1, W2 = self.layers[l]
             dW1, dW2 = self.grads[l]
             out = self.dacts[l % 2]
+            if self.dropout:       # the caller's dy stays as it is
+                cur = binding.swiglu_mlp_dropout(cur, self.dropout, self.seed, self._mask(l),
+                                                 y=self.dacts[(l + 1) % 2] if cur is dy else cur)
             binding.swiglu_mlp_bwd(self.acts[l], W1, W2, self.preacts[l], cur, out, dW1, dW2, self.ws_b)
             cur = out
         return cur, self.grads
