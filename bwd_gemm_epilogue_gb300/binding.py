@@ -980,6 +980,10 @@ def swiglu_moe_gate_fwd(logits, top_k: int, renormalize: bool = True, ids=None, 
     (ids [T,top_k] int32, gates [T,top_k] fp32).  logits [T,E] bf16, fp16 or fp32, rows at any
     stride; minus infinity switches an expert off, and a choice without an expert has id -1 and
     gate 0.  renormalize: the chosen gates sum to one."""
+    if ids is None and gates is None:
+        done = _short().moe_gate_fwd(logits, top_k, renormalize)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_moe_gate_fwd")
     T, E = _rows_of(logits, "logits").shape
     code, device = _dtype(logits, "logits"), logits.device
     p, ld = _rows(logits, "logits", (T, E), logits.dtype, device)
@@ -1000,6 +1004,10 @@ def _top_k(k, E):
 def swiglu_moe_gate_bwd(logits, ids, gates, dgates, renormalize: bool = True, dlogits=None):
     """Gradient of the gates with respect to the logits: dlogits [T,E] of the logits' type.  ids,
     gates: the forward's; dgates [T,top_k] fp32.  dlogits may be logits (in place)."""
+    if dlogits is None:
+        done = _short().moe_gate_bwd(logits, ids, gates, dgates, renormalize)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_moe_gate_bwd")
     T, E = _rows_of(logits, "logits").shape
     code, device = _dtype(logits, "logits"), logits.device
     p, ld = _rows(logits, "logits", (T, E), logits.dtype, device)
@@ -1018,6 +1026,10 @@ def swiglu_moe_gate_bwd(logits, ids, gates, dgates, renormalize: bool = True, dl
 def swiglu_moe_sort(ids, E: int, counts=None, pos=None):
     """(token, choice) pairs by expert, in their order; returns (counts [E] int32: rows of each
     expert, pos: the pair's row, of ids' shape, int32, -1 where ids is outside 0 .. E - 1)."""
+    if counts is None and pos is None:
+        done = _short().moe_sort(ids, E)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_moe_sort")
     device = ids.device
     pids = _vector(ids, "ids", ids.shape, torch.int32, device)
     counts, pc = _out_vector(counts, "counts", (E,), torch.int32, device)
@@ -1032,6 +1044,10 @@ def swiglu_moe_dispatch_fwd(x, pos, n_rows: int | None = None, rows=None):
     """Tokens to their experts' rows: rows[pos[t,j]] = x[t].  x [T,D] bf16, fp16 or fp32; n_rows:
     rows of a new output (all pairs' by default; the sum of the counts leaves none unwritten).
     Rows that no pair has, and pairs with pos outside the rows, are left alone."""
+    if rows is None:
+        done = _short().moe_dispatch_fwd(x, pos, n_rows)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_moe_dispatch_fwd")
     T, D = _rows_of(x, "x").shape
     k = _rows_of(pos, "pos").shape[1]
     code, device = _dtype(x, "x"), x.device
@@ -1055,6 +1071,10 @@ def swiglu_moe_dispatch_fwd(x, pos, n_rows: int | None = None, rows=None):
 def swiglu_moe_dispatch_bwd(drows, pos, add=None, dx=None):
     """Gradient of the dispatch: dx [T,D], dx[t] = add[t] + sum_j drows[pos[t,j]].  add: of drows'
     type or fp32 (the router's part of the gradient, say); dx may be add (in place)."""
+    if dx is None:
+        done = _short().moe_dispatch_bwd(drows, pos, add)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_moe_dispatch_bwd")
     n_rows, D = _rows_of(drows, "drows").shape
     T, k = _rows_of(pos, "pos").shape
     code, device = _dtype(drows, "drows"), drows.device
@@ -1084,6 +1104,10 @@ def swiglu_moe_combine_fwd(rows, pos, gates, residual=None, p: float = 0.0, seed
     """The experts' rows back to their tokens: y[t] = residual[t] + dropout(sum_j gates[t,j] *
     rows[pos[t,j]]).  rows [n,D] bf16, fp16 or fp32, residual of the same type; y may be residual
     (in place).  p, seed, offset, step: the dropout's, as in swiglu_mlp_dropout."""
+    if y is None:
+        done = _short().moe_combine_fwd(rows, pos, gates, residual, p, seed, offset, step)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_moe_combine_fwd")
     n_rows, D = _rows_of(rows, "rows").shape
     T, k = _rows_of(pos, "pos").shape
     code, device = _dtype(rows, "rows"), rows.device
@@ -1104,6 +1128,10 @@ def swiglu_moe_combine_bwd(dy, rows, pos, gates, p: float = 0.0, seed: int = 0, 
                            dgates=None):
     """Gradient of the combine; returns (drows, dgates [T,k] fp32).  The residual's gradient is dy.
     dgates is 0 where a pair has no row; rows that no pair has are left alone in drows."""
+    if drows is None and dgates is None:
+        done = _short().moe_combine_bwd(dy, rows, pos, gates, p, seed, offset, step)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_moe_combine_bwd")
     n_rows, D = _rows_of(rows, "rows").shape
     T, k = _rows_of(pos, "pos").shape
     code, device = _dtype(rows, "rows"), rows.device
@@ -1214,6 +1242,10 @@ def swiglu_mlp_dropout(x, p: float, seed: int, offset: int = 0, step=None, resid
     is never stored: the gradient is the same call on dy.  x, residual [M,D] bf16, fp16 or fp32; y may
     be x or residual (in place).  step: an int64 scalar on the device, so that a captured graph has
     another mask on every replay; leave it alone between a forward and its backward."""
+    if y is None:
+        done = _short().dropout(x, residual, p, seed, offset, step)
+        if done is not None:
+            return done if done.__class__ is not int else _check(done, "swiglu_mlp_dropout")
     M, D = _rows_of(x, "x").shape
     code, device = _dtype(x, "x"), x.device
     px, ldx = _rows(x, "x", (M, D), x.dtype, device)

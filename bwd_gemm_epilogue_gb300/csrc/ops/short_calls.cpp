@@ -1,5 +1,5 @@
-// short_calls.cpp -- a Python module with the usual calls of the operators in swiglu_ops.h and
-// swiglu_moe.h over torch tensors, for binding.py.
+// short_calls.cpp -- a Python module with the usual calls of the operators in swiglu_ops.h,
+// swiglu_tokens.h and swiglu_moe.h over torch tensors, for binding.py.
 //
 // On the device these calls can be shorter than the 20 to 30 us that Python takes to check a call's
 // tensors, make its outputs and pass its 20 arguments (a norm of 16 rows: 4 us), so the usual call,
@@ -19,6 +19,7 @@
 
 #include "swiglu_moe.h"
 #include "swiglu_ops.h"
+#include "swiglu_tokens.h"
 
 namespace {
 
@@ -224,10 +225,238 @@ PyObject* moe_routed_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
+// ---------------------------------------------------------------- tokens to experts and back
+
+// [M, D] rows of `type`, each contiguous, none overlapping.
+bool rows_of(const Arg& a, int64_t M, int64_t D, at::ScalarType type, at::Device device) {
+    if (!a.t) return true;
+    const Tensor& t = *a.t;
+    return t.dim() == 2 && t.size(0) == M && t.size(1) == D && t.stride(1) == 1 && t.stride(0) >= D && t.scalar_type() == type &&
+           t.device() == device;
+}
+
+// Rows of one of the element types on the current device.
+bool rows_alone(const Arg& a, int* code) {
+    if (!a.ok || !a.t || a.t->dim() != 2) return false;
+    *code = code_of(a.t->scalar_type());
+    return *code >= 0 && rows_like(a, *a.t) && on_current_device(a.t->device());
+}
+
+bool pairs_of(const Arg& a, int64_t T, int64_t k, at::ScalarType type, at::Device device) {
+    return a.ok && a.t && contiguous(a, {T, k}, type, device);
+}
+
+// A whole number in 0 .. 2^63 - 1 (larger ones, which are rare, are taken by binding.py).
+bool whole(PyObject* o, int64_t* v) {
+    if (!PyLong_CheckExact(o)) return false;
+    int over = 0;
+    *v = PyLong_AsLongLongAndOverflow(o, &over);
+    return !over && *v >= 0;
+}
+
+// (p, seed, offset, step) of a dropout.
+struct Mask {
+    double p = 0;
+    int64_t seed = 0, offset = 0;
+    Arg step;
+    bool ok;
+    Mask(PyObject* const* args, at::Device device) : step(args[3], true) {
+        ok = PyFloat_CheckExact(args[0]) && whole(args[1], &seed) && whole(args[2], &offset) && step.ok &&
+             (!step.t || (step.t->dim() == 0 && step.t->scalar_type() == at::kLong && step.t->device() == device));
+        if (ok) p = PyFloat_AS_DOUBLE(args[0]);
+    }
+    const int64_t* at() const { return static_cast<const int64_t*>(step.data()); }
+};
+
+// (logits, top_k, renormalize) -> (ids, gates)
+PyObject* moe_gate_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 3) Py_RETURN_NONE;
+        const Arg l(args[0], false);
+        int64_t k;
+        int code;
+        const int renorm = PyObject_IsTrue(args[2]);
+        if (renorm < 0) return nullptr;
+        if (!whole(args[1], &k) || !rows_alone(l, &code) || k < 1 || k > l.t->size(1)) Py_RETURN_NONE;
+        const int64_t T = l.t->size(0), E = l.t->size(1);
+        const at::Device device = l.t->device();
+        Tensor ids = fresh({T, k}, at::kInt, device), gates = fresh({T, k}, at::kFloat, device);
+        const int st = released([&] {
+            return swiglu_moe_gate_fwd(l.data(), l.stride(), ids.data_ptr<int>(), gates.data_ptr<float>(), T, E, k, renorm, code,
+                stream_of(device));
+        });
+        if (st) return PyLong_FromLong(st);
+        return tuple_of({THPVariable_Wrap(std::move(ids)), THPVariable_Wrap(std::move(gates))});
+    });
+}
+
+// (logits, ids, gates, dgates, renormalize) -> dlogits
+PyObject* moe_gate_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 5) Py_RETURN_NONE;
+        const Arg l(args[0], false), ids(args[1], false), q(args[2], false), dq(args[3], false);
+        int code;
+        const int renorm = PyObject_IsTrue(args[4]);
+        if (renorm < 0) return nullptr;
+        if (!rows_alone(l, &code) || !ids.ok || ids.t->dim() != 2) Py_RETURN_NONE;
+        const int64_t T = l.t->size(0), E = l.t->size(1), k = ids.t->size(1);
+        const at::Device device = l.t->device();
+        if (k < 1 || k > E || !pairs_of(ids, T, k, at::kInt, device) || !pairs_of(q, T, k, at::kFloat, device) ||
+            !pairs_of(dq, T, k, at::kFloat, device))
+            Py_RETURN_NONE;
+        Tensor d = fresh({T, E}, l.t->scalar_type(), device);
+        const int st = released([&] {
+            return swiglu_moe_gate_bwd(l.data(), l.stride(), ids.t->data_ptr<int>(), q.t->data_ptr<float>(), dq.t->data_ptr<float>(),
+                d.data_ptr(), E, T, E, k, renorm, code, stream_of(device));
+        });
+        if (st) return PyLong_FromLong(st);
+        return THPVariable_Wrap(std::move(d));
+    });
+}
+
+// (ids, E) -> (counts, pos)
+PyObject* moe_sort(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 2) Py_RETURN_NONE;
+        const Arg ids(args[0], false);
+        int64_t E;
+        if (!whole(args[1], &E) || E > 1024 || !ids.ok || ids.t->scalar_type() != at::kInt || !ids.t->is_contiguous() ||
+            !on_current_device(ids.t->device()))
+            Py_RETURN_NONE;
+        const at::Device device = ids.t->device();
+        Tensor counts = fresh({E}, at::kInt, device), pos = fresh(ids.t->sizes(), at::kInt, device);
+        const int st = released([&] {
+            return swiglu_moe_sort(ids.t->data_ptr<int>(), counts.data_ptr<int>(), pos.data_ptr<int>(), ids.t->numel(), E, stream_of(device));
+        });
+        if (st) return PyLong_FromLong(st);
+        return tuple_of({THPVariable_Wrap(std::move(counts)), THPVariable_Wrap(std::move(pos))});
+    });
+}
+
+// (x, pos, n_rows or None: one for each pair) -> rows
+PyObject* moe_dispatch_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 3) Py_RETURN_NONE;
+        const Arg x(args[0], false), pos(args[1], false);
+        int code;
+        if (!rows_alone(x, &code) || !pos.ok || pos.t->dim() != 2) Py_RETURN_NONE;
+        const int64_t T = x.t->size(0), D = x.t->size(1), k = pos.t->size(1);
+        const at::Device device = x.t->device();
+        int64_t rows = T * k;
+        if (!pairs_of(pos, T, k, at::kInt, device) || (args[2] != Py_None && !whole(args[2], &rows))) Py_RETURN_NONE;
+        Tensor out = fresh({rows, D}, x.t->scalar_type(), device);
+        const int st = released([&] {
+            return swiglu_moe_dispatch_fwd(x.data(), x.stride(), pos.t->data_ptr<int>(), out.data_ptr(), D, T, D, k, rows, code,
+                stream_of(device));
+        });
+        if (st) return PyLong_FromLong(st);
+        return THPVariable_Wrap(std::move(out));
+    });
+}
+
+// (drows, pos, add) -> dx
+PyObject* moe_dispatch_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 3) Py_RETURN_NONE;
+        const Arg d(args[0], false), pos(args[1], false), add(args[2], true);
+        int code;
+        if (!rows_alone(d, &code) || !pos.ok || pos.t->dim() != 2 || !add.ok) Py_RETURN_NONE;
+        const int64_t rows = d.t->size(0), D = d.t->size(1), T = pos.t->size(0), k = pos.t->size(1);
+        const at::Device device = d.t->device();
+        const at::ScalarType type = d.t->scalar_type(), atype = add.t && add.t->scalar_type() == at::kFloat ? at::kFloat : type;
+        if (!pairs_of(pos, T, k, at::kInt, device) || !rows_of(add, T, D, atype, device)) Py_RETURN_NONE;
+        Tensor dx = fresh({T, D}, type, device);
+        const int st = released([&] {
+            return swiglu_moe_dispatch_bwd(d.data(), d.stride(), pos.t->data_ptr<int>(), add.data(), add.stride(), dx.data_ptr(), D, T, D,
+                k, rows, code, code_of(atype), stream_of(device));
+        });
+        if (st) return PyLong_FromLong(st);
+        return THPVariable_Wrap(std::move(dx));
+    });
+}
+
+// (rows, pos, gates, residual, p, seed, offset, step) -> y
+PyObject* moe_combine_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 8) Py_RETURN_NONE;
+        const Arg rows(args[0], false), pos(args[1], false), gates(args[2], false), r(args[3], true);
+        int code;
+        if (!rows_alone(rows, &code) || !pos.ok || pos.t->dim() != 2 || !r.ok) Py_RETURN_NONE;
+        const int64_t R = rows.t->size(0), D = rows.t->size(1), T = pos.t->size(0), k = pos.t->size(1);
+        const at::Device device = rows.t->device();
+        const at::ScalarType type = rows.t->scalar_type();
+        const Mask m(args + 4, device);
+        if (!m.ok || !pairs_of(pos, T, k, at::kInt, device) || !pairs_of(gates, T, k, at::kFloat, device) ||
+            !rows_of(r, T, D, type, device))
+            Py_RETURN_NONE;
+        Tensor y = fresh({T, D}, type, device);
+        const int st = released([&] {
+            return swiglu_moe_combine_fwd(rows.data(), rows.stride(), pos.t->data_ptr<int>(), gates.t->data_ptr<float>(), r.data(),
+                r.stride(), y.data_ptr(), D, T, D, k, R, code, m.p, m.seed, m.offset, m.at(), stream_of(device));
+        });
+        if (st) return PyLong_FromLong(st);
+        return THPVariable_Wrap(std::move(y));
+    });
+}
+
+// (dy, rows, pos, gates, p, seed, offset, step) -> (drows, dgates)
+PyObject* moe_combine_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 8) Py_RETURN_NONE;
+        const Arg dy(args[0], false), rows(args[1], false), pos(args[2], false), gates(args[3], false);
+        int code;
+        if (!rows_alone(rows, &code) || !pos.ok || pos.t->dim() != 2 || !dy.ok) Py_RETURN_NONE;
+        const int64_t R = rows.t->size(0), D = rows.t->size(1), T = pos.t->size(0), k = pos.t->size(1);
+        const at::Device device = rows.t->device();
+        const at::ScalarType type = rows.t->scalar_type();
+        const Mask m(args + 4, device);
+        if (!m.ok || !pairs_of(pos, T, k, at::kInt, device) || !pairs_of(gates, T, k, at::kFloat, device) ||
+            !rows_of(dy, T, D, type, device))
+            Py_RETURN_NONE;
+        Tensor drows = fresh({R, D}, type, device), dgates = fresh({T, k}, at::kFloat, device);
+        const int st = released([&] {
+            return swiglu_moe_combine_bwd(dy.data(), dy.stride(), rows.data(), rows.stride(), pos.t->data_ptr<int>(),
+                gates.t->data_ptr<float>(), drows.data_ptr(), D, dgates.data_ptr<float>(), T, D, k, R, code, m.p, m.seed, m.offset,
+                m.at(), stream_of(device));
+        });
+        if (st) return PyLong_FromLong(st);
+        return tuple_of({THPVariable_Wrap(std::move(drows)), THPVariable_Wrap(std::move(dgates))});
+    });
+}
+
+// (x, residual, p, seed, offset, step) -> y
+PyObject* dropout(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        if (n != 6) Py_RETURN_NONE;
+        const Arg x(args[0], false), r(args[1], true);
+        int code;
+        if (!rows_alone(x, &code) || !r.ok || !rows_like(r, *x.t)) Py_RETURN_NONE;
+        const int64_t M = x.t->size(0), D = x.t->size(1);
+        const at::Device device = x.t->device();
+        const Mask m(args + 2, device);
+        if (!m.ok) Py_RETURN_NONE;
+        Tensor y = fresh({M, D}, x.t->scalar_type(), device);
+        const int st = released([&] {
+            return swiglu_mlp_dropout(x.data(), x.stride(), r.data(), r.stride(), y.data_ptr(), D, M, D, code, m.p, m.seed, m.offset,
+                m.at(), stream_of(device));
+        });
+        if (st) return PyLong_FromLong(st);
+        return THPVariable_Wrap(std::move(y));
+    });
+}
+
 PyMethodDef methods[] = {{"layer_norm_fwd", (PyCFunction)(void (*)())layer_norm_fwd, METH_FASTCALL, nullptr},
                          {"layer_norm_bwd", (PyCFunction)(void (*)())layer_norm_bwd, METH_FASTCALL, nullptr},
                          {"clip_grads", (PyCFunction)(void (*)())clip_grads, METH_FASTCALL, nullptr},
                          {"moe_routed_fwd", (PyCFunction)(void (*)())moe_routed_fwd, METH_FASTCALL, nullptr},
+                         {"moe_gate_fwd", (PyCFunction)(void (*)())moe_gate_fwd, METH_FASTCALL, nullptr},
+                         {"moe_gate_bwd", (PyCFunction)(void (*)())moe_gate_bwd, METH_FASTCALL, nullptr},
+                         {"moe_sort", (PyCFunction)(void (*)())moe_sort, METH_FASTCALL, nullptr},
+                         {"moe_dispatch_fwd", (PyCFunction)(void (*)())moe_dispatch_fwd, METH_FASTCALL, nullptr},
+                         {"moe_dispatch_bwd", (PyCFunction)(void (*)())moe_dispatch_bwd, METH_FASTCALL, nullptr},
+                         {"moe_combine_fwd", (PyCFunction)(void (*)())moe_combine_fwd, METH_FASTCALL, nullptr},
+                         {"moe_combine_bwd", (PyCFunction)(void (*)())moe_combine_bwd, METH_FASTCALL, nullptr},
+                         {"dropout", (PyCFunction)(void (*)())dropout, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_short_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
