@@ -11,7 +11,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxExperts = 1024;
-constexpr int kGateWarps = 4;
+constexpr int kGateThreads = 128;
 
 struct Gate {
     const void* logits;
@@ -32,121 +32,307 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+// A token's logits belong to a group of G lanes of a warp.  A lane has OWN of them, in runs of RUN
+// consecutive experts; its i-th one (rising with i):
+template <int G, int RUN>
+__device__ __forceinline__ int expert(int i) {
+    return (i / RUN * G + (threadIdx.x & (G - 1))) * RUN + i % RUN;
 }
-
-// A token's logits, lane's own of them in registers (experts lane + 32 i), their largest (0 where none
-// is above minus infinity) and the sum of the exponentials.
-template <class T, int OWN>
-struct Logits {
-    float v[OWN], top, sum;
-    __device__ __forceinline__ Logits(const Gate& a, int64_t t) {
-        const int lane = threadIdx.x & 31;
-        const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-        top = -INFINITY;
+template <int G>
+struct Group {
+    static __device__ __forceinline__ int lane() { return threadIdx.x & (G - 1); }
+    static __device__ __forceinline__ int64_t token() { return ((int64_t)blockIdx.x * kGateThreads + threadIdx.x) / G; }
+    static __device__ __forceinline__ uint32_t max(uint32_t v) {
+        if constexpr (G == 32) {
+            v = __reduce_max_sync(0xffffffffu, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-            v[i] = lane + 32 * i < a.E ? to_f32(row[lane + 32 * i]) : -INFINITY;
-            top = fmaxf(top, v[i]);
+            for (int o = G / 2; o; o >>= 1) v = ::max(v, __shfl_xor_sync(0xffffffffu, v, o));
         }
-        top = warp_max(top);
-        if (top == -INFINITY) top = 0.f;
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < OWN; ++i) sum += expf(v[i] - top);
-        sum = warp_sum(sum);
+        return v;
     }
+    static __device__ __forceinline__ float max(float v) {
+#pragma unroll
+        for (int o = G / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    }
+    static __device__ __forceinline__ float sum(float v) {
+#pragma unroll
+        for (int o = G / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    template <class V>
+    static __device__ __forceinline__ V of(V v, int lane) { return __shfl_sync(0xffffffffu, v, lane, G); }
 };
 
-// One warp a token.
-template <class T, int OWN>
-__global__ void __launch_bounds__(kGateWarps * 32) moe_gate_fwd_kernel(const Gate a) {
-    const int64_t t = (int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (t >= a.T) return;
-    const Logits<T, OWN> l(a, t);
-    uint32_t key[OWN];
+template <class T, int N>
+struct alignas(N * sizeof(T)) Run {
+    T v[N];
+};
+
+// The lane's own logits; minus infinity past the row's end (and for a token past the last).  A run is one
+// load (the gradient of 65536 tokens of 128 experts, fp32: 12.3 us with runs of 4, 13.7 without).
+template <class T, int OWN, int G, int RUN>
+__device__ __forceinline__ void load_logits(float* v, const Gate& a, int64_t t) {
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    const int E = t < a.T ? a.E : 0;
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) key[i] = lane + 32 * i < a.E ? logit_key(l.v[i]) : 0;
+    for (int i = 0; i < OWN; i += RUN) {
+        const int e = expert<G, RUN>(i);
+        Run<T, RUN> r;
+        if (e < E) r = *reinterpret_cast<const Run<T, RUN>*>(row + e);
+#pragma unroll
+        for (int j = 0; j < RUN; ++j) v[i + j] = e < E ? to_f32(r.v[j]) : -INFINITY;
+    }
+}
+
+template <int OWN, int G>
+__device__ __forceinline__ float exp_sum(const float* v, float top) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) sum += expf(v[i] - top);
+    return Group<G>::sum(sum);
+}
+
+// Batcher's odd-even merge sort, largest first.  Every index is a template's, so that the words stay
+// in registers.
+template <int A, int B>
+__device__ __forceinline__ void order(uint32_t* w) {
+    const uint32_t hi = max(w[A], w[B]), lo = min(w[A], w[B]);
+    w[A] = hi, w[B] = lo;
+}
+template <int I, int END, int R>
+__device__ __forceinline__ void order_pairs(uint32_t* w) {
+    if constexpr (I + R < END) {
+        order<I, I + R>(w);
+        order_pairs<I + 2 * R, END, R>(w);
+    }
+}
+// Merges the halves of w[AT] .. w[AT + N - 1], of which every R-th word is meant.
+template <int AT, int N, int R>
+__device__ __forceinline__ void merge_words(uint32_t* w) {
+    if constexpr (2 * R < N) {
+        merge_words<AT, N, 2 * R>(w);
+        merge_words<AT + R, N, 2 * R>(w);
+        order_pairs<AT + R, AT + N, R>(w);
+    } else {
+        order<AT, AT + R>(w);
+    }
+}
+template <int AT, int N>
+__device__ __forceinline__ void sort_words(uint32_t* w) {
+    if constexpr (N > 1) {
+        sort_words<AT, N / 2>(w);
+        sort_words<AT + N / 2, N / 2>(w);
+        merge_words<AT, N, 1>(w);
+    }
+}
+
+// The choices by whole keys, one after the other: the largest that is left, of equal ones the lowest
+// index.  Lane j has the choice j0 + j of each run of G; the gates of a run that is not the last wait
+// in memory, as exponentials, until all are known.
+template <class T, int OWN, int G>
+__device__ __noinline__ void choose_by_keys(const Gate& a, int64_t t) {
+    const int lane = Group<G>::lane();
+    float v[OWN], top = -INFINITY;
+    uint32_t key[OWN];
+    load_logits<T, OWN, G, 1>(v, a, t);
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        top = fmaxf(top, v[i]);
+        key[i] = expert<G, 1>(i) < a.E ? logit_key(v[i]) : 0;
+    }
+    top = Group<G>::max(top);
+    if (top == -INFINITY) top = 0.f;
+    const float total = exp_sum<OWN, G>(v, top);
     int* ids = a.ids + t * a.k;
     float* gates = a.gates + t * a.k;
     float chosen = 0.f, p;
     int mine;
-    for (int j0 = 0; j0 < a.k; j0 += 32) {                 // lane j: choice j0 + j
-        const int n = min(32, a.k - j0);
+    for (int j0 = 0; j0 < a.k; j0 += G) {
+        const int n = min(G, a.k - j0);
         mine = -1, p = 0.f;
         for (int j = 0; j < n; ++j) {
             uint32_t best = key[0];
-            float v = l.v[0];
-            int at = 0;
+            float value = v[0];
+            int at = expert<G, 1>(0);
 #pragma unroll
             for (int i = 1; i < OWN; ++i)
-                if (key[i] > best) best = key[i], v = l.v[i], at = i;
-            const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-            if (high == 0) break;                          // no expert is left
-            const int e = __reduce_min_sync(0xffffffffu, best == high ? lane + 32 * at : kMaxExperts);
-            v = __shfl_sync(0xffffffffu, v, e & 31);
+                if (key[i] > best) best = key[i], value = v[i], at = expert<G, 1>(i);
+            const uint32_t high = Group<G>::max(best);
+            const int e = kMaxExperts - (int)Group<G>::max(best == high ? (uint32_t)(kMaxExperts - at) : 0u);
+            value = Group<G>::of(value, e & (G - 1));
 #pragma unroll
             for (int i = 0; i < OWN; ++i)
-                if (e == lane + 32 * i) key[i] = 0;
-            if (lane == j) mine = e, p = expf(v - l.top);
+                if (e == expert<G, 1>(i)) key[i] = 0;
+            if (lane == j && high != 0) mine = e, p = value;
         }
-        chosen += warp_sum(p);
-        if (lane < n) ids[j0 + lane] = mine;
-        if (j0 + 32 < a.k) gates[j0 + lane] = mine < 0 ? -1.f : p;      // until all are known
+        p = mine < 0 ? 0.f : expf(p - top);
+        chosen += Group<G>::sum(p);
+        if (t < a.T && lane < n) {
+            ids[j0 + lane] = mine;
+            if (j0 + G < a.k) gates[j0 + lane] = mine < 0 ? -1.f : p;
+        }
     }
-    const float by = a.renorm ? chosen : l.sum;
-    auto gate = [&](float e) { return e < 0.f ? 0.f : (isnan(l.sum) ? l.sum : e) / by; };
-    const int last = (a.k - 1) / 32 * 32 + lane;
-    if (last < a.k) gates[last] = gate(mine < 0 ? -1.f : p);
-    for (int j = last - 32; j >= 0; j -= 32) gates[j] = gate(gates[j]);
+    const float by = a.renorm ? chosen + 0.f * total : total;          // total: NaN where a logit is
+    if (t >= a.T) return;
+    const int last = (a.k - 1) / G * G + lane;
+    if (last < a.k) gates[last] = mine < 0 ? 0.f : p / by;
+    for (int j = last - G; j >= 0; j -= G) gates[j] = gates[j] < 0.f ? 0.f : gates[j] / by;
 }
 
+// top_k of more than 32.
 template <class T, int OWN>
-__global__ void __launch_bounds__(kGateWarps * 32) moe_gate_bwd_kernel(const Gate a) {
-    const int64_t t = (int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (t >= a.T) return;
-    // q and g of choice j0 + lane; its id, -1 where it is no expert
-    int id;
-    float q, g;
-    auto load = [&](int j0) {
-        id = j0 + lane < a.k ? a.ids[t * a.k + j0 + lane] : -1, q = g = 0.f;
-        if ((unsigned)id < (unsigned)a.E) q = a.gates[t * a.k + j0 + lane], g = a.dgates[t * a.k + j0 + lane];
-        else id = -1;
-    };
-    float s = 0.f;
-    for (int j0 = (a.k - 1) / 32 * 32; j0 >= 0; j0 -= 32) {
-        load(j0);
-        s += q * g;
-    }
-    s = warp_sum(s);
-    T* out = static_cast<T*>(a.dlogits) + t * a.lddl;
-    float d[OWN];
+__global__ void __launch_bounds__(kGateThreads) moe_gate_fwd_keys_kernel(const __grid_constant__ Gate a) {
+    choose_by_keys<T, OWN, 32>(a, Group<32>::token());
+}
+
+// top_k up to G.  An expert's word has its index in the lowest bits (from all experts down, so that of equal
+// logits the lowest index is the largest word) and as many of the first bits of its key as there is room
+// for: one maximum over the group finds the next choice and who has it, and a lane that keeps its words
+// sorted shows only the first.  These are at least 21 bits, which is all of a 16-bit logit's key.  For fp32
+// the order by words can be wrong only among keys alike in them; where that is among the chosen, or
+// between the last one and the next, the warp chooses by whole keys, and so it does where a logit is NaN.
+template <class T, int OWN, int G>
+__global__ void __launch_bounds__(kGateThreads, OWN > 16 ? 3 : 8) moe_gate_fwd_kernel(const __grid_constant__ Gate a) {
+    constexpr uint32_t kAll = OWN * G, kIndex = 2 * kAll - 1;
+    constexpr int kKeep = OWN > G ? G + 1 : OWN;           // no more than top_k + 1 of a lane's words are asked for
+    const int64_t t = Group<G>::token();
+    const int lane = Group<G>::lane();
+    uint32_t word[OWN];
+    float total = 0.f;
+    {
+        float v[OWN];
+        load_logits<T, OWN, G, 1>(v, a, t);
+        // Places past the row's end, minus infinity too, come after all the row's.
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) d[i] = 0.f;
-    for (int j0 = 0; j0 < a.k; j0 += 32) {
-        if (j0 > 0) load(j0);
-        const float up = a.renorm ? q * (g - s) : g;
-        for (int j = 0; j < min(32, a.k - j0); ++j) {
-            const int e = __shfl_sync(0xffffffffu, id, j);
-            const float u = __shfl_sync(0xffffffffu, up, j);
+        for (int i = 0; i < OWN; ++i) {
+            const uint32_t u = __float_as_uint(v[i] + 0.f);            // -0 counts as 0, each NaN is 0x7fffffff
+            const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+            word[i] = (key & ~kIndex) | (kAll - expert<G, 1>(i));
+        }
+        if (!a.renorm) {
+            float top = v[0];
 #pragma unroll
-            for (int i = 0; i < OWN; ++i)
-                if (e == lane + 32 * i) d[i] += u;
+            for (int i = 1; i < OWN; ++i) top = fmaxf(top, v[i]);
+            top = Group<G>::max(top);
+            total = exp_sum<OWN, G>(v, top == -INFINITY ? 0.f : top);
         }
     }
-    if (!a.renorm) {
-        const Logits<T, OWN> l(a, t);
+    sort_words<0, OWN>(word);
+    bool again = word[0] > (0xffffffffu & ~kIndex);        // a NaN's key is the largest
+    uint32_t mine = 0;
+    for (int j = 0; j < a.k; ++j) {
+        const uint32_t high = Group<G>::max(word[0]);
+        if (lane == j) mine = high;
+        if (word[0] == high) {
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) d[i] = l.sum == 0.f ? 0.f : expf(l.v[i] - l.top) / l.sum * (d[i] - s);
+            for (int i = 0; i + 1 < kKeep; ++i) word[i] = word[i + 1];
+            word[kKeep - 1] = 0;
+        }
     }
+    int e = lane < a.k ? (int)(kAll - (mine & kIndex)) : -1;
+    const float value = e < 0 || t >= a.T ? -INFINITY : to_f32(static_cast<const T*>(a.logits)[t * a.ld + e]);
+    const float top = Group<G>::of(value, 0);
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t next = Group<G>::max(word[0]), after = Group<G>::of(mine, lane + 1);
+        const float other = Group<G>::of(value, lane + 1);
+        again |= lane < a.k - 1 ? (mine ^ after) <= kIndex && value != other : lane == a.k - 1 && (mine ^ next) <= kIndex && value != -INFINITY;
+    }
+    if (__any_sync(0xffffffffu, again)) return choose_by_keys<T, OWN, G>(a, t);
+    if (value == -INFINITY) e = -1;                        // off
+    const float p = e < 0 ? 0.f : expf(value - top);
+    if (a.renorm) total = Group<G>::sum(p);
+    if (t < a.T && lane < a.k) {
+        a.ids[t * a.k + lane] = e;
+        a.gates[t * a.k + lane] = e < 0 ? 0.f : p / total;
+    }
+}
+
+// dlogits_e = q_j (g_j - s) where e is choice j; else 0 (renormalize) or -p_e s.  First the latter for
+// every expert, then the choices in their places.
+template <class T, int OWN, int G, int RUN>
+__global__ void __launch_bounds__(kGateThreads) moe_gate_bwd_kernel(const __grid_constant__ Gate a) {
+    __shared__ uint8_t owners[kGateThreads / G][OWN * G];
+    const int lane = Group<G>::lane();
+    // q and g of choice j0 + lane of token t; its id, -1 where it is no expert
+    struct Choice {
+        int id;
+        float q, g;
+    };
+    auto load = [&](int64_t t, int j0) {
+        Choice c{-1, 0.f, 0.f};
+        if (t < a.T && j0 + lane < a.k) {
+            const int64_t at = t * a.k + j0 + lane;
+            c = Choice{a.ids[at], a.gates[at], a.dgates[at]};
+            if ((unsigned)c.id >= (unsigned)a.E) c = Choice{-1, 0.f, 0.f};
+        }
+        return c;
+    };
+    const int64_t t = Group<G>::token();
+    float d[OWN], s = 0.f;
+    if (!a.renorm) load_logits<T, OWN, G, RUN>(d, a, t);
+    Choice c = load(t, 0);
+    // an index twice (or choices that one load does not hold) makes each expert add up its own
+    uint8_t* owner = owners[threadIdx.x / G];
+    if (c.id >= 0) owner[c.id] = (uint8_t)lane;
+    __syncwarp();
+    const bool sums = __any_sync(0xffffffffu, c.id >= 0 && owner[c.id] != lane) || a.k > G;
+    s = c.q * c.g;
+    for (int j0 = G; j0 < a.k; j0 += G) {
+        const Choice more = load(t, j0);
+        s += more.q * more.g;
+    }
+    s = Group<G>::sum(s);
+    if (a.renorm) {
 #pragma unroll
-    for (int i = 0; i < OWN; ++i)
-        if (lane + 32 * i < a.E) out[lane + 32 * i] = from_f32<T>(d[i]);
+        for (int i = 0; i < OWN; ++i) d[i] = 0.f;
+    } else {
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) top = fmaxf(top, d[i]);
+        top = Group<G>::max(top);
+        if (top == -INFINITY) top = 0.f;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) sum += d[i] = expf(d[i] - top);
+        sum = Group<G>::sum(sum);
+        const float by = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) d[i] *= by;          // p
+    }
+    const float place = c.q * (c.g - s);
+    if (sums) {
+        float up[OWN];
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) up[i] = 0.f;
+        for (int j0 = 0; j0 < a.k; j0 += G) {
+            if (j0 > 0) c = load(t, j0);
+            const float u = a.renorm ? c.q * (c.g - s) : c.g;
+            for (int j = 0; j < min(G, a.k - j0); ++j) {
+                const int e = Group<G>::of(c.id, j);
+                const float w = Group<G>::of(u, j);
+#pragma unroll
+                for (int i = 0; i < OWN; ++i)
+                    if (e == expert<G, RUN>(i)) up[i] += w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) d[i] = a.renorm ? up[i] : d[i] * (up[i] - s);
+        c.id = -1;
+    } else if (!a.renorm) {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) d[i] *= -s;
+    }
+    T* out = static_cast<T*>(a.dlogits) + t * a.lddl;
+#pragma unroll
+    for (int i = 0; i < OWN; i += RUN) {
+        Run<T, RUN> r;
+#pragma unroll
+        for (int j = 0; j < RUN; ++j) r.v[j] = from_f32<T>(d[i + j]);
+        if (t < a.T && expert<G, RUN>(i) < a.E) *reinterpret_cast<Run<T, RUN>*>(out + expert<G, RUN>(i)) = r;
+    }
+    __syncwarp();
+    if (c.id >= 0) out[c.id] = from_f32<T>(place);
 }
 
 // ---------------------------------------------------------------- sort
@@ -241,21 +427,33 @@ __global__ void __launch_bounds__(kSortWarps * 32) moe_sort_kernel(const Sort a)
 
 struct LaunchGate {
     const Gate& a;
-    bool bwd;
+    bool bwd, runs;            // runs: whether rows can be moved four elements at a time
     cudaStream_t s;
-    template <class T, int OWN>
+    template <class T, int OWN, int G>
     cudaError_t go() const {
-        const unsigned grid = (unsigned)((a.T + kGateWarps - 1) / kGateWarps);
-        if (bwd) moe_gate_bwd_kernel<T, OWN><<<grid, kGateWarps * 32, 0, s>>>(a);
-        else moe_gate_fwd_kernel<T, OWN><<<grid, kGateWarps * 32, 0, s>>>(a);
+        const unsigned grid = (unsigned)((a.T * G + kGateThreads - 1) / kGateThreads);
+        if (bwd) {
+            if (runs) moe_gate_bwd_kernel<T, OWN, G, OWN < 4 ? OWN : 4><<<grid, kGateThreads, 0, s>>>(a);
+            else moe_gate_bwd_kernel<T, OWN, G, 1><<<grid, kGateThreads, 0, s>>>(a);
+        } else if (a.k <= G) {
+            moe_gate_fwd_kernel<T, OWN, G><<<grid, kGateThreads, 0, s>>>(a);
+        } else {
+            if constexpr (G == 32) moe_gate_fwd_keys_kernel<T, OWN><<<grid, kGateThreads, 0, s>>>(a);
+        }
         return cudaGetLastError();
     }
+    // Few lanes a token share out its fixed costs best; a lane has up to 16 experts where there are few
+    // enough, and a choice a lane where top_k is at most 32.
     template <class T>
     cudaError_t run() const {
-        return a.E <= 32 ? go<T, 1>() : a.E <= 64 ? go<T, 2>() : a.E <= 128 ? go<T, 4>() : a.E <= 256 ? go<T, 8>()
-             : a.E <= 512 ? go<T, 16>() : go<T, 32>();
+        if (a.k <= 8 && a.E <= 128) return a.E <= 16 ? go<T, 2, 8>() : a.E <= 32 ? go<T, 4, 8>() : a.E <= 64 ? go<T, 8, 8>() : go<T, 16, 8>();
+        if (a.k <= 16 && a.E <= 256) return a.E <= 64 ? go<T, 4, 16>() : a.E <= 128 ? go<T, 8, 16>() : go<T, 16, 16>();
+        return a.E <= 128 ? go<T, 4, 32>() : a.E <= 512 ? go<T, 16, 32>() : go<T, 32, 32>();
     }
 };
+
+// Whether rows of `ld` elements of `n` bytes from p on, E of them used, can be moved four at a time.
+bool in_runs(const void* p, int64_t ld, int64_t E, int n) { return n > 0 && !misaligned(p, 4 * n) && ld % 4 == 0 && E % 4 == 0; }
 
 swiglu_status gate_check(const Gate& a, int64_t E, int64_t k, int type) {
     if (a.T < 0 || E <= 0 || k <= 0 || k > E) return fail(SWIGLU_ERR_INVALID_ARG, "gate: a size is negative or zero, or top_k above E");
@@ -274,38 +472,40 @@ extern "C" {
 
 swiglu_status swiglu_moe_gate_fwd(const void* logits, int64_t ld, int32_t* ids, float* gates, int64_t T, int64_t E,
                                   int64_t top_k, int renormalize, int type, void* stream) {
+    const int n = type_bytes(type);
     const Gate a{logits, nullptr, ids, gates, nullptr, ld, 0, T, (int)E, (int)top_k, renormalize != 0};
     swiglu_status rc = gate_check(a, E, top_k, type);
     if (rc != SWIGLU_OK || T == 0) return rc;
     if (!logits || !ids || !gates) return fail(SWIGLU_ERR_INVALID_ARG, "gate: a required pointer is null");
     if (ld < E) return fail(SWIGLU_ERR_INVALID_ARG, "gate: a row stride is smaller than E");
-    if (misaligned(logits, type_bytes(type)) || misaligned(ids, 4) || misaligned(gates, 4))
+    if (misaligned(logits, n) || misaligned(ids, 4) || misaligned(gates, 4))
         return fail(SWIGLU_ERR_MISALIGNED, "gate: a pointer is not aligned to its element");
     int sms;
     rc = device_sms(&sms);
     if (rc != SWIGLU_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launch_traced(SWIGLU_KERNEL_MOE_GATE, s, [&] { return with_type(type, LaunchGate{a, false, s}); });
+    return launch_traced(SWIGLU_KERNEL_MOE_GATE, s, [&] { return with_type(type, LaunchGate{a, false, false, s}); });
 }
 
 swiglu_status swiglu_moe_gate_bwd(const void* logits, int64_t ld, const int32_t* ids, const float* gates,
                                   const float* dgates, void* dlogits, int64_t lddl, int64_t T, int64_t E,
                                   int64_t top_k, int renormalize, int type, void* stream) {
+    const int n = type_bytes(type);
     const Gate a{logits, dlogits, const_cast<int32_t*>(ids), const_cast<float*>(gates), dgates, ld, lddl, T, (int)E,
                  (int)top_k, renormalize != 0};
+    const bool runs = (renormalize || in_runs(logits, ld, E, n)) && in_runs(dlogits, lddl, E, n);
     swiglu_status rc = gate_check(a, E, top_k, type);
     if (rc != SWIGLU_OK || T == 0) return rc;
     if ((!logits && !renormalize) || !ids || !gates || !dgates || !dlogits)
         return fail(SWIGLU_ERR_INVALID_ARG, "gate: a required pointer is null");
     if ((!renormalize && ld < E) || lddl < E) return fail(SWIGLU_ERR_INVALID_ARG, "gate: a row stride is smaller than E");
-    const size_t n = type_bytes(type);
     if (misaligned(logits, n) || misaligned(dlogits, n) || misaligned(ids, 4) || misaligned(gates, 4) || misaligned(dgates, 4))
         return fail(SWIGLU_ERR_MISALIGNED, "gate: a pointer is not aligned to its element");
     int sms;
     rc = device_sms(&sms);
     if (rc != SWIGLU_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return launch_traced(SWIGLU_KERNEL_MOE_GATE, s, [&] { return with_type(type, LaunchGate{a, true, s}); });
+    return launch_traced(SWIGLU_KERNEL_MOE_GATE, s, [&] { return with_type(type, LaunchGate{a, true, runs, s}); });
 }
 
 swiglu_status swiglu_moe_sort(const int32_t* ids, int32_t* counts, int32_t* pos, int64_t pairs, int64_t E,

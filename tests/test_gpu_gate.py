@@ -86,6 +86,25 @@ def test_ties_go_to_the_lowest_index(b):  # noqa: F811
     assert ids.tolist() == [[0, 1, 2, 3], [0, 2, 4, 6], [0, 1, 2, 3]] and torch.equal(gates, torch.full_like(gates, 0.25))
 
 
+@pytest.mark.parametrize("E", [7, 13, 30, 60, 100, 250, 300, 1000])
+def test_logits_that_differ_in_their_last_bits(b, E):  # noqa: F811
+    """Around +1 and -1, in steps of one to a few units of the last place, some equal; and far apart
+    but for two that end the chosen and begin the rest."""
+    g = torch.Generator().manual_seed(E)
+    T = 64
+    steps = torch.randint(0, 2 * E, (T, E), generator=g)
+    l = (1 + steps.double() * 2.0 ** -23).float()
+    l[::2] = -l[::2]
+    l[40:] = torch.randn(T - 40, E, generator=g)
+    k = min(E - 1, 6)
+    top = torch.sort(l[50:], dim=1, descending=True)
+    l[50:].scatter_(1, top[1][:, k:k + 1], torch.nextafter(top[0][:, k - 1:k], torch.tensor(-9e9)))
+    l = l.cuda()
+    for renormalize in (True, False):
+        for n in (1, 2, k, min(E, 9)):
+            check(b, l, n, renormalize, g)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF, F32], ids=str)
 def test_lowest_values_count_as_values(b, dtype):  # noqa: F811
     low = torch.finfo(dtype).min
