@@ -41,12 +41,12 @@ __device__ __forceinline__ uint4 dropout_block(const Dropout& d, uint64_t offset
     return philox(b, row, (uint32_t)offset, (uint32_t)(offset >> 32), d.key0, d.key1);
 }
 
-// Of kVec<T> columns from c on (c >= -7; EDGE: any, else a multiple of kVec<T>), in order.
-template <class T, bool EDGE>
+// Of kVec<T> columns from c on (c >= -7; WHOLE: a multiple of kVec<T>), in order.
+template <class T, bool WHOLE>
 __device__ __forceinline__ uint4 dropout_bits(const Dropout& d, uint64_t offset, uint32_t row, int c) {
     const int b = c >> 3, o = c & 7;       // rounded down, where c is before the row too
     uint4 v = dropout_block(d, offset, row, (uint32_t)b);
-    if constexpr (EDGE) {
+    if constexpr (!WHOLE) {
         if (o != 0) v = shift_right(v, o + kVec<T> > 8 ? dropout_block(d, offset, row, (uint32_t)b + 1) : v, 2 * o);
     } else if constexpr (kVec<T> == 4) {
         if (o != 0) v.x = v.z, v.y = v.w;

@@ -1,6 +1,7 @@
 // moe_tokens.cu -- tokens to their experts' rows and back, with the gates, dropout and the residual
 // stream, the gradients of both, and dropout alone (include/swiglu_tokens.h).
 #include <algorithm>
+#include <type_traits>
 
 #include "dropout.cuh"
 #include "swiglu_tokens.h"
@@ -10,6 +11,10 @@ namespace {
 
 constexpr int kMaxTop = 1024;
 constexpr int kThreads = 256;
+
+// How the rows of a call lie: all on 16-byte boundaries; off them; or off them, fp32, and moved in singles,
+// which takes fewer instructions than shifted packs but would compute a dropout's bits four times over.
+enum Lie { kWhole, kShifted, kApart };
 
 // ---------------------------------------------------------------- rows to tokens
 
@@ -26,65 +31,105 @@ struct Gather {
     Dropout drop;
 };
 
-// kVec<T> columns of add from c on, added to v.
-template <class T, bool EDGE>
-__device__ __forceinline__ void add_cols(F2* v, const Gather& a, uint32_t t, int c) {
-    F2 f[kVec<T> / 2];
-    if (sizeof(T) == 2 && a.add_fp32) {
-        const float* row = static_cast<const float*>(a.add) + (int64_t)t * a.ldadd;
-        unpack16<float>(load_cols<float, EDGE>(row, c, a.D), f);
-        if constexpr (sizeof(T) == 2) unpack16<float>(load_cols<float, EDGE>(row, c + 4, a.D), f + 2);
-    } else {
-        unpack16<T>(load_cols<T, EDGE>(static_cast<const T*>(a.add) + (int64_t)t * a.ldadd, c, a.D), f);
+// Columns c .. of add_t: of the rows' type, or fp32 beside rows of 16 bits.
+template <class T, int HOW>
+struct AddCols {
+    Cols<T, HOW> v;
+    Cols<float, HOW> f[2];
+    static __device__ __forceinline__ bool wide(const Gather& a) { return sizeof(T) == 2 && a.add_fp32; }
+    __device__ __forceinline__ void load(const Gather& a, uint32_t t, int c) {
+        if (!a.add) return;
+        if (wide(a)) {
+            const float* row = static_cast<const float*>(a.add) + (int64_t)t * a.ldadd;
+            f[0].load(row, c, a.D);
+            f[1].load(row, c + 4, a.D);
+        } else {
+            v.load(static_cast<const T*>(a.add) + (int64_t)t * a.ldadd, c, a.D);
+        }
     }
+    __device__ __forceinline__ void add_to(F2* o, const Gather& a) const {
+        if (!a.add) return;
+        F2 x[4];
+        if (wide(a)) unpack16<float>(f[0].get(), x), unpack16<float>(f[1].get(), x + 2);
+        else unpack16<T>(v.get(), x);
 #pragma unroll
-    for (int i = 0; i < kVec<T> / 2; ++i) v[i] = v[i] + f[i];
-}
+        for (int i = 0; i < kVec<T> / 2; ++i) o[i] = o[i] + x[i];
+    }
+};
 
-// y_t = add_t + drop(sum_j g_tj rows[pos_tj]), a pack of y a thread.
-template <class T, bool EDGE, bool DROP, bool SELF>
-__global__ void __launch_bounds__(kThreads) moe_gather_kernel(const Gather a) {
-    constexpr int V2 = kVec<T> / 2, kAhead = 4;
-    const uint32_t item = blockIdx.x * kThreads + threadIdx.x;
-    const uint32_t n = a.packs.quotient(item), t = a.first + n;
-    if (n >= a.T) return;
-    T* y = static_cast<T*>(a.y) + (int64_t)t * a.ldy;
-    const int c = first_col<T, EDGE>(y, item - n * a.packs.d);
-    if (EDGE && c >= a.D) return;
+// Columns c .. of y_t, AHEAD rows' loads at a time.
+template <class T, int HOW, bool DROP, bool SELF, int AHEAD>
+__device__ __forceinline__ void gather(const Gather& a, uint32_t t, T* y, int c) {
+    constexpr int V2 = kVec<T> / 2;
     const T* rows = static_cast<const T*>(a.rows);
     F2 v[V2];
+    AddCols<T, HOW> add;
     if constexpr (SELF) {
-        unpack16<T>(load_cols<T, EDGE>(rows + (int64_t)t * a.ldrows, c, a.D), v);
+        Cols<T, HOW> x;
+        x.load(rows + (int64_t)t * a.ldrows, c, a.D);
+        add.load(a, t, c);
+        unpack16<T>(x.get(), v);
     } else {
 #pragma unroll
         for (int i = 0; i < V2; ++i) v[i] = f2(0.f);
         const int64_t pair = (int64_t)t * a.k;
-        for (int j0 = 0; j0 < a.k; j0 += kAhead) {
-            uint32_t at[kAhead];
-            uint4 b[kAhead];
-            float g[kAhead];
+        uint32_t at[AHEAD], next[AHEAD];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) at[i] = j0 + i < a.k ? (uint32_t)__ldg(a.pos + pair + j0 + i) : ~0u;
+        for (int i = 0; i < AHEAD; ++i) next[i] = i < a.k ? (uint32_t)__ldg(a.pos + pair + i) : ~0u;
+        for (int j0 = 0; j0 < a.k; j0 += AHEAD) {
+            Cols<T, HOW> x[AHEAD];
+            float g[AHEAD];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (at[i] >= a.n_rows) continue;
-                b[i] = load_cols<T, EDGE>(rows + (int64_t)at[i] * a.ldrows, c, a.D);
-                g[i] = a.gates ? __ldg(a.gates + pair + j0 + i) : 1.f;
+            for (int i = 0; i < AHEAD; ++i) {
+                at[i] = next[i];
+                next[i] = j0 + AHEAD + i < a.k ? (uint32_t)__ldg(a.pos + pair + j0 + AHEAD + i) : ~0u;
+                g[i] = a.gates && j0 + i < a.k ? __ldg(a.gates + pair + j0 + i) : 1.f;
             }
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
+            for (int i = 0; i < AHEAD; ++i)
+                if (at[i] < a.n_rows) x[i].load(rows + (int64_t)at[i] * a.ldrows, c, a.D);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
                 if (at[i] >= a.n_rows) continue;
                 F2 f[V2];
-                unpack16<T>(b[i], f);
+                unpack16<T>(x[i].get(), f);
                 const F2 w = f2(g[i]);
 #pragma unroll
-                for (int x = 0; x < V2; ++x) v[x] = fma(w, f[x], v[x]);
+                for (int q = 0; q < V2; ++q) v[q] = fma(w, f[q], v[q]);
             }
         }
     }
-    if constexpr (DROP) drop<T>(v, dropout_bits<T, EDGE>(a.drop, dropout_offset(a.drop), t, c), a.drop.keep, a.drop.scale);
-    if (a.add) add_cols<T, EDGE>(v, a, t, c);
-    store_cols<T, EDGE>(y, c, a.D, pack16<T>(v));
+    if constexpr (!SELF) add.load(a, t, c);
+    if constexpr (DROP) drop<T>(v, dropout_bits<T, HOW == kOnPacks>(a.drop, dropout_offset(a.drop), t, c), a.drop.keep, a.drop.scale);
+    add.add_to(v, a);
+    store_cols<T, HOW>(y, c, a.D, pack16<T>(v));
+}
+
+// y_t = add_t + drop(sum_j g_tj rows[pos_tj]), a pack of y a thread.
+template <class T, Lie LIE, bool DROP, bool SELF>
+__device__ __forceinline__ void gather_item(const Gather& a) {
+    const uint32_t item = blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t n = a.packs.quotient(item), t = a.first + n;
+    if (n >= a.T) return;
+    T* y = static_cast<T*>(a.y) + (int64_t)t * a.ldy;
+    const int k = item - n * a.packs.d;
+    if constexpr (LIE == kWhole) {
+        gather<T, kOnPacks, DROP, SELF, 2>(a, t, y, k * kVec<T>);
+    } else if constexpr (LIE == kApart) {
+        if (single_col(k) < a.D) gather<T, kSingles, DROP, SELF, 2>(a, t, y, single_col(k));
+    } else {
+        const int c = first_col(y, k);
+        if (c >= 0 && c + kVec<T> <= a.D) gather<T, kInside, DROP, SELF, 2>(a, t, y, c);
+        else if (c < a.D) gather<T, kEnds, DROP, SELF, 1>(a, t, y, c);
+    }
+}
+template <class T, Lie LIE, bool DROP>
+__global__ void __launch_bounds__(kThreads, LIE == kShifted ? 5 : 8) moe_gather_kernel(const __grid_constant__ Gather a) {
+    gather_item<T, LIE, DROP, false>(a);
+}
+template <class T, Lie LIE, bool DROP>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ Gather a) {
+    gather_item<T, LIE, DROP, true>(a);
 }
 
 // ---------------------------------------------------------------- tokens to rows
@@ -102,112 +147,241 @@ struct Scatter {
     Dropout drop;
 };
 
-// rows[pos_tj] = x_t, a pack of x a thread; EDGE: a pack of a row, whose boundaries differ from row to row.
-template <class T, bool EDGE>
-__global__ void __launch_bounds__(kThreads) moe_scatter_kernel(const Scatter a) {
+// rows[pos_tj] = x_t, a pack of x a thread; kShifted: a pack of a row, whose boundaries differ from row to
+// row.
+template <class T, Lie LIE>
+__global__ void __launch_bounds__(kThreads) moe_scatter_kernel(const __grid_constant__ Scatter a) {
     const uint32_t item = blockIdx.x * kThreads + threadIdx.x;
     const uint32_t n = a.packs.quotient(item);
     const int k = item - n * a.packs.d;
     T* out = static_cast<T*>(a.out);
-    if constexpr (EDGE) {
+    if constexpr (LIE != kShifted) {
+        constexpr int how = LIE == kWhole ? kOnPacks : kSingles;
+        const int c = LIE == kWhole ? k * kVec<T> : single_col(k);
+        if (n >= a.T || (LIE == kApart && c >= a.D)) return;
+        const uint32_t t = a.first + n;
+        const uint4 v = load_cols<T, how>(static_cast<const T*>(a.x) + (int64_t)t * a.ldx, c, a.D);
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t at = (uint32_t)__ldg(a.pos + (int64_t)t * a.k + j);
+            if (at < a.n_rows) store_cols<T, how>(out + (int64_t)at * a.ldout, c, a.D, v);
+        }
+    } else {
         const uint32_t m = a.top.quotient(n), t = a.first + m;
         if (m >= a.T) return;
         const uint32_t at = (uint32_t)__ldg(a.pos + (int64_t)t * a.k + (n - m * a.k));
         if (at >= a.n_rows) return;
+        const T* x = static_cast<const T*>(a.x) + (int64_t)t * a.ldx;
         T* to = out + (int64_t)at * a.ldout;
-        const int c = first_col<T, true>(to, k);
-        if (c >= a.D) return;
-        store_cols<T, true>(to, c, a.D, load_cols<T, true>(static_cast<const T*>(a.x) + (int64_t)t * a.ldx, c, a.D));
-    } else {
-        if (n >= a.T) return;
-        const uint32_t t = a.first + n;
-        const int c = k * kVec<T>;
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + (int64_t)t * a.ldx + c);
-        for (int j = 0; j < a.k; ++j) {
-            const uint32_t at = (uint32_t)__ldg(a.pos + (int64_t)t * a.k + j);
-            if (at < a.n_rows) *reinterpret_cast<uint4*>(out + (int64_t)at * a.ldout + c) = v;
-        }
+        const int c = first_col(to, k);
+        if (c >= 0 && c + kVec<T> <= a.D) store_cols<T, kInside>(to, c, a.D, load_cols<T, kInside>(x, c, a.D));
+        else if (c < a.D) store_cols<T, kEnds>(to, c, a.D, load_cols<T, kEnds>(x, c, a.D));
     }
 }
 
+// Columns c .. of drop(dy_t).
+template <class T, int HOW, bool DROP>
+__device__ __forceinline__ void dropped_cols(F2* e, const Scatter& a, uint64_t offset, uint32_t t, int c) {
+    Cols<T, HOW> d;
+    d.load(static_cast<const T*>(a.x) + (int64_t)t * a.ldx, c, a.D);
+    uint4 bits;
+    if constexpr (DROP) bits = dropout_bits<T, HOW == kOnPacks>(a.drop, offset, t, c);
+    unpack16<T>(d.get(), e);
+    if constexpr (DROP) drop<T>(e, bits, a.drop.keep, a.drop.scale);
+}
+
+// Both halves of a warp's sums at once: lane 0 has v0's, lane 16 v1's.
+__device__ __forceinline__ float warp_sums(float v0, float v1) {
+    const bool low = (threadIdx.x & 16) == 0;
+    float v = (low ? v0 : v1) + __shfl_xor_sync(0xffffffffu, low ? v1 : v0, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // The combine's gradient: with e = drop(dy_t), drows[pos_tj] = g_tj e and dgates_tj = <e, rows[pos_tj]>.
-// A CTA a token, kAhead choices at a time (EDGE: one, as their rows' boundaries differ).
-template <class T, bool EDGE, bool DROP>
-__global__ void __launch_bounds__(kThreads) moe_combine_bwd_kernel(const Scatter a) {
-    constexpr int V2 = kVec<T> / 2, kAhead = EDGE ? 1 : 4;
-    __shared__ float part[2][kThreads / 32][kAhead];
+// A CTA a token.  Up to CHOICES choices: all of them at a time, their sums in registers.
+template <class T, Lie LIE, bool DROP, int CHOICES>
+__global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 8 : 6) moe_combine_bwd_few_kernel(const __grid_constant__ Scatter a) {
+    constexpr int V2 = kVec<T> / 2, how = LIE == kWhole ? kOnPacks : kSingles;
+    __shared__ float part[kThreads / 32][CHOICES];
     const uint32_t t = a.first + blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const T *dy = static_cast<const T*>(a.x) + (int64_t)t * a.ldx, *rows = static_cast<const T*>(a.rows);
+    const int64_t pair = (int64_t)t * a.k;
+    uint64_t offset = 0;
+    if constexpr (DROP) offset = dropout_offset(a.drop);
+    uint32_t at[CHOICES];
+    float g[CHOICES];
+    F2 sum[CHOICES];
+#pragma unroll
+    for (int i = 0; i < CHOICES; ++i) {
+        at[i] = i < a.k ? (uint32_t)__ldg(a.pos + pair + i) : ~0u;
+        g[i] = i < a.k ? __ldg(a.gates + pair + i) : 0.f;
+        sum[i] = f2(0.f);
+    }
+    for (int k = threadIdx.x; k < (int)a.packs.d; k += blockDim.x) {
+        const int c = LIE == kWhole ? k * kVec<T> : single_col(k);
+        if (LIE != kWhole && c >= a.D) break;
+        Cols<T, how> d, x[CHOICES];
+        d.load(static_cast<const T*>(a.x) + (int64_t)t * a.ldx, c, a.D);
+#pragma unroll
+        for (int i = 0; i < CHOICES; ++i)
+            if (at[i] < a.n_rows) x[i].load(static_cast<const T*>(a.rows) + (int64_t)at[i] * a.ldrows, c, a.D);
+        uint4 bits;
+        if constexpr (DROP) bits = dropout_bits<T, true>(a.drop, offset, t, c);
+        F2 e[V2];
+        unpack16<T>(d.get(), e);
+        if constexpr (DROP) drop<T>(e, bits, a.drop.keep, a.drop.scale);
+#pragma unroll
+        for (int i = 0; i < CHOICES; ++i) {
+            if (at[i] >= a.n_rows) continue;
+            F2 f[V2];
+            unpack16<T>(x[i].get(), f);
+            const F2 w = f2(g[i]);
+#pragma unroll
+            for (int q = 0; q < V2; ++q) {
+                sum[i] = fma(e[q], f[q], sum[i]);
+                f[q] = w * e[q];
+            }
+            store_cols<T, how>(static_cast<T*>(a.out) + (int64_t)at[i] * a.ldout, c, a.D, pack16<T>(f));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < CHOICES; i += 2) {
+        const float2 s0 = split(sum[i]), s1 = split(sum[i + 1]);
+        const float v = warp_sums(s0.x + s0.y, s1.x + s1.y);
+        if ((lane & 15) == 0) part[warp][i + (lane >> 4)] = v;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < a.k) {
+        float v = 0.f;
+        for (int w = 0; w < warps; ++w) v += part[w][threadIdx.x];
+        a.dgates[pair + threadIdx.x] = v;
+    }
+}
+
+// More choices: two at a time for each pack of dy_t, so that it and its dropout are computed once; `part`: a
+// sum a warp for each choice.
+template <class T, Lie LIE, bool DROP>
+__global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_kernel(const __grid_constant__ Scatter a) {
+    constexpr int V2 = kVec<T> / 2, how = LIE == kWhole ? kOnPacks : kSingles;
+    extern __shared__ float part[];        // [top_k][warps]
+    const uint32_t t = a.first + blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const T* rows = static_cast<const T*>(a.rows);
     T* drows = static_cast<T*>(a.out);
     const int64_t pair = (int64_t)t * a.k;
     uint64_t offset = 0;
     if constexpr (DROP) offset = dropout_offset(a.drop);
-    for (int j0 = 0, buffer = 0; j0 < a.k; j0 += kAhead, buffer ^= 1) {
-        uint32_t at[kAhead];
-        float g[kAhead];
-        F2 sum[kAhead];
+    // every lane takes part in the sums, with a pack or without
+    for (int k0 = warp * 32; k0 < (int)a.packs.d; k0 += blockDim.x) {
+        const int k = k0 + lane, c = LIE == kWhole ? k * kVec<T> : single_col(k);
+        const bool in = LIE == kWhole ? k < (int)a.packs.d : c < a.D;
+        F2 e[V2];
+        if (in) dropped_cols<T, how, DROP>(e, a, offset, t, c);
+        for (int j = 0; j < a.k; j += 2) {
+            const uint32_t at0 = (uint32_t)__ldg(a.pos + pair + j), at1 = j + 1 < a.k ? (uint32_t)__ldg(a.pos + pair + j + 1) : ~0u;
+            const bool in0 = in && at0 < a.n_rows, in1 = in && at1 < a.n_rows;
+            Cols<T, how> x0, x1;
+            if (in0) x0.load(rows + (int64_t)at0 * a.ldrows, c, a.D);
+            if (in1) x1.load(rows + (int64_t)at1 * a.ldrows, c, a.D);
+            F2 s0 = f2(0.f), s1 = s0, f[V2];
+            auto choice = [&](const Cols<T, how>& x, F2& s, uint32_t at, int at_j) {
+                const F2 g = f2(__ldg(a.gates + pair + at_j));
+                unpack16<T>(x.get(), f);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            at[i] = j0 + i < a.k ? (uint32_t)__ldg(a.pos + pair + j0 + i) : ~0u;
-            g[i] = at[i] < a.n_rows ? __ldg(a.gates + pair + j0 + i) : 0.f;
-            sum[i] = f2(0.f);
-        }
-        const T* shape = drows + (int64_t)(at[0] < a.n_rows ? at[0] : 0) * a.ldout;    // EDGE: this row's packs
-        for (int k = threadIdx.x; k < (int)a.packs.d; k += blockDim.x) {
-            const int c = first_col<T, EDGE>(shape, k);
-            if (EDGE && (c >= a.D || at[0] >= a.n_rows)) continue;
-            F2 e[V2];
-            unpack16<T>(load_cols<T, EDGE>(dy, c, a.D), e);
-            uint4 b[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (at[i] < a.n_rows) b[i] = load_cols<T, EDGE>(rows + (int64_t)at[i] * a.ldrows, c, a.D);
-            if constexpr (DROP) drop<T>(e, dropout_bits<T, EDGE>(a.drop, offset, t, c), a.drop.keep, a.drop.scale);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (at[i] >= a.n_rows) continue;
-                F2 f[V2], o[V2];
-                unpack16<T>(b[i], f);
-                const F2 w = f2(g[i]);
-#pragma unroll
-                for (int x = 0; x < V2; ++x) {
-                    sum[i] = fma(e[x], f[x], sum[i]);
-                    o[x] = w * e[x];
+                for (int q = 0; q < V2; ++q) {
+                    s = fma(e[q], f[q], s);
+                    f[q] = g * e[q];
                 }
-                store_cols<T, EDGE>(drows + (int64_t)at[i] * a.ldout, c, a.D, pack16<T>(o));
+                store_cols<T, how>(drows + (int64_t)at * a.ldout, c, a.D, pack16<T>(f));
+            };
+            if (in0) choice(x0, s0, at0, j);
+            if (in1) choice(x1, s1, at1, j + 1);
+            const float2 p0 = split(s0), p1 = split(s1);
+            const float v = warp_sums(p0.x + p0.y, p1.x + p1.y);
+            const int mine = j + (lane >> 4);
+            if ((lane & 15) == 0 && mine < a.k) {
+                float* p = part + mine * warps + warp;
+                *p = k0 < (int)blockDim.x ? v : *p + v;
             }
         }
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
+        float v = 0.f;
+        for (int w = 0; w < warps; ++w) v += part[j * warps + w];
+        a.dgates[pair + j] = v;
+    }
+}
+
+// The same of rows off 16-byte boundaries, which differ from row to row: `lanes` threads a choice, one warp
+// or the CTA.
+template <class T, bool DROP>
+__global__ void __launch_bounds__(kThreads) moe_combine_bwd_shifted_kernel(const __grid_constant__ Scatter a, int lanes) {
+    constexpr int V2 = kVec<T> / 2;
+    __shared__ float part[kThreads / 32];
+    const int group = lanes == 32 ? threadIdx.x >> 5 : 0, lane = lanes == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const uint32_t p = lanes == 32 ? blockIdx.x * (blockDim.x >> 5) + group : blockIdx.x;
+    const uint32_t n = a.top.quotient(p), t = a.first + n;
+    if (n >= a.T) return;                  // a warp's, where there are more than one choice's
+    const int64_t pair = (int64_t)t * a.k + (p - n * a.k);
+    const uint32_t at = (uint32_t)__ldg(a.pos + pair);
+    F2 sum = f2(0.f);
+    if (at < a.n_rows) {
+        uint64_t offset = 0;
+        if constexpr (DROP) offset = dropout_offset(a.drop);
+        const F2 g = f2(__ldg(a.gates + pair));
+        const T* row = static_cast<const T*>(a.rows) + (int64_t)at * a.ldrows;
+        T* to = static_cast<T*>(a.out) + (int64_t)at * a.ldout;
+        auto item = [&](auto how, int c) {
+            constexpr int kHow = decltype(how)::value;
+            Cols<T, kHow> x;
+            x.load(row, c, a.D);
+            F2 e[V2], f[V2];
+            dropped_cols<T, kHow, DROP>(e, a, offset, t, c);
+            unpack16<T>(x.get(), f);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const float2 s = split(sum[i]);
-            const float v = warp_sum(s.x + s.y);
-            if (lane == 0) part[buffer][warp][i] = v;
-        }
-        __syncthreads();                   // a buffer is rewritten after the other one's barrier
-        if (threadIdx.x < kAhead && j0 + (int)threadIdx.x < a.k) {
-            float v = 0.f;
-            for (int w = 0; w < warps; ++w) v += part[buffer][w][threadIdx.x];
-            a.dgates[pair + j0 + threadIdx.x] = v;
+            for (int q = 0; q < V2; ++q) {
+                sum = fma(e[q], f[q], sum);
+                f[q] = g * e[q];
+            }
+            store_cols<T, kHow>(to, c, a.D, pack16<T>(f));
+        };
+        for (int k = lane; k < (int)a.packs.d; k += lanes) {
+            const int c = first_col(to, k);
+            if (c >= 0 && c + kVec<T> <= a.D) item(std::integral_constant<int, kInside>(), c);
+            else if (c < a.D) item(std::integral_constant<int, kEnds>(), c);
         }
     }
+    const float2 s = split(sum);
+    float v = warp_sum(s.x + s.y);
+    if (lanes > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+        for (int w = 0; w < lanes / 32; ++w) v += part[w];
+    }
+    if (lane == 0) a.dgates[pair] = v;
 }
 
 // ---------------------------------------------------------------- host side
 
-// Whether all rows of a call start and end on 16-byte boundaries.
 struct Rows16 {
     int64_t bits = 0;
     void add(const void* p, int64_t ld, int size) {
         if (p) bits |= (int64_t)(reinterpret_cast<uintptr_t>(p) & 15) | (ld * size & 15);
     }
-    bool whole(int64_t D, int size) const { return ((bits | (D * size)) & 15) == 0; }
+    Lie lie(int64_t D, int size, bool dropping) const {
+        if (((bits | (D * size)) & 15) == 0) return kWhole;
+        return size == 4 && !dropping ? kApart : kShifted;
+    }
 };
 
-// Packs of an output row: EDGE rows may start up to a pack less an element into their first one.
-uint32_t packs_of(int64_t D, int size, bool whole) {
+// Items of an output row, a thread each: packs, of which shifted rows may have one more than they fill (they
+// start up to a pack less an element into their first one), or 32 for 128 columns.
+uint32_t items_of(int64_t D, int size, Lie lie) {
     const int v = 16 / size;
-    return (uint32_t)(whole ? D / v : (D + 2 * v - 2) / v);
+    return (uint32_t)(lie == kWhole ? D / v : lie == kShifted ? (D + 2 * v - 2) / v : (D + 127) / 128 * 32);
 }
 
 // Tokens of a launch, each of `items` threads: kernels number them by 31 bits.
@@ -216,42 +390,61 @@ int64_t tokens_of_launch(int64_t T, int64_t items) {
     return std::min(T, most);
 }
 
-struct LaunchGather {
-    const Gather& a;
-    bool whole, dropping;
-    cudaStream_t s;
-    template <class T, bool EDGE, bool DROP>
-    cudaError_t go() const {
-        const unsigned grid = (unsigned)(((uint64_t)a.T * a.packs.d + kThreads - 1) / kThreads);
-        if (a.pos) moe_gather_kernel<T, EDGE, DROP, false><<<grid, kThreads, 0, s>>>(a);
-        else moe_gather_kernel<T, EDGE, DROP, true><<<grid, kThreads, 0, s>>>(a);
-        return cudaGetLastError();
-    }
+// f.go<T, LIE, DROP>() for a call's rows.
+template <class F>
+struct WithRows {
+    const F& f;
+    Lie lie;
+    bool dropping;
     template <class T>
     cudaError_t run() const {
-        return whole ? (dropping ? go<T, false, true>() : go<T, false, false>())
-                     : (dropping ? go<T, true, true>() : go<T, true, false>());
+        if (lie == kWhole) return dropping ? f.template go<T, kWhole, true>() : f.template go<T, kWhole, false>();
+        if constexpr (sizeof(T) == 4)
+            if (lie == kApart) return f.template go<T, kApart, false>();
+        return dropping ? f.template go<T, kShifted, true>() : f.template go<T, kShifted, false>();
+    }
+};
+
+struct LaunchGather {
+    const Gather& a;
+    cudaStream_t s;
+    template <class T, Lie LIE, bool DROP>
+    cudaError_t go() const {
+        const unsigned grid = (unsigned)(((uint64_t)a.T * a.packs.d + kThreads - 1) / kThreads);
+        if (a.pos) moe_gather_kernel<T, LIE, DROP><<<grid, kThreads, 0, s>>>(a);
+        else dropout_kernel<T, LIE, DROP><<<grid, kThreads, 0, s>>>(a);
+        return cudaGetLastError();
     }
 };
 
 struct LaunchScatter {
     const Scatter& a;
-    bool whole, bwd, dropping;
     cudaStream_t s;
-    template <class T, bool EDGE>
+    template <class T, Lie LIE, bool>
     cudaError_t go() const {
-        if (!bwd) {
-            const uint64_t items = (uint64_t)a.T * a.packs.d * (EDGE ? a.k : 1);
-            moe_scatter_kernel<T, EDGE><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+        const uint64_t items = (uint64_t)a.T * a.packs.d * (LIE == kShifted ? a.k : 1);
+        moe_scatter_kernel<T, LIE><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+};
+
+struct LaunchCombineBwd {
+    const Scatter& a;
+    cudaStream_t s;
+    template <class T, Lie LIE, bool DROP>
+    cudaError_t go() const {
+        if constexpr (LIE == kShifted) {   // a warp for rows of up to 16 packs a lane, where there are many
+            const uint64_t pairs = (uint64_t)a.T * a.k;
+            const int lanes = a.packs.d <= 512 ? 32 : kThreads, threads = lanes == 32 ? 128 : kThreads;
+            moe_combine_bwd_shifted_kernel<T, DROP><<<(unsigned)(lanes == 32 ? (pairs + 3) / 4 : pairs), threads, 0, s>>>(a, lanes);
         } else {
-            const int threads = a.packs.d >= kThreads ? kThreads : (int)(a.packs.d + 31) / 32 * 32;
-            if (dropping) moe_combine_bwd_kernel<T, EDGE, true><<<a.T, threads, 0, s>>>(a);
-            else moe_combine_bwd_kernel<T, EDGE, false><<<a.T, threads, 0, s>>>(a);
+            const int warps = std::min<int>(kThreads / 32, (int)(a.packs.d + 31) / 32);
+            if (a.k <= 2) moe_combine_bwd_few_kernel<T, LIE, DROP, 2><<<a.T, warps * 32, 0, s>>>(a);
+            else if (a.k <= 4) moe_combine_bwd_few_kernel<T, LIE, DROP, 4><<<a.T, warps * 32, 0, s>>>(a);
+            else moe_combine_bwd_kernel<T, LIE, DROP><<<a.T, warps * 32, (size_t)warps * a.k * sizeof(float), s>>>(a);
         }
         return cudaGetLastError();
     }
-    template <class T>
-    cudaError_t run() const { return whole ? go<T, false>() : go<T, true>(); }
 };
 
 swiglu_status tokens_check(int64_t T, int64_t D, int64_t k, int64_t n_rows, int type, const char* sizes, const char* limits,
@@ -273,31 +466,33 @@ swiglu_status run_gather(Gather a, int kind, int64_t T, int type, int add_type, 
     const int n = type_bytes(type);
     Rows16 v;
     v.add(a.rows, a.ldrows, n), v.add(a.y, a.ldy, n), v.add(a.add, a.ldadd, type_bytes(add_type));
-    const bool whole = v.whole(a.D, n);
-    a.packs = Divisor::of(packs_of(a.D, n, whole));
+    const Lie lie = v.lie(a.D, n, dropping);
+    a.packs = Divisor::of(items_of(a.D, n, lie));
     a.add_fp32 = add_type == SWIGLU_FP32;
     const int64_t step = tokens_of_launch(T, a.packs.d);
     for (int64_t t = 0; rc == SWIGLU_OK && t < T; t += step) {
         a.first = (uint32_t)t, a.T = (uint32_t)std::min(step, T - t);
-        rc = launch_traced(kind, s, [&] { return with_type(type, LaunchGather{a, whole, dropping, s}); });
+        const LaunchGather f{a, s};
+        rc = launch_traced(kind, s, [&] { return with_type(type, WithRows<LaunchGather>{f, lie, dropping}); });
     }
     return rc;
 }
 
-swiglu_status run_scatter(Scatter a, int64_t T, int type, bool bwd, bool dropping, cudaStream_t s) {
+template <class Launch>
+swiglu_status run_scatter(Scatter a, int64_t T, int type, bool dropping, cudaStream_t s) {
     int sms;
     swiglu_status rc = device_sms(&sms);
     const int n = type_bytes(type);
     Rows16 v;
     v.add(a.x, a.ldx, n), v.add(a.rows, a.ldrows, n), v.add(a.out, a.ldout, n);
-    const bool whole = v.whole(a.D, n);
-    a.packs = Divisor::of(packs_of(a.D, n, whole));
+    const Lie lie = v.lie(a.D, n, dropping);
+    a.packs = Divisor::of(items_of(a.D, n, lie));
     a.top = Divisor::of((uint32_t)a.k);
-    const int64_t step = bwd ? T : tokens_of_launch(T, (int64_t)a.packs.d * (whole ? 1 : a.k));
+    const int64_t step = tokens_of_launch(T, (int64_t)a.packs.d * (lie == kShifted ? a.k : 1));
     for (int64_t t = 0; rc == SWIGLU_OK && t < T; t += step) {
         a.first = (uint32_t)t, a.T = (uint32_t)std::min(step, T - t);
-        rc = launch_traced(SWIGLU_KERNEL_MOE_SCATTER, s,
-                           [&] { return with_type(type, LaunchScatter{a, whole, bwd, dropping, s}); });
+        const Launch f{a, s};
+        rc = launch_traced(SWIGLU_KERNEL_MOE_SCATTER, s, [&] { return with_type(type, WithRows<Launch>{f, lie, dropping}); });
     }
     return rc;
 }
@@ -321,7 +516,7 @@ swiglu_status swiglu_moe_dispatch_fwd(const void* x, int64_t ldx, const int32_t*
     Scatter a{};
     a.x = x, a.ldx = ldx, a.pos = pos, a.out = rows, a.ldout = ldrows;
     a.D = (int)D, a.k = (int)top_k, a.n_rows = (uint32_t)n_rows;
-    return run_scatter(a, T, type, false, false, static_cast<cudaStream_t>(stream));
+    return run_scatter<LaunchScatter>(a, T, type, false, static_cast<cudaStream_t>(stream));
 }
 
 swiglu_status swiglu_moe_dispatch_bwd(const void* drows, int64_t lddrows, const int32_t* pos, const void* add,
@@ -383,7 +578,7 @@ swiglu_status swiglu_moe_combine_bwd(const void* dy, int64_t lddy, const void* r
         return fail(SWIGLU_ERR_MISALIGNED, "combine: a pointer is not aligned to its element");
     a.x = dy, a.ldx = lddy, a.rows = rows, a.ldrows = ldrows, a.pos = pos, a.gates = gates, a.out = drows, a.ldout = lddrows;
     a.dgates = dgates, a.D = (int)D, a.k = (int)top_k, a.n_rows = (uint32_t)n_rows;
-    return run_scatter(a, T, type, true, a.drop.keep < 65536, static_cast<cudaStream_t>(stream));
+    return run_scatter<LaunchCombineBwd>(a, T, type, a.drop.keep < 65536, static_cast<cudaStream_t>(stream));
 }
 
 swiglu_status swiglu_mlp_dropout(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* y, int64_t ldy,

@@ -56,37 +56,62 @@ __device__ __forceinline__ uint4 shift_right(const uint4& lo, const uint4& hi, u
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 16 bytes of a row that need not start on a 16-byte boundary: columns c .. c + kVec - 1, those past the
-// row's ends as 0.  Whole ones come out of the two aligned packs that hold them (each has at least one
-// element of this row, so nothing outside the tensor's own 16-byte granules is read).
-template <class T>
-__device__ __forceinline__ uint4 load_shifted(const T* row, int c, int D) {
-    if (c < 0 || c + kVec<T> > D) return load_edge(row, c, D);
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
-    const uint4* p = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
-    const unsigned m = (unsigned)(at & 15);
-    const uint4 lo = p[0];
-    if (m == 0) return lo;
-    const uint4 hi = p[1];
-    return shift_right(lo, hi, m);
-}
+// How kVec columns of rows are moved: columns c .. c + kVec - 1 of rows and widths on 16-byte boundaries
+// (kOnPacks); of rows anywhere, all inside them (kInside), or some of them before or past the row
+// (kEnds), which go element by element; or columns c, c + 32, c + 64, c + 96 of fp32 rows anywhere
+// (kSingles), which a warp's accesses take 128 bytes at a time.
+enum How { kOnPacks, kInside, kEnds, kSingles };
 
-// Columns c .. c + kVec - 1 of a row; EDGE: whether rows may lie off 16-byte boundaries or end off them.
-template <class T, bool EDGE>
+// Such columns of a row, loaded and put together in two steps, so that many loads can be on their way:
+// kInside's come out of the two aligned packs that hold them, each of which has at least one of them, so
+// nothing outside the tensor's own 16-byte granules is read.
+template <class T, int HOW>
+struct Cols {
+    uint4 lo, hi;
+    unsigned m;
+    __device__ __forceinline__ void load(const T* row, int c, int D) {
+        if constexpr (HOW == kOnPacks) {
+            lo = *reinterpret_cast<const uint4*>(row + c);
+        } else if constexpr (HOW == kInside) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+            const uint4* p = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
+            m = (unsigned)(at & 15);
+            lo = p[0];
+            hi = p[m != 0];
+        } else if constexpr (HOW == kSingles) {
+            static_assert(sizeof(T) == 4, "fp32 rows");
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
+            lo = make_uint4(p[c], c + 32 < D ? p[c + 32] : 0, c + 64 < D ? p[c + 64] : 0, c + 96 < D ? p[c + 96] : 0);
+        } else {
+            lo = load_edge(row, c, D);
+        }
+    }
+    __device__ __forceinline__ uint4 get() const { return HOW == kInside ? shift_right(lo, hi, m) : lo; }
+};
+template <class T, int HOW>
 __device__ __forceinline__ uint4 load_cols(const T* row, int c, int D) {
-    if constexpr (EDGE) return load_shifted(row, c, D);
-    else return *reinterpret_cast<const uint4*>(row + c);
+    Cols<T, HOW> v;
+    v.load(row, c, D);
+    return v.get();
 }
 // The same of an output, whose packs are taken on its 16-byte boundaries (first_col).
-template <class T, bool EDGE>
+template <class T, int HOW>
 __device__ __forceinline__ void store_cols(T* row, int c, int D, const uint4& v) {
-    if (EDGE && (c < 0 || c + kVec<T> > D)) store_edge(row, c, D, v);
+    if constexpr (HOW == kSingles) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(row);
+        p[c] = v.x;
+        if (c + 32 < D) p[c + 32] = v.y;
+        if (c + 64 < D) p[c + 64] = v.z;
+        if (c + 96 < D) p[c + 96] = v.w;
+    } else if constexpr (HOW == kEnds) store_edge(row, c, D, v);
     else *reinterpret_cast<uint4*>(row + c) = v;
 }
+// Item k of a row moved in singles: its first column (an item may have none).
+__device__ __forceinline__ int single_col(int k) { return (k >> 5) * 128 + (k & 31); }
 // First column of pack k of an output row (up to kVec - 1 before the row).
-template <class T, bool EDGE>
+template <class T>
 __device__ __forceinline__ int first_col(const T* row, int k) {
-    return k * kVec<T> - (EDGE ? (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)) : 0);
+    return k * kVec<T> - (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
