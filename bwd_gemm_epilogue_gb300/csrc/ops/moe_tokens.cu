@@ -12,9 +12,10 @@ namespace {
 constexpr int kMaxTop = 1024;
 constexpr int kThreads = 256;
 
-// How the rows of a call lie: all on 16-byte boundaries; off them; or off them, fp32, and moved in singles,
-// which takes fewer instructions than shifted packs but would compute a dropout's bits four times over.
-enum Lie { kWhole, kShifted, kApart };
+// How the rows of a call lie: all on 16-byte boundaries; off them, but each row alike in all tensors (of
+// one row a token only: dropout); off them; or off them, fp32, and moved in singles, which takes fewer
+// instructions than shifted packs but would compute a dropout's bits four times over.
+enum Lie { kWhole, kAlike, kShifted, kApart };
 
 // ---------------------------------------------------------------- rows to tokens
 
@@ -119,7 +120,7 @@ __device__ __forceinline__ void gather_item(const Gather& a) {
         if (single_col(k) < a.D) gather<T, kSingles, DROP, SELF, 2>(a, t, y, single_col(k));
     } else {
         const int c = first_col(y, k);
-        if (c >= 0 && c + kVec<T> <= a.D) gather<T, kInside, DROP, SELF, 2>(a, t, y, c);
+        if (c >= 0 && c + kVec<T> <= a.D) gather<T, LIE == kAlike ? kAligned : kInside, DROP, SELF, 2>(a, t, y, c);
         else if (c < a.D) gather<T, kEnds, DROP, SELF, 1>(a, t, y, c);
     }
 }
@@ -201,22 +202,20 @@ __device__ __forceinline__ float warp_sums(float v0, float v1) {
 // The combine's gradient: with e = drop(dy_t), drows[pos_tj] = g_tj e and dgates_tj = <e, rows[pos_tj]>.
 // A CTA a token.  Up to CHOICES choices: all of them at a time, their sums in registers.
 template <class T, Lie LIE, bool DROP, int CHOICES>
-__global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 8 : 6) moe_combine_bwd_few_kernel(const __grid_constant__ Scatter a) {
+__global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 6 : CHOICES == 4 ? 4 : 3) moe_combine_bwd_few_kernel(const __grid_constant__ Scatter a) {
     constexpr int V2 = kVec<T> / 2, how = LIE == kWhole ? kOnPacks : kSingles;
     __shared__ float part[kThreads / 32][CHOICES];
     const uint32_t t = a.first + blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t pair = (int64_t)t * a.k;
-    uint64_t offset = 0;
-    if constexpr (DROP) offset = dropout_offset(a.drop);
     uint32_t at[CHOICES];
     float g[CHOICES];
-    F2 sum[CHOICES];
+    float sum[CHOICES];
 #pragma unroll
     for (int i = 0; i < CHOICES; ++i) {
         at[i] = i < a.k ? (uint32_t)__ldg(a.pos + pair + i) : ~0u;
         g[i] = i < a.k ? __ldg(a.gates + pair + i) : 0.f;
-        sum[i] = f2(0.f);
+        sum[i] = 0.f;
     }
     for (int k = threadIdx.x; k < (int)a.packs.d; k += blockDim.x) {
         const int c = LIE == kWhole ? k * kVec<T> : single_col(k);
@@ -227,28 +226,29 @@ __global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 8 : 6) moe_combine_bw
         for (int i = 0; i < CHOICES; ++i)
             if (at[i] < a.n_rows) x[i].load(static_cast<const T*>(a.rows) + (int64_t)at[i] * a.ldrows, c, a.D);
         uint4 bits;
-        if constexpr (DROP) bits = dropout_bits<T, true>(a.drop, offset, t, c);
+        if constexpr (DROP) bits = dropout_bits<T, true>(a.drop, dropout_offset(a.drop), t, c);
         F2 e[V2];
         unpack16<T>(d.get(), e);
         if constexpr (DROP) drop<T>(e, bits, a.drop.keep, a.drop.scale);
 #pragma unroll
         for (int i = 0; i < CHOICES; ++i) {
             if (at[i] >= a.n_rows) continue;
-            F2 f[V2];
+            F2 f[V2], s = f2(0.f);
             unpack16<T>(x[i].get(), f);
             const F2 w = f2(g[i]);
 #pragma unroll
             for (int q = 0; q < V2; ++q) {
-                sum[i] = fma(e[q], f[q], sum[i]);
+                s = fma(e[q], f[q], s);
                 f[q] = w * e[q];
             }
+            const float2 p = split(s);
+            sum[i] += p.x + p.y;
             store_cols<T, how>(static_cast<T*>(a.out) + (int64_t)at[i] * a.ldout, c, a.D, pack16<T>(f));
         }
     }
 #pragma unroll
     for (int i = 0; i < CHOICES; i += 2) {
-        const float2 s0 = split(sum[i]), s1 = split(sum[i + 1]);
-        const float v = warp_sums(s0.x + s0.y, s1.x + s1.y);
+        const float v = warp_sums(sum[i], sum[i + 1]);
         if ((lane & 15) == 0) part[warp][i + (lane >> 4)] = v;
     }
     __syncthreads();
@@ -314,47 +314,54 @@ __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_kernel(const __gr
     }
 }
 
-// The same of rows off 16-byte boundaries, which differ from row to row: `lanes` threads a choice, one warp
-// or the CTA.
-template <class T, bool DROP>
-__global__ void __launch_bounds__(kThreads) moe_combine_bwd_shifted_kernel(const __grid_constant__ Scatter a, int lanes) {
+// Rows off 16-byte boundaries differ from row to row, so each choice has packs of its own.  Columns c .. of
+// drows = g e, and their part of <e, rows>; drop(e, c) makes e of dy.
+template <class T, int HOW, class Drop>
+__device__ __forceinline__ float pair_cols(const T* dy, const T* row, T* to, F2 g, int c, int D, const Drop& drop) {
     constexpr int V2 = kVec<T> / 2;
+    Cols<T, HOW> x, d;
+    x.load(row, c, D);
+    d.load(dy, c, D);
+    F2 e[V2], f[V2], s = f2(0.f);
+    unpack16<T>(d.get(), e);
+    drop(e, c);
+    unpack16<T>(x.get(), f);
+#pragma unroll
+    for (int q = 0; q < V2; ++q) {
+        s = fma(e[q], f[q], s);
+        f[q] = g * e[q];
+    }
+    store_cols<T, HOW>(to, c, D, pack16<T>(f));
+    const float2 p = split(s);
+    return p.x + p.y;
+}
+// Packs k, k + step, ... below `end` of a choice.
+template <class T, class Drop>
+__device__ __forceinline__ float pair_packs(const Scatter& a, uint32_t t, uint32_t at, float g, int k, int end, int step, const Drop& drop) {
+    const T *dy = static_cast<const T*>(a.x) + (int64_t)t * a.ldx, *row = static_cast<const T*>(a.rows) + (int64_t)at * a.ldrows;
+    T* to = static_cast<T*>(a.out) + (int64_t)at * a.ldout;
+    float sum = 0.f;
+    for (; k < end; k += step) {
+        const int c = first_col(to, k);
+        if (c >= 0 && c + kVec<T> <= a.D) sum += pair_cols<T, kInside>(dy, row, to, f2(g), c, a.D, drop);
+        else if (c < a.D) sum += pair_cols<T, kEnds>(dy, row, to, f2(g), c, a.D, drop);
+    }
+    return sum;
+}
+
+// Without dropout: `lanes` threads a choice, one warp (four choices a CTA) or the CTA.
+template <class T>
+__global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_pairs_kernel(const __grid_constant__ Scatter a, int lanes) {
     __shared__ float part[kThreads / 32];
-    const int group = lanes == 32 ? threadIdx.x >> 5 : 0, lane = lanes == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const uint32_t p = lanes == 32 ? blockIdx.x * (blockDim.x >> 5) + group : blockIdx.x;
+    const uint32_t p = lanes == 32 ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+    const int lane = lanes == 32 ? threadIdx.x & 31 : threadIdx.x;
     const uint32_t n = a.top.quotient(p), t = a.first + n;
-    if (n >= a.T) return;                  // a warp's, where there are more than one choice's
+    if (n >= a.T) return;                  // a whole warp, of a CTA that has no barrier
     const int64_t pair = (int64_t)t * a.k + (p - n * a.k);
     const uint32_t at = (uint32_t)__ldg(a.pos + pair);
-    F2 sum = f2(0.f);
-    if (at < a.n_rows) {
-        uint64_t offset = 0;
-        if constexpr (DROP) offset = dropout_offset(a.drop);
-        const F2 g = f2(__ldg(a.gates + pair));
-        const T* row = static_cast<const T*>(a.rows) + (int64_t)at * a.ldrows;
-        T* to = static_cast<T*>(a.out) + (int64_t)at * a.ldout;
-        auto item = [&](auto how, int c) {
-            constexpr int kHow = decltype(how)::value;
-            Cols<T, kHow> x;
-            x.load(row, c, a.D);
-            F2 e[V2], f[V2];
-            dropped_cols<T, kHow, DROP>(e, a, offset, t, c);
-            unpack16<T>(x.get(), f);
-#pragma unroll
-            for (int q = 0; q < V2; ++q) {
-                sum = fma(e[q], f[q], sum);
-                f[q] = g * e[q];
-            }
-            store_cols<T, kHow>(to, c, a.D, pack16<T>(f));
-        };
-        for (int k = lane; k < (int)a.packs.d; k += lanes) {
-            const int c = first_col(to, k);
-            if (c >= 0 && c + kVec<T> <= a.D) item(std::integral_constant<int, kInside>(), c);
-            else if (c < a.D) item(std::integral_constant<int, kEnds>(), c);
-        }
-    }
-    const float2 s = split(sum);
-    float v = warp_sum(s.x + s.y);
+    float v = 0.f;
+    if (at < a.n_rows) v = pair_packs<T>(a, t, at, __ldg(a.gates + pair), lane, (int)a.packs.d, lanes, [](F2*, int) {});
+    v = warp_sum(v);
     if (lanes > 32) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
         __syncthreads();
@@ -364,16 +371,66 @@ __global__ void __launch_bounds__(kThreads) moe_combine_bwd_shifted_kernel(const
     if (lane == 0) a.dgates[pair] = v;
 }
 
+// With dropout: a CTA a token, `split` warps a choice, kSegment columns at a time, of which it is first
+// computed once for all choices, into shared memory, which ones are dropped: a byte for eight columns.
+// (Computed at each choice's packs, which begin anywhere in those eight, 2048 tokens' 4 choices of 8191
+// bf16 columns took 105 us instead of 73.)
+constexpr int kSegment = 32768;
+template <class T>
+__global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_drop_kernel(const __grid_constant__ Scatter a, int split) {
+    constexpr int kPacks = kSegment / kVec<T>;
+    __shared__ uint8_t keep[kSegment / 8 + 2];             // keep[0]: the eight columns before the segment
+    extern __shared__ float part[];                        // [top_k][split]
+    const uint32_t t = a.first + blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t pair = (int64_t)t * a.k;
+    const uint64_t offset = dropout_offset(a.drop);
+    for (int k0 = 0; k0 < (int)a.packs.d; k0 += kPacks) {
+        const int c0 = k0 * kVec<T>;
+        if (k0 > 0) __syncthreads();
+        for (int b = threadIdx.x; b < min(kSegment, a.D - c0 + 7) / 8 + 2; b += blockDim.x)
+            keep[b] = dropout_byte(a.drop, offset, t, (uint32_t)(c0 / 8 - 1 + b));
+        __syncthreads();
+        for (int j = warp / split; j < a.k; j += (blockDim.x >> 5) / split) {
+            const uint32_t at = (uint32_t)__ldg(a.pos + pair + j);
+            float sum = 0.f;
+            if (at < a.n_rows)
+                sum = pair_packs<T>(a, t, at, __ldg(a.gates + pair + j), k0 + warp % split * 32 + lane, min(k0 + kPacks, (int)a.packs.d),
+                                    split * 32, [&](F2* e, int c) {
+                                        const uint8_t* bytes = keep + 1 + ((c - c0) >> 3);
+                                        drop<T>(e, (uint32_t)(bytes[0] | bytes[1] << 8) >> (c & 7), a.drop.scale);
+                                    });
+            sum = warp_sum(sum);
+            if (lane == 0) {
+                float* p = part + j * split + warp % split;
+                *p = k0 == 0 ? sum : *p + sum;
+            }
+        }
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
+        float v = 0.f;
+        for (int w = 0; w < split; ++w) v += part[j * split + w];
+        a.dgates[pair + j] = v;
+    }
+}
+
 // ---------------------------------------------------------------- host side
 
 struct Rows16 {
-    int64_t bits = 0;
+    int64_t bits = 0, first = -1;
+    bool alike = true;
     void add(const void* p, int64_t ld, int size) {
-        if (p) bits |= (int64_t)(reinterpret_cast<uintptr_t>(p) & 15) | (ld * size & 15);
+        if (!p) return;
+        const int64_t base = (int64_t)(reinterpret_cast<uintptr_t>(p) & 15), step = ld * size & 15;
+        bits |= base | step;
+        if (first < 0) first = base << 4 | step;
+        alike = alike && first == (base << 4 | step);
     }
-    Lie lie(int64_t D, int size, bool dropping) const {
+    Lie lie(int64_t D, int size, bool dropping, bool self) const {
         if (((bits | (D * size)) & 15) == 0) return kWhole;
-        return size == 4 && !dropping ? kApart : kShifted;
+        if (size == 4 && !dropping) return kApart;
+        return self && alike ? kAlike : kShifted;
     }
 };
 
@@ -381,7 +438,7 @@ struct Rows16 {
 // start up to a pack less an element into their first one), or 32 for 128 columns.
 uint32_t items_of(int64_t D, int size, Lie lie) {
     const int v = 16 / size;
-    return (uint32_t)(lie == kWhole ? D / v : lie == kShifted ? (D + 2 * v - 2) / v : (D + 127) / 128 * 32);
+    return (uint32_t)(lie == kWhole ? D / v : lie == kApart ? (D + 127) / 128 * 32 : (D + 2 * v - 2) / v);
 }
 
 // Tokens of a launch, each of `items` threads: kernels number them by 31 bits.
@@ -401,6 +458,7 @@ struct WithRows {
         if (lie == kWhole) return dropping ? f.template go<T, kWhole, true>() : f.template go<T, kWhole, false>();
         if constexpr (sizeof(T) == 4)
             if (lie == kApart) return f.template go<T, kApart, false>();
+        if (lie == kAlike) return dropping ? f.template go<T, kAlike, true>() : f.template go<T, kAlike, false>();
         return dropping ? f.template go<T, kShifted, true>() : f.template go<T, kShifted, false>();
     }
 };
@@ -411,19 +469,21 @@ struct LaunchGather {
     template <class T, Lie LIE, bool DROP>
     cudaError_t go() const {
         const unsigned grid = (unsigned)(((uint64_t)a.T * a.packs.d + kThreads - 1) / kThreads);
-        if (a.pos) moe_gather_kernel<T, LIE, DROP><<<grid, kThreads, 0, s>>>(a);
-        else dropout_kernel<T, LIE, DROP><<<grid, kThreads, 0, s>>>(a);
+        if (!a.pos) dropout_kernel<T, LIE, DROP><<<grid, kThreads, 0, s>>>(a);
+        else if constexpr (LIE != kAlike) moe_gather_kernel<T, LIE, DROP><<<grid, kThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
 };
 
+// A row's place differs from its token's, so no rows are alike below.
 struct LaunchScatter {
     const Scatter& a;
     cudaStream_t s;
     template <class T, Lie LIE, bool>
     cudaError_t go() const {
-        const uint64_t items = (uint64_t)a.T * a.packs.d * (LIE == kShifted ? a.k : 1);
-        moe_scatter_kernel<T, LIE><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+        constexpr Lie lie = LIE == kAlike ? kShifted : LIE;
+        const uint64_t items = (uint64_t)a.T * a.packs.d * (lie == kShifted ? a.k : 1);
+        moe_scatter_kernel<T, lie><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
 };
@@ -433,14 +493,22 @@ struct LaunchCombineBwd {
     cudaStream_t s;
     template <class T, Lie LIE, bool DROP>
     cudaError_t go() const {
-        if constexpr (LIE == kShifted) {   // a warp for rows of up to 16 packs a lane, where there are many
+        const int wide = (int)(a.packs.d + 31) / 32;
+        constexpr bool shifted = LIE == kShifted || LIE == kAlike;
+        if constexpr (shifted && DROP) {   // as many warps a choice as there are for all, and as its packs are for
+            int split = 1;
+            while (2 * split * a.k <= kThreads / 32 && 2 * split <= wide) split *= 2;
+            const int warps = std::min(kThreads / 32, split * a.k);
+            moe_combine_bwd_drop_kernel<T><<<a.T, warps * 32, (size_t)a.k * split * sizeof(float), s>>>(a, split);
+        } else if constexpr (shifted) {    // a warp for rows of up to 16 packs a lane
             const uint64_t pairs = (uint64_t)a.T * a.k;
-            const int lanes = a.packs.d <= 512 ? 32 : kThreads, threads = lanes == 32 ? 128 : kThreads;
-            moe_combine_bwd_shifted_kernel<T, DROP><<<(unsigned)(lanes == 32 ? (pairs + 3) / 4 : pairs), threads, 0, s>>>(a, lanes);
+            const int lanes = wide <= 16 ? 32 : kThreads, threads = lanes == 32 ? 128 : kThreads;
+            moe_combine_bwd_pairs_kernel<T><<<(unsigned)(lanes == 32 ? (pairs + 3) / 4 : pairs), threads, 0, s>>>(a, lanes);
         } else {
-            const int warps = std::min<int>(kThreads / 32, (int)(a.packs.d + 31) / 32);
+            const int warps = std::min(kThreads / 32, wide);
             if (a.k <= 2) moe_combine_bwd_few_kernel<T, LIE, DROP, 2><<<a.T, warps * 32, 0, s>>>(a);
             else if (a.k <= 4) moe_combine_bwd_few_kernel<T, LIE, DROP, 4><<<a.T, warps * 32, 0, s>>>(a);
+            else if (a.k <= 8) moe_combine_bwd_few_kernel<T, LIE, DROP, 8><<<a.T, warps * 32, 0, s>>>(a);
             else moe_combine_bwd_kernel<T, LIE, DROP><<<a.T, warps * 32, (size_t)warps * a.k * sizeof(float), s>>>(a);
         }
         return cudaGetLastError();
@@ -466,7 +534,7 @@ swiglu_status run_gather(Gather a, int kind, int64_t T, int type, int add_type, 
     const int n = type_bytes(type);
     Rows16 v;
     v.add(a.rows, a.ldrows, n), v.add(a.y, a.ldy, n), v.add(a.add, a.ldadd, type_bytes(add_type));
-    const Lie lie = v.lie(a.D, n, dropping);
+    const Lie lie = v.lie(a.D, n, dropping, a.pos == nullptr);
     a.packs = Divisor::of(items_of(a.D, n, lie));
     a.add_fp32 = add_type == SWIGLU_FP32;
     const int64_t step = tokens_of_launch(T, a.packs.d);
@@ -485,7 +553,7 @@ swiglu_status run_scatter(Scatter a, int64_t T, int type, bool dropping, cudaStr
     const int n = type_bytes(type);
     Rows16 v;
     v.add(a.x, a.ldx, n), v.add(a.rows, a.ldrows, n), v.add(a.out, a.ldout, n);
-    const Lie lie = v.lie(a.D, n, dropping);
+    const Lie lie = v.lie(a.D, n, dropping, false);
     a.packs = Divisor::of(items_of(a.D, n, lie));
     a.top = Divisor::of((uint32_t)a.k);
     const int64_t step = tokens_of_launch(T, (int64_t)a.packs.d * (lie == kShifted ? a.k : 1));

@@ -56,11 +56,11 @@ __device__ __forceinline__ uint4 shift_right(const uint4& lo, const uint4& hi, u
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// How kVec columns of rows are moved: columns c .. c + kVec - 1 of rows and widths on 16-byte boundaries
-// (kOnPacks); of rows anywhere, all inside them (kInside), or some of them before or past the row
-// (kEnds), which go element by element; or columns c, c + 32, c + 64, c + 96 of fp32 rows anywhere
-// (kSingles), which a warp's accesses take 128 bytes at a time.
-enum How { kOnPacks, kInside, kEnds, kSingles };
+// How kVec columns of rows are moved: columns c .. c + kVec - 1 that start on a 16-byte boundary, c a
+// multiple of kVec (kOnPacks) or any (kAligned); that start anywhere, all inside the row (kInside); some of
+// them before or past the row (kEnds), which go element by element; or columns c, c + 32, c + 64, c + 96
+// of fp32 rows anywhere (kSingles), which a warp's accesses take 128 bytes at a time.
+enum How { kOnPacks, kAligned, kInside, kEnds, kSingles };
 
 // Such columns of a row, loaded and put together in two steps, so that many loads can be on their way:
 // kInside's come out of the two aligned packs that hold them, each of which has at least one of them, so
@@ -70,7 +70,7 @@ struct Cols {
     uint4 lo, hi;
     unsigned m;
     __device__ __forceinline__ void load(const T* row, int c, int D) {
-        if constexpr (HOW == kOnPacks) {
+        if constexpr (HOW == kOnPacks || HOW == kAligned) {
             lo = *reinterpret_cast<const uint4*>(row + c);
         } else if constexpr (HOW == kInside) {
             const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);

@@ -104,7 +104,8 @@ def check_all(b, T, E, k, D, dtype, drop=0.2, p=0.0, ld=None, start=(0, 0, 0, 0)
 # tokens, experts, choices, width: one token; one column; fewer than a pack; ragged and odd widths; one pack
 # more than a CTA's threads; choices past a register block; wide rows
 SHAPES = [(1, 4, 1, 1), (1, 8, 8, 2048), (3, 5, 2, 7), (16, 8, 2, 4096), (37, 6, 3, 8), (33, 40, 7, 1021), (5, 3, 3, 2056),
-          (130, 64, 6, 264), (2, 700, 20, 100), (7, 9, 5, 8193), (3, 2, 1, 65536 + 24), (1000, 16, 4, 36)]
+          (130, 64, 6, 264), (2, 700, 20, 100), (7, 9, 5, 8193), (3, 2, 1, 65536 + 24), (1000, 16, 4, 36),
+          (2, 5, 3, 40001), (3, 4, 2, 32771), (70, 16, 9, 130)]
 
 
 @pytest.mark.parametrize("dtype", [BF, HF, F32], ids=str)
@@ -117,7 +118,7 @@ def test_there_and_back(b, T, E, k, D, dtype):
 @pytest.mark.parametrize("dtype", [BF, F32], ids=str)
 @pytest.mark.parametrize("D,ld,start", [(64, 72, (0, 0, 0, 0)), (64, 65, (0, 0, 0, 0)), (61, 64, (0, 0, 0, 0)), (64, 64, (1, 2, 3, 5)),
                                         (1021, 1021, (3, 0, 1, 6)), (515, 600, (7, 7, 7, 7)), (9, 9, (1, 1, 1, 1)),
-                                        (64, 64, (0, 1, 0, 0)), (4, 5, (2, 1, 3, 0))])
+                                        (64, 64, (0, 1, 0, 0)), (4, 5, (2, 1, 3, 0)), (32768, 32776, (1, 3, 3, 5))])
 def test_rows_at_any_place(b, D, ld, start, dtype):
     check_all(b, 19, 6, 3, D, dtype, p=0.5, ld=ld, start=start)
     check_all(b, 19, 6, 3, D, dtype, ld=ld, start=start, add32=True)
