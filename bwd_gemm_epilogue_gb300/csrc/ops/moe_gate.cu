@@ -184,6 +184,7 @@ __device__ __noinline__ void choose_by_keys(const Gate& a, int64_t t) {
 // top_k of more than 32.
 template <class T, int OWN>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_fwd_keys_kernel(const __grid_constant__ Gate a) {
+    after_previous();
     choose_by_keys<T, OWN, 32>(a, Group<32>::token());
 }
 
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kGateThreads) moe_gate_fwd_keys_kernel(const _
 // between the last one and the next, the warp chooses by whole keys, and so it does where a logit is NaN.
 template <class T, int OWN, int G>
 __global__ void __launch_bounds__(kGateThreads, OWN > 16 ? 3 : 8) moe_gate_fwd_kernel(const __grid_constant__ Gate a) {
+    after_previous();
     constexpr uint32_t kAll = OWN * G, kIndex = 2 * kAll - 1;
     constexpr int kKeep = OWN > G ? G + 1 : OWN;           // no more than top_k + 1 of a lane's words are asked for
     const int64_t t = Group<G>::token();
@@ -253,6 +255,7 @@ __global__ void __launch_bounds__(kGateThreads, OWN > 16 ? 3 : 8) moe_gate_fwd_k
 // every expert, then the choices in their places.
 template <class T, int OWN, int G, int RUN>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_bwd_kernel(const __grid_constant__ Gate a) {
+    after_previous();
     __shared__ uint8_t owners[kGateThreads / G][OWN * G];
     const int lane = Group<G>::lane();
     // q and g of choice j0 + lane of token t; its id, -1 where it is no expert
@@ -352,6 +355,7 @@ struct Sort {
 // experts before, are where its first pair of each expert goes.
 __global__ void __launch_bounds__(kSortWarps * 32) moe_sort_kernel(const Sort a) {
     extern __shared__ int smem[];
+    after_previous();
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* mine = smem;                      // [E] this CTA's pairs of each expert
     int* base = mine + a.E;                // [E] first row of this CTA's pairs
@@ -432,15 +436,12 @@ struct LaunchGate {
     template <class T, int OWN, int G>
     cudaError_t go() const {
         const unsigned grid = (unsigned)((a.T * G + kGateThreads - 1) / kGateThreads);
-        if (bwd) {
-            if (runs) moe_gate_bwd_kernel<T, OWN, G, OWN < 4 ? OWN : 4><<<grid, kGateThreads, 0, s>>>(a);
-            else moe_gate_bwd_kernel<T, OWN, G, 1><<<grid, kGateThreads, 0, s>>>(a);
-        } else if (a.k <= G) {
-            moe_gate_fwd_kernel<T, OWN, G><<<grid, kGateThreads, 0, s>>>(a);
-        } else {
-            if constexpr (G == 32) moe_gate_fwd_keys_kernel<T, OWN><<<grid, kGateThreads, 0, s>>>(a);
-        }
-        return cudaGetLastError();
+        if (bwd)
+            return runs ? launch_early(moe_gate_bwd_kernel<T, OWN, G, OWN < 4 ? OWN : 4>, grid, kGateThreads, 0, s, a)
+                        : launch_early(moe_gate_bwd_kernel<T, OWN, G, 1>, grid, kGateThreads, 0, s, a);
+        if constexpr (G == 32)
+            if (a.k > G) return launch_early(moe_gate_fwd_keys_kernel<T, OWN>, grid, kGateThreads, 0, s, a);
+        return launch_early(moe_gate_fwd_kernel<T, OWN, G>, grid, kGateThreads, 0, s, a);
     }
     // Few lanes a token share out its fixed costs best; a lane has up to 16 experts where there are few
     // enough, and a choice a lane where top_k is at most 32.
@@ -533,12 +534,14 @@ swiglu_status swiglu_moe_sort(const int32_t* ids, int32_t* counts, int32_t* pos,
             if (e != cudaSuccess) return e;
         }
         cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = ctas;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         cfg.gridDim = dim3(ctas);
         cfg.blockDim = dim3(warps * 32);
         cfg.dynamicSmemBytes = smem;

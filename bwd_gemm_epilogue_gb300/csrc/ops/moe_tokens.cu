@@ -126,10 +126,12 @@ __device__ __forceinline__ void gather_item(const Gather& a) {
 }
 template <class T, Lie LIE, bool DROP>
 __global__ void __launch_bounds__(kThreads, LIE == kShifted ? 5 : 8) moe_gather_kernel(const __grid_constant__ Gather a) {
+    after_previous();
     gather_item<T, LIE, DROP, false>(a);
 }
 template <class T, Lie LIE, bool DROP>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ Gather a) {
+    after_previous();
     gather_item<T, LIE, DROP, true>(a);
 }
 
@@ -152,6 +154,7 @@ struct Scatter {
 // row.
 template <class T, Lie LIE>
 __global__ void __launch_bounds__(kThreads) moe_scatter_kernel(const __grid_constant__ Scatter a) {
+    after_previous();
     const uint32_t item = blockIdx.x * kThreads + threadIdx.x;
     const uint32_t n = a.packs.quotient(item);
     const int k = item - n * a.packs.d;
@@ -203,6 +206,7 @@ __device__ __forceinline__ float warp_sums(float v0, float v1) {
 // A CTA a token.  Up to CHOICES choices: all of them at a time, their sums in registers.
 template <class T, Lie LIE, bool DROP, int CHOICES>
 __global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 6 : CHOICES == 4 ? 4 : 3) moe_combine_bwd_few_kernel(const __grid_constant__ Scatter a) {
+    after_previous();
     constexpr int V2 = kVec<T> / 2, how = LIE == kWhole ? kOnPacks : kSingles;
     __shared__ float part[kThreads / 32][CHOICES];
     const uint32_t t = a.first + blockIdx.x;
@@ -263,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 6 : CHOICES == 4 ? 4 
 // sum a warp for each choice.
 template <class T, Lie LIE, bool DROP>
 __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_kernel(const __grid_constant__ Scatter a) {
+    after_previous();
     constexpr int V2 = kVec<T> / 2, how = LIE == kWhole ? kOnPacks : kSingles;
     extern __shared__ float part[];        // [top_k][warps]
     const uint32_t t = a.first + blockIdx.x;
@@ -352,6 +357,7 @@ __device__ __forceinline__ float pair_packs(const Scatter& a, uint32_t t, uint32
 // Without dropout: `lanes` threads a choice, one warp (four choices a CTA) or the CTA.
 template <class T>
 __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_pairs_kernel(const __grid_constant__ Scatter a, int lanes) {
+    after_previous();
     __shared__ float part[kThreads / 32];
     const uint32_t p = lanes == 32 ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     const int lane = lanes == 32 ? threadIdx.x & 31 : threadIdx.x;
@@ -378,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_pairs_kernel(cons
 constexpr int kSegment = 32768;
 template <class T>
 __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_drop_kernel(const __grid_constant__ Scatter a, int split) {
+    after_previous();
     constexpr int kPacks = kSegment / kVec<T>;
     __shared__ uint8_t keep[kSegment / 8 + 2];             // keep[0]: the eight columns before the segment
     extern __shared__ float part[];                        // [top_k][split]
@@ -469,9 +476,9 @@ struct LaunchGather {
     template <class T, Lie LIE, bool DROP>
     cudaError_t go() const {
         const unsigned grid = (unsigned)(((uint64_t)a.T * a.packs.d + kThreads - 1) / kThreads);
-        if (!a.pos) dropout_kernel<T, LIE, DROP><<<grid, kThreads, 0, s>>>(a);
-        else if constexpr (LIE != kAlike) moe_gather_kernel<T, LIE, DROP><<<grid, kThreads, 0, s>>>(a);
-        return cudaGetLastError();
+        if constexpr (LIE != kAlike)
+            if (a.pos) return launch_early(moe_gather_kernel<T, LIE, DROP>, grid, kThreads, 0, s, a);
+        return launch_early(dropout_kernel<T, LIE, DROP>, grid, kThreads, 0, s, a);
     }
 };
 
@@ -483,8 +490,7 @@ struct LaunchScatter {
     cudaError_t go() const {
         constexpr Lie lie = LIE == kAlike ? kShifted : LIE;
         const uint64_t items = (uint64_t)a.T * a.packs.d * (lie == kShifted ? a.k : 1);
-        moe_scatter_kernel<T, lie><<<(unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
-        return cudaGetLastError();
+        return launch_early(moe_scatter_kernel<T, lie>, (unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s, a);
     }
 };
 
@@ -499,19 +505,18 @@ struct LaunchCombineBwd {
             int split = 1;
             while (2 * split * a.k <= kThreads / 32 && 2 * split <= wide) split *= 2;
             const int warps = std::min(kThreads / 32, split * a.k);
-            moe_combine_bwd_drop_kernel<T><<<a.T, warps * 32, (size_t)a.k * split * sizeof(float), s>>>(a, split);
+            return launch_early(moe_combine_bwd_drop_kernel<T>, a.T, warps * 32, (size_t)a.k * split * sizeof(float), s, a, split);
         } else if constexpr (shifted) {    // a warp for rows of up to 16 packs a lane
             const uint64_t pairs = (uint64_t)a.T * a.k;
             const int lanes = wide <= 16 ? 32 : kThreads, threads = lanes == 32 ? 128 : kThreads;
-            moe_combine_bwd_pairs_kernel<T><<<(unsigned)(lanes == 32 ? (pairs + 3) / 4 : pairs), threads, 0, s>>>(a, lanes);
+            return launch_early(moe_combine_bwd_pairs_kernel<T>, (unsigned)(lanes == 32 ? (pairs + 3) / 4 : pairs), threads, 0, s, a, lanes);
         } else {
             const int warps = std::min(kThreads / 32, wide);
-            if (a.k <= 2) moe_combine_bwd_few_kernel<T, LIE, DROP, 2><<<a.T, warps * 32, 0, s>>>(a);
-            else if (a.k <= 4) moe_combine_bwd_few_kernel<T, LIE, DROP, 4><<<a.T, warps * 32, 0, s>>>(a);
-            else if (a.k <= 8) moe_combine_bwd_few_kernel<T, LIE, DROP, 8><<<a.T, warps * 32, 0, s>>>(a);
-            else moe_combine_bwd_kernel<T, LIE, DROP><<<a.T, warps * 32, (size_t)warps * a.k * sizeof(float), s>>>(a);
+            if (a.k <= 2) return launch_early(moe_combine_bwd_few_kernel<T, LIE, DROP, 2>, a.T, warps * 32, 0, s, a);
+            if (a.k <= 4) return launch_early(moe_combine_bwd_few_kernel<T, LIE, DROP, 4>, a.T, warps * 32, 0, s, a);
+            if (a.k <= 8) return launch_early(moe_combine_bwd_few_kernel<T, LIE, DROP, 8>, a.T, warps * 32, 0, s, a);
+            return launch_early(moe_combine_bwd_kernel<T, LIE, DROP>, a.T, warps * 32, (size_t)warps * a.k * sizeof(float), s, a);
         }
-        return cudaGetLastError();
     }
 };
 

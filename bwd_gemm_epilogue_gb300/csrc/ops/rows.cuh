@@ -114,6 +114,12 @@ __device__ __forceinline__ int first_col(const T* row, int k) {
     return k * kVec<T> - (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
 
+// Waits for what the kernels before this one in the stream wrote; the next one may come up from now on.
+__device__ __forceinline__ void after_previous() {
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -133,6 +139,23 @@ cudaError_t with_type(int type, const F& f) {
     if (type == SWIGLU_FP32) return f.template run<float>();
     if (type == SWIGLU_FP16) return f.template run<__half>();
     return f.template run<__nv_bfloat16>();
+}
+
+// A launch that may come up while the kernel before it in the stream ends: the kernel calls
+// after_previous() before it reads or writes anything, and nothing is left of the launch's latency then.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // x / d for 0 <= x < 2^31 and 1 <= d < 2^31 by a product: with 2^(l - 1) < d <= 2^l and
