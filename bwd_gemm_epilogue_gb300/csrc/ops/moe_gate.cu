@@ -364,16 +364,19 @@ __global__ void __launch_bounds__(kSortWarps * 32) moe_sort_kernel(const Sort a)
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
     int* own = hist + warp * a.E;
-    for (int e = lane; e < a.E; e += 32) own[e] = 0;
+    unsigned* lanes = reinterpret_cast<unsigned*>(hist + (warps + warp) * a.E);        // [E] the lanes that have an expert
+    for (int e = lane; e < a.E; e += 32) own[e] = 0, lanes[e] = 0;
     __syncwarp();
     const int64_t begin = ((int64_t)rank * warps + warp) * a.per_warp;
     const int64_t end = min(begin + a.per_warp, a.n);
-    for (int64_t p0 = begin; p0 < end; p0 += 32) {
-        const int e = p0 + lane < end ? a.ids[p0 + lane] : -1;
-        const bool in = (unsigned)e < (unsigned)a.E;
-        const unsigned same = __match_any_sync(0xffffffffu, in ? e : -1);
-        if (in && lane == __ffs(same) - 1) own[e] += __popc(same);
-        __syncwarp();
+    auto load = [&](int64_t p) {
+        const int e = p < end ? a.ids[p] : -1;
+        return (unsigned)e < (unsigned)a.E ? e : a.E;
+    };
+#pragma unroll 4
+    for (int64_t p = begin + lane; p < end; p += 32) {
+        const int e = load(p);
+        if (e < a.E) atomicAdd(own + e, 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
@@ -415,14 +418,17 @@ __global__ void __launch_bounds__(kSortWarps * 32) moe_sort_kernel(const Sort a)
         for (int w = 0; w < warps; ++w) hist[w * a.E + e] += sum;
     }
     __syncthreads();
-    for (int64_t p0 = begin; p0 < end; p0 += 32) {
-        const int e = p0 + lane < end ? a.ids[p0 + lane] : -1;
-        const bool in = (unsigned)e < (unsigned)a.E;
-        const unsigned same = __match_any_sync(0xffffffffu, in ? e : -1);
-        const int first = in ? own[e] : -1;
+    int next = load(begin + lane);
+    for (int64_t p = begin + lane; p - lane < end; p += 32) {
+        const int e = next;
+        next = load(p + 32);
+        if (e < a.E) atomicOr(lanes + e, 1u << lane);
         __syncwarp();
-        if (in && lane == __ffs(same) - 1) own[e] = first + __popc(same);
-        if (p0 + lane < end) a.pos[p0 + lane] = in ? first + __popc(same & ((1u << lane) - 1)) : -1;
+        const unsigned same = e < a.E ? lanes[e] : 0;
+        const int first = e < a.E ? own[e] : -1;
+        __syncwarp();
+        if (e < a.E && same >> lane == 1) own[e] = first + __popc(same), lanes[e] = 0;          // the last of them
+        if (p < end) a.pos[p] = first + __popc(same & ((1u << lane) - 1));
         __syncwarp();
     }
 }
@@ -523,10 +529,11 @@ swiglu_status swiglu_moe_sort(const int32_t* ids, int32_t* counts, int32_t* pos,
     int ctas = 1;
     while (ctas < kSortCtas && pairs > (int64_t)ctas * kSortWarps * 32) ctas *= 2;
     const int64_t runs = (pairs + 31) / 32, per_cta = (runs + ctas - 1) / ctas;
-    const int warps = (int)(per_cta < 4 ? 4 : per_cta < kSortWarps ? per_cta : kSortWarps);
+    const int most = E <= 768 ? kSortWarps : 24;           // of 227 KB
+    const int warps = (int)(per_cta < 4 ? 4 : per_cta < most ? per_cta : most);
     const int64_t per_warp = (per_cta + warps - 1) / warps * 32;
     const Sort a{ids, counts, pos, pairs, per_warp, (int)E};
-    const size_t smem = ((size_t)(warps + 2) * E + 32) * sizeof(int);
+    const size_t smem = ((size_t)(2 * warps + 2) * E + 32) * sizeof(int);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launch_traced(SWIGLU_KERNEL_MOE_SORT, s, [&] {
         if (smem > 48 * 1024) {
