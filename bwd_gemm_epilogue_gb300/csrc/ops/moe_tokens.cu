@@ -130,8 +130,10 @@ __device__ __forceinline__ void gather_item(const Gather& a) {
         if (single_col(k) < a.D) gather<T, kSingles, DROP, SELF, 2>(a, t, y, single_col(k));
     } else {
         const int c = first_col(y, k);
-        if (c >= 0 && c + kVec<T> <= a.D) gather<T, LIE == kAlike ? kAligned : kInside, DROP, SELF, 2>(a, t, y, c);
-        else if (c < a.D) gather<T, kEnds, DROP, SELF, 1>(a, t, y, c);
+        if (c >= a.D) return;
+        const bool packs = LIE == kAlike ? c >= 0 && c + kVec<T> <= a.D : a.D >= kVec<T>;
+        if (packs) gather<T, LIE == kAlike ? kAligned : kAnywhere, DROP, SELF, 2>(a, t, y, c);
+        else gather<T, kElements, DROP, SELF, 1>(a, t, y, c);
     }
 }
 template <class T, Lie LIE, bool DROP>
@@ -160,8 +162,28 @@ struct Scatter {
     Dropout drop;
 };
 
+// Pack k of each of a token's rows, AHEAD of them at a time.
+template <class T, int HOW, int AHEAD>
+__device__ __forceinline__ void scatter_packs(const Scatter& a, const int* pos, const T* x, T* out, int k) {
+    for (int j0 = 0; j0 < a.k; j0 += AHEAD) {
+        uint32_t at[AHEAD];
+        int c[AHEAD];
+        Cols<T, HOW> v[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) at[i] = j0 + i < a.k ? (uint32_t)__ldg(pos + j0 + i) : ~0u;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            c[i] = at[i] < a.n_rows ? first_col(out + (int64_t)at[i] * a.ldout, k) : a.D;
+            if (c[i] < a.D) v[i].load(x, c[i], a.D);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (c[i] < a.D) store_cols<T, HOW>(out + (int64_t)at[i] * a.ldout, c[i], a.D, v[i].get());
+    }
+}
+
 // rows[pos_tj] = x_t, a pack of x a thread; kShifted: a pack of each of the token's rows, whose boundaries
-// differ, kAhead of them at a time (one at a time 4099 tokens' 7 choices of 1021 bf16 columns took 23 us).
+// differ.
 template <class T, Lie LIE>
 __global__ void __launch_bounds__(kThreads) moe_scatter_kernel(const __grid_constant__ Scatter a) {
     after_previous();
@@ -182,25 +204,8 @@ __global__ void __launch_bounds__(kThreads) moe_scatter_kernel(const __grid_cons
             if (at < a.n_rows) store_cols<T, how>(out + (int64_t)at * a.ldout, c, a.D, v);
         }
     } else {
-        constexpr int kAhead = 2;
-        for (int j0 = 0; j0 < a.k; j0 += kAhead) {
-            uint32_t at[kAhead];
-            int c[kAhead];
-            Cols<T, kInside> v[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) at[i] = j0 + i < a.k ? (uint32_t)__ldg(pos + j0 + i) : ~0u;
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                c[i] = at[i] < a.n_rows ? first_col(out + (int64_t)at[i] * a.ldout, k) : a.D;
-                if (c[i] >= 0 && c[i] + kVec<T> <= a.D) v[i].load(x, c[i], a.D);
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                T* to = out + (int64_t)at[i] * a.ldout;
-                if (c[i] >= 0 && c[i] + kVec<T> <= a.D) store_cols<T, kInside>(to, c[i], a.D, v[i].get());
-                else if (c[i] < a.D) store_cols<T, kEnds>(to, c[i], a.D, load_cols<T, kEnds>(x, c[i], a.D));
-            }
-        }
+        if (a.D >= kVec<T>) scatter_packs<T, kAnywhere, 2>(a, pos, x, out, k);
+        else scatter_packs<T, kElements, 1>(a, pos, x, out, k);
     }
 }
 
@@ -370,8 +375,9 @@ __device__ __forceinline__ float pair_packs(const Scatter& a, uint32_t t, uint32
     float sum = 0.f;
     for (; k < end; k += step) {
         const int c = first_col(to, k);
-        if (c >= 0 && c + kVec<T> <= a.D) sum += pair_cols<T, kInside>(dy, row, to, f2(g), c, a.D, drop);
-        else if (c < a.D) sum += pair_cols<T, kEnds>(dy, row, to, f2(g), c, a.D, drop);
+        if (c >= a.D) break;
+        sum += a.D >= kVec<T> ? pair_cols<T, kAnywhere>(dy, row, to, f2(g), c, a.D, drop)
+                              : pair_cols<T, kElements>(dy, row, to, f2(g), c, a.D, drop);
     }
     return sum;
 }

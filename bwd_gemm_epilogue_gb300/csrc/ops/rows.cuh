@@ -57,23 +57,27 @@ __device__ __forceinline__ uint4 shift_right(const uint4& lo, const uint4& hi, u
 }
 
 // How kVec columns of rows are moved: columns c .. c + kVec - 1 that start on a 16-byte boundary, c a
-// multiple of kVec (kOnPacks) or any (kAligned); that start anywhere, all inside the row (kInside); some of
-// them before or past the row (kEnds), which go element by element; or columns c, c + 32, c + 64, c + 96
-// of fp32 rows anywhere (kSingles), which a warp's accesses take 128 bytes at a time.
-enum How { kOnPacks, kAligned, kInside, kEnds, kSingles };
+// multiple of kVec (kOnPacks) or any (kAligned); that start anywhere, some of them possibly before or past a
+// row of kVec columns or more (kAnywhere); the same of any row, element by element (kElements); or columns
+// c, c + 32, c + 64, c + 96 of fp32 rows anywhere (kSingles), which a warp's accesses take 128 bytes at a
+// time.  Columns outside the row are loaded as 0 and not stored.
+enum How { kOnPacks, kAligned, kAnywhere, kElements, kSingles };
 
-// Such columns of a row, loaded and put together in two steps, so that many loads can be on their way:
-// kInside's come out of the two aligned packs that hold them, each of which has at least one of them, so
-// nothing outside the tensor's own 16-byte granules is read.
+// Such columns of a row, loaded and put together in two steps, so that many loads can be on their way.
+// kAnywhere's, moved inside the row where they are not, come out of the two aligned packs that hold them,
+// each of which has at least one of them, so nothing outside the tensor's own 16-byte granules is read.
 template <class T, int HOW>
 struct Cols {
     uint4 lo, hi;
     unsigned m;
+    int moved;
     __device__ __forceinline__ void load(const T* row, int c, int D) {
         if constexpr (HOW == kOnPacks || HOW == kAligned) {
             lo = *reinterpret_cast<const uint4*>(row + c);
-        } else if constexpr (HOW == kInside) {
-            const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+        } else if constexpr (HOW == kAnywhere) {
+            const int inside = min(max(c, 0), D - kVec<T>);
+            moved = (c - inside) * (int)sizeof(T);
+            const uintptr_t at = reinterpret_cast<uintptr_t>(row + inside);
             const uint4* p = reinterpret_cast<const uint4*>(at & ~(uintptr_t)15);
             m = (unsigned)(at & 15);
             lo = p[0];
@@ -86,7 +90,14 @@ struct Cols {
             lo = load_edge(row, c, D);
         }
     }
-    __device__ __forceinline__ uint4 get() const { return HOW == kInside ? shift_right(lo, hi, m) : lo; }
+    __device__ __forceinline__ uint4 get() const {
+        if constexpr (HOW != kAnywhere) return lo;
+        uint4 v = shift_right(lo, hi, m);
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        if (moved > 0) v = shift_right(v, none, moved);
+        else if (moved < 0) v = shift_right(none, v, 16 + moved);
+        return v;
+    }
 };
 template <class T, int HOW>
 __device__ __forceinline__ uint4 load_cols(const T* row, int c, int D) {
@@ -103,8 +114,11 @@ __device__ __forceinline__ void store_cols(T* row, int c, int D, const uint4& v)
         if (c + 32 < D) p[c + 32] = v.y;
         if (c + 64 < D) p[c + 64] = v.z;
         if (c + 96 < D) p[c + 96] = v.w;
-    } else if constexpr (HOW == kEnds) store_edge(row, c, D, v);
-    else *reinterpret_cast<uint4*>(row + c) = v;
+    } else if (HOW == kElements || (HOW == kAnywhere && (c < 0 || c + kVec<T> > D))) {
+        store_edge(row, c, D, v);
+    } else {
+        *reinterpret_cast<uint4*>(row + c) = v;
+    }
 }
 // Item k of a row moved in singles: its first column (an item may have none).
 __device__ __forceinline__ int single_col(int k) { return (k >> 5) * 128 + (k & 31); }
