@@ -128,6 +128,23 @@ def test_infinite_and_nan_logits(b):  # noqa: F811
         assert not d[3:].any()
 
 
+@pytest.mark.parametrize("E", [6, 40, 128, 300])
+def test_nan_of_any_sign_and_payload(b, E):  # noqa: F811
+    """A NaN ranks lowest and makes its token's gates NaN, and no other token's."""
+    for bits in (0x7fc00000, 0xffc00000, 0x7f800001, 0xff800001, 0x7fffffff, 0xffffffff):
+        for dtype, shift in ((F32, 0), (BF, 16)):
+            l = torch.randn(32, E, device="cuda").to(dtype)
+            raw = (bits >> shift) | (1 if shift and not bits & 0x7f0000 else 0)
+            ints, width = (torch.int32, 32) if shift == 0 else (torch.int16, 16)
+            l[5, 2] = torch.tensor([raw - (1 << width) if raw >> (width - 1) else raw], dtype=ints).view(dtype).cuda()[0]
+            assert l.isnan().sum() == 1
+            for renormalize in (True, False):
+                ids, gates = b.swiglu_moe_gate_fwd(l, 3, renormalize)
+                want_ids, want, _ = gate(l, 3, renormalize)
+                assert torch.equal(ids.long(), want_ids) and torch.equal(gates.isnan(), want.isnan())
+                assert gates[5].isnan().all() and not gates[torch.arange(32) != 5].isnan().any()
+
+
 def test_an_index_twice_and_indices_that_are_none(b):  # noqa: F811
     """The gradient takes any ids: shares of one index add up."""
     l = torch.randn(1, 5, device="cuda")
