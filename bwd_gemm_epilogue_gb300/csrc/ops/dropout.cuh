@@ -33,7 +33,7 @@ __device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, u
 }
 
 __device__ __forceinline__ uint64_t dropout_offset(const Dropout& d) {
-    return d.offset + (d.step ? (uint64_t)__ldg(reinterpret_cast<const long long*>(d.step)) : 0);
+    return d.offset + (d.step ? (uint64_t)*d.step : 0);
 }
 
 // The 16 bits of columns 8 b .. 8 b + 7 of a row.

@@ -81,21 +81,21 @@ __device__ __forceinline__ void gather(const Gather& a, uint32_t t, T* y, int c)
 #pragma unroll
         for (int i = 0; i < V2; ++i) v[i] = f2(0.f);
         const int64_t pair = (int64_t)t * a.k;
-        // the sum's last addend is loaded last, when registers are free, out of L2 (8192 tokens' 2 choices of
-        // 4096 bf16 columns: 41.0 us, without 44.5)
-        if (HOW == kOnPacks && a.add) prefetch_add<T>(a, t, c);
-        uint32_t at[AHEAD], next[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) next[i] = i < a.k ? (uint32_t)__ldg(a.pos + pair + i) : ~0u;
-        for (int j0 = 0; j0 < a.k; j0 += AHEAD) {
-            Cols<T, HOW> x[AHEAD];
-            float g[AHEAD];
+        uint32_t at[AHEAD];
+        float g[AHEAD];
+        auto load_pairs = [&](int j0) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
-                at[i] = next[i];
-                next[i] = j0 + AHEAD + i < a.k ? (uint32_t)__ldg(a.pos + pair + j0 + AHEAD + i) : ~0u;
-                g[i] = a.gates && j0 + i < a.k ? __ldg(a.gates + pair + j0 + i) : 1.f;
+                at[i] = j0 + i < a.k ? (uint32_t)a.pos[pair + j0 + i] : ~0u;
+                g[i] = a.gates && j0 + i < a.k ? a.gates[pair + j0 + i] : 1.f;
             }
+        };
+        load_pairs(0);
+        // the sum's last addend is loaded last, when registers are free, out of L2 (8192 tokens' 2 choices of
+        // 4096 bf16 columns: 41.5 us, without 44.5)
+        if (HOW == kOnPacks && a.add) prefetch_add<T>(a, t, c);
+        for (int j0 = 0; j0 < a.k; j0 += AHEAD) {
+            Cols<T, HOW> x[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
                 if (at[i] < a.n_rows) x[i].load(rows + (int64_t)at[i] * a.ldrows, c, a.D);
@@ -108,6 +108,7 @@ __device__ __forceinline__ void gather(const Gather& a, uint32_t t, T* y, int c)
 #pragma unroll
                 for (int q = 0; q < V2; ++q) v[q] = fma(w, f[q], v[q]);
             }
+            load_pairs(j0 + AHEAD);
         }
     }
     if constexpr (!SELF) add.load(a, t, c);
@@ -170,7 +171,7 @@ __device__ __forceinline__ void scatter_packs(const Scatter& a, const int* pos, 
         int c[AHEAD];
         Cols<T, HOW> v[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) at[i] = j0 + i < a.k ? (uint32_t)__ldg(pos + j0 + i) : ~0u;
+        for (int i = 0; i < AHEAD; ++i) at[i] = j0 + i < a.k ? (uint32_t)pos[j0 + i] : ~0u;
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             c[i] = at[i] < a.n_rows ? first_col(out + (int64_t)at[i] * a.ldout, k) : a.D;
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads) moe_scatter_kernel(const __grid_cons
         if (LIE == kApart && c >= a.D) return;
         const uint4 v = load_cols<T, how>(x, c, a.D);
         for (int j = 0; j < a.k; ++j) {
-            const uint32_t at = (uint32_t)__ldg(pos + j);
+            const uint32_t at = (uint32_t)pos[j];
             if (at < a.n_rows) store_cols<T, how>(out + (int64_t)at * a.ldout, c, a.D, v);
         }
     } else {
@@ -244,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 6 : CHOICES == 4 ? 4 
     float sum[CHOICES];
 #pragma unroll
     for (int i = 0; i < CHOICES; ++i) {
-        at[i] = i < a.k ? (uint32_t)__ldg(a.pos + pair + i) : ~0u;
-        g[i] = i < a.k ? __ldg(a.gates + pair + i) : 0.f;
+        at[i] = i < a.k ? (uint32_t)a.pos[pair + i] : ~0u;
+        g[i] = i < a.k ? a.gates[pair + i] : 0.f;
         sum[i] = 0.f;
     }
     for (int k = threadIdx.x; k < (int)a.packs.d; k += blockDim.x) {
@@ -311,14 +312,14 @@ __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_kernel(const __gr
         F2 e[V2];
         if (in) dropped_cols<T, how, DROP>(e, a, offset, t, c);
         for (int j = 0; j < a.k; j += 2) {
-            const uint32_t at0 = (uint32_t)__ldg(a.pos + pair + j), at1 = j + 1 < a.k ? (uint32_t)__ldg(a.pos + pair + j + 1) : ~0u;
+            const uint32_t at0 = (uint32_t)a.pos[pair + j], at1 = j + 1 < a.k ? (uint32_t)a.pos[pair + j + 1] : ~0u;
             const bool in0 = in && at0 < a.n_rows, in1 = in && at1 < a.n_rows;
             Cols<T, how> x0, x1;
             if (in0) x0.load(rows + (int64_t)at0 * a.ldrows, c, a.D);
             if (in1) x1.load(rows + (int64_t)at1 * a.ldrows, c, a.D);
             F2 s0 = f2(0.f), s1 = s0, f[V2];
             auto choice = [&](const Cols<T, how>& x, F2& s, uint32_t at, int at_j) {
-                const F2 g = f2(__ldg(a.gates + pair + at_j));
+                const F2 g = f2(a.gates[pair + at_j]);
                 unpack16<T>(x.get(), f);
 #pragma unroll
                 for (int q = 0; q < V2; ++q) {
@@ -392,9 +393,9 @@ __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_pairs_kernel(cons
     const uint32_t n = a.top.quotient(p), t = a.first + n;
     if (n >= a.T) return;                  // a whole warp, of a CTA that has no barrier
     const int64_t pair = (int64_t)t * a.k + (p - n * a.k);
-    const uint32_t at = (uint32_t)__ldg(a.pos + pair);
+    const uint32_t at = (uint32_t)a.pos[pair];
     float v = 0.f;
-    if (at < a.n_rows) v = pair_packs<T>(a, t, at, __ldg(a.gates + pair), lane, (int)a.packs.d, lanes, [](F2*, int) {});
+    if (at < a.n_rows) v = pair_packs<T>(a, t, at, a.gates[pair], lane, (int)a.packs.d, lanes, [](F2*, int) {});
     v = warp_sum(v);
     if (lanes > 32) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
@@ -427,10 +428,10 @@ __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_drop_kernel(const
             keep[b] = dropout_byte(a.drop, offset, t, (uint32_t)(c0 / 8 - 1 + b));
         __syncthreads();
         for (int j = warp / split; j < a.k; j += (blockDim.x >> 5) / split) {
-            const uint32_t at = (uint32_t)__ldg(a.pos + pair + j);
+            const uint32_t at = (uint32_t)a.pos[pair + j];
             float sum = 0.f;
             if (at < a.n_rows)
-                sum = pair_packs<T>(a, t, at, __ldg(a.gates + pair + j), k0 + warp % split * 32 + lane, min(k0 + kPacks, (int)a.packs.d),
+                sum = pair_packs<T>(a, t, at, a.gates[pair + j], k0 + warp % split * 32 + lane, min(k0 + kPacks, (int)a.packs.d),
                                     split * 32, [&](F2* e, int c) {
                                         const uint8_t* bytes = keep + 1 + ((c - c0) >> 3);
                                         drop<T>(e, (uint32_t)(bytes[0] | bytes[1] << 8) >> (c & 7), a.drop.scale);

@@ -129,6 +129,7 @@ __device__ __forceinline__ int first_col(const T* row, int k) {
 }
 
 // Waits for what the kernels before this one in the stream wrote; the next one may come up from now on.
+// (What they wrote was not constant while this kernel ran, so it is not for ld.global.nc, __ldg's.)
 __device__ __forceinline__ void after_previous() {
     cudaTriggerProgrammaticLaunchCompletion();
     cudaGridDependencySynchronize();
