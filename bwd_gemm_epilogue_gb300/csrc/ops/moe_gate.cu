@@ -1,5 +1,10 @@
 // moe_gate.cu -- the choice of experts from the router's logits and its gradient, and the (token,
 // choice) pairs sorted by expert (include/swiglu_tokens.h).
+//
+// One GB300, device times: the choice of 8 of 128 experts for 65536 tokens (fp32, 38 MB) 15.3 us, bound by
+// integer instructions (141 a token, two thirds of that pipe busy); its gradient 7.3 us, and 11.7 where it
+// needs all experts' probabilities (75 MB), both near HBM's rate; 40961 tokens of 61 experts, bf16, 5.8 us.
+// The sort of 16384 pairs 5.2 us, of 131072 9.6 us.
 #include <cooperative_groups.h>
 
 #include "rows.cuh"
@@ -252,7 +257,9 @@ __global__ void __launch_bounds__(kGateThreads, OWN > 16 ? 3 : 8) moe_gate_fwd_k
 }
 
 // dlogits_e = q_j (g_j - s) where e is choice j; else 0 (renormalize) or -p_e s.  First the latter for
-// every expert, then the choices in their places.
+// every expert, then the choices in their places, which need no search for who has which (with a compare
+// for every choice and expert, and match.any for repeated ones, 65536 tokens of 128 experts took 20 us
+// instead of 7.3).
 template <class T, int OWN, int G, int RUN>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_bwd_kernel(const __grid_constant__ Gate a) {
     after_previous();
@@ -350,9 +357,12 @@ struct Sort {
     int E;
 };
 
-// Counting sort of the pairs by one cluster.  Each warp has a run of consecutive pairs, 32 at a time,
-// and a count for each expert; the counts of all warps, added up over the warps before it and over the
-// experts before, are where its first pair of each expert goes.
+// Counting sort of the pairs by one cluster, in one launch.  Each warp has a run of consecutive pairs, 32
+// at a time, and a count for each expert; the counts of all warps, added up over the warps before it and
+// over the experts before, are where its first pair of each expert goes.  The lanes that have one expert
+// find each other by a bit each in a word of it, so that the order does not depend on timing (131072
+// pairs 9.6 us; by a vote a bit 15.2, by match.any 30).  Latencies bound it: four barriers, two of them the
+// cluster's.
 __global__ void __launch_bounds__(kSortWarps * 32) moe_sort_kernel(const Sort a) {
     extern __shared__ int smem[];
     after_previous();
@@ -449,8 +459,8 @@ struct LaunchGate {
             if (a.k > G) return launch_early(moe_gate_fwd_keys_kernel<T, OWN>, grid, kGateThreads, 0, s, a);
         return launch_early(moe_gate_fwd_kernel<T, OWN, G>, grid, kGateThreads, 0, s, a);
     }
-    // Few lanes a token share out its fixed costs best; a lane has up to 16 experts where there are few
-    // enough, and a choice a lane where top_k is at most 32.
+    // Few lanes a token share out its fixed costs best (65536 tokens, 8 of 128 experts, fp32: 15.3 us with 8
+    // lanes, 23.8 with 32): as many as there are choices, each with up to 16 experts.
     template <class T>
     cudaError_t run() const {
         if (a.k <= 8 && a.E <= 128) return a.E <= 16 ? go<T, 2, 8>() : a.E <= 32 ? go<T, 4, 8>() : a.E <= 64 ? go<T, 8, 8>() : go<T, 16, 8>();

@@ -1,5 +1,20 @@
 // moe_tokens.cu -- tokens to their experts' rows and back, with the gates, dropout and the residual
 // stream, the gradients of both, and dropout alone (include/swiglu_tokens.h).
+//
+// All of them move rows and compute little, so HBM bounds them where rows are whole 16-byte packs; one
+// GB300, copies at 6.7 TB/s, device times without the launch's latency, which runs beside the kernel
+// before (launch_early):
+//   dispatch   8192 tokens to 2 of 8 experts, 4096 bf16 columns      31 us, 6.5 TB/s (with the sort 34)
+//   combine    4096 tokens of 6 experts, 2048 bf16, dropout          24.8 us, 5.4 TB/s
+//              8192 tokens of 2, 4096 bf16                           41.5 us, 6.5 TB/s
+//   gradient   8192 tokens of 2, 4096 bf16, dropout                  49.6 us, 6.8 TB/s
+//   dropout    11136 x 3584 bf16 into the residual stream            34.9 us, 6.9 TB/s
+// A thread has a pack of the output, and what hides the latency of the rows, whose places have to be read
+// first, is as many threads as an SM holds: two rows in flight a thread at 32 registers (combine above,
+// 4 in flight at 40 and 48 registers: 28 and 27 us).  Rows off 16-byte boundaries start at another place
+// of a pack each: those are put together from two aligned packs, about 25 instructions for 16 bytes, and
+// these bound them (7 choices of 1021 columns, 4099 tokens: combine bf16 24.5 us for 10.4 of traffic, its
+// gradient fp16 25.1 for 17.1); fp32 rows, which are moved a column a thread instead, 24.9 for 20.8.
 #include <algorithm>
 #include <type_traits>
 
@@ -117,7 +132,8 @@ __device__ __forceinline__ void gather(const Gather& a, uint32_t t, T* y, int c)
     store_cols<T, HOW>(y, c, a.D, pack16<T>(v));
 }
 
-// y_t = add_t + drop(sum_j g_tj rows[pos_tj]), a pack of y a thread.
+// y_t = add_t + drop(sum_j g_tj rows[pos_tj]), a pack of y a thread.  Sums and products in fp32, by rising
+// j; the one rounding to fewer bits is y's.
 template <class T, Lie LIE, bool DROP, bool SELF>
 __device__ __forceinline__ void gather_item(const Gather& a) {
     const uint32_t item = blockIdx.x * kThreads + threadIdx.x;
@@ -137,11 +153,14 @@ __device__ __forceinline__ void gather_item(const Gather& a) {
         else gather<T, kElements, DROP, SELF, 1>(a, t, y, c);
     }
 }
+// (Shifted packs take more registers: 6 CTAs an SM would spill them, 39 us instead of 24 for the odd combine.)
 template <class T, Lie LIE, bool DROP>
 __global__ void __launch_bounds__(kThreads, LIE == kShifted ? 5 : 8) moe_gather_kernel(const __grid_constant__ Gather a) {
     after_previous();
     gather_item<T, LIE, DROP, false>(a);
 }
+// Dropout alone: HBM, with 45 % of the issue slots taken (of odd width, rows alike: 55 us for 36 of traffic;
+// a thread's columns then lie in two of the generator's blocks).
 template <class T, Lie LIE, bool DROP>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ Gather a) {
     after_previous();
@@ -231,7 +250,10 @@ __device__ __forceinline__ float warp_sums(float v0, float v1) {
 }
 
 // The combine's gradient: with e = drop(dy_t), drows[pos_tj] = g_tj e and dgates_tj = <e, rows[pos_tj]>.
-// A CTA a token.  Up to CHOICES choices: all of them at a time, their sums in registers.
+// A CTA a token.  Up to CHOICES choices: all of them at a time, their sums in registers, so a token's
+// gradient and its dropout are read and computed once (4096 tokens of 6 experts of 2048 bf16, p 0.1: 36.0 us
+// for 32.7 of traffic, two at a time 38.3; the CTAs an SM as they measured best: 8192 tokens of 2, 51 us at 6,
+// 52 at 5).
 template <class T, Lie LIE, bool DROP, int CHOICES>
 __global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 6 : CHOICES == 4 ? 4 : 3) moe_combine_bwd_few_kernel(const __grid_constant__ Scatter a) {
     after_previous();
@@ -358,7 +380,7 @@ __device__ __forceinline__ float pair_cols(const T* dy, const T* row, T* to, F2 
     F2 e[V2], f[V2], s = f2(0.f);
     unpack16<T>(d.get(), e);
     drop(e, c);
-    unpack16<T>(x.get(), f);
+    unpack16<T>(HOW == kAnywhere && (x.m | x.moved) == 0 ? x.lo : x.get(), f);       // rows that lie as drows do
 #pragma unroll
     for (int q = 0; q < V2; ++q) {
         s = fma(e[q], f[q], s);
@@ -383,7 +405,8 @@ __device__ __forceinline__ float pair_packs(const Scatter& a, uint32_t t, uint32
     return sum;
 }
 
-// Without dropout: `lanes` threads a choice, one warp (four choices a CTA) or the CTA.
+// Without dropout: `lanes` threads a choice, one warp (four choices a CTA, no barrier) or the CTA.  (A CTA a
+// token with a warp a choice, as below: 34 us instead of 26 for 4099 tokens' 7 choices of 1021 columns.)
 template <class T>
 __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_pairs_kernel(const __grid_constant__ Scatter a, int lanes) {
     after_previous();

@@ -40,7 +40,8 @@ swiglu_status swiglu_moe_gate_fwd(const void* logits, int64_t ld, int32_t* ids, 
                                   int64_t top_k, int renormalize, int type, void* stream);
 
 /*
- * Its gradient.  With q = gates, g = dgates, and c_j = 1 where ids_j is an expert, else 0:
+ * Its gradient.  With q = gates, the forward's (without renormalize the experts' p), g = dgates, and c_j = 1
+ * where ids_j is an expert, else 0:
  *   s = sum_j c_j q_j g_j
  *   renormalize:  dlogits_e = sum_{j: ids_j = e} q_j (g_j - s)
  *   else:         dlogits_e = p_e (sum_{j: ids_j = e} g_j - s),   p = softmax(l)
@@ -93,7 +94,7 @@ swiglu_status swiglu_moe_dispatch_bwd(const void* drows, int64_t lddrows, const 
  * (low and high word of seed).  With b = d % 8 the element's 16 bits are the low (b even) or high (b
  * odd) half of w[b / 2], and it is kept where they are below K.  The mask is computed where it is used
  * and never stored; the gradient's call with the same seed and offset has the same mask.
- *   p                   0 <= p <= 1.  0 (or less than 2^-17): no dropout; 1: everything is dropped
+ *   p                   0 <= p <= 1.  Up to 2^-17: no dropout; from 1 - 2^-17 on everything is dropped
  *   seed, offset        any 64 bits; one (seed, offset) for each mask
  *   step                device int64, or NULL: added to offset (modulo 2^64), read on the device, so
  *                       that a captured graph can have another mask on every replay
