@@ -2,7 +2,7 @@
 // choice) pairs sorted by expert (include/swiglu_tokens.h).
 //
 // One GB300, device times: the choice of 8 of 128 experts for 65536 tokens (fp32, 38 MB) 15.3 us, bound by
-// integer instructions (141 a token, two thirds of that pipe busy); its gradient 7.3 us, and 11.7 where it
+// integer instructions (146 a token, two thirds of that pipe busy); its gradient 7.3 us, and 11.7 where it
 // needs all experts' probabilities (75 MB), both near HBM's rate; 40961 tokens of 61 experts, bf16, 5.8 us.
 // The sort of 16384 pairs 5.2 us, of 131072 9.6 us.
 #include <cooperative_groups.h>
