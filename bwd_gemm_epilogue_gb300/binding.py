@@ -1057,10 +1057,11 @@ def swiglu_moe_dispatch_fwd(x, pos, n_rows: int | None = None, rows=None):
         n_rows = T * k if n_rows is None else n_rows
         if n_rows < 0:
             raise ValueError(f"n_rows: {n_rows} is negative")
-    elif n_rows is not None and n_rows != rows.shape[0]:
-        raise ValueError(f"n_rows: {n_rows}, but rows has {rows.shape[0]}")
     else:
-        n_rows = _rows_of(rows, "rows").shape[0]
+        have = _rows_of(rows, "rows").shape[0]
+        if n_rows is not None and n_rows != have:
+            raise ValueError(f"n_rows: {n_rows}, but rows has {have}")
+        n_rows = have
     rows, pr, ldr = _out_rows(rows, "rows", (n_rows, D), x.dtype, device)
     st = lib().swiglu_moe_dispatch_fwd(px, ldx, ppos, pr, ldr, T, D, k, n_rows, code, _device_stream(device))
     if st:

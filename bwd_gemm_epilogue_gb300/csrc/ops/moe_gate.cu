@@ -4,8 +4,10 @@
 // One GB300, device times: the choice of 8 of 128 experts for 65536 tokens (fp32, 38 MB) 15.3 us, bound by
 // integer instructions (146 a token, two thirds of that pipe busy); its gradient 7.3 us, and 11.7 where it
 // needs all experts' probabilities (75 MB), both near HBM's rate; 40961 tokens of 61 experts, bf16, 5.8 us.
-// The sort of 16384 pairs 5.2 us, of 131072 9.6 us.
+// The sort of 16384 pairs 4.7 us, of 131072 9.1 us.
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 #include "rows.cuh"
 #include "swiglu_tokens.h"
@@ -357,11 +359,34 @@ struct Sort {
     int E;
 };
 
+// Of n counts `ld` apart, a multiple of 4: each becomes the sum of those before it; returns the sum of all.
+// Four loads at a time (one by one, the latencies add up: 0.5 us for 32 warps).
+__device__ __forceinline__ int sum_before(int* p, int ld, int n) {
+    int sum = 0;
+    for (int w = 0; w < n; w += 4) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = p[(w + i) * ld];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[(w + i) * ld] = sum, sum += v[i];
+    }
+    return sum;
+}
+__device__ __forceinline__ void add_to_all(int* p, int ld, int n, int add) {
+    for (int w = 0; w < n; w += 4) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = p[(w + i) * ld];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[(w + i) * ld] = v[i] + add;
+    }
+}
+
 // Counting sort of the pairs by one cluster, in one launch.  Each warp has a run of consecutive pairs, 32
 // at a time, and a count for each expert; the counts of all warps, added up over the warps before it and
 // over the experts before, are where its first pair of each expert goes.  The lanes that have one expert
 // find each other by a bit each in a word of it, so that the order does not depend on timing (131072
-// pairs 9.6 us; by a vote a bit 15.2, by match.any 30).  Latencies bound it: four barriers, two of them the
+// pairs 9.1 us; by a vote a bit 15.2, by match.any 30).  Latencies bound it: four barriers, two of them the
 // cluster's.
 __global__ void __launch_bounds__(kSortWarps * 32) moe_sort_kernel(const Sort a) {
     extern __shared__ int smem[];
@@ -389,15 +414,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) moe_sort_kernel(const Sort a)
         if (e < a.E) atomicAdd(own + e, 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        int sum = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int v = hist[w * a.E + e];
-            hist[w * a.E + e] = sum;
-            sum += v;
-        }
-        mine[e] = sum;
-    }
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) mine[e] = sum_before(hist + e, a.E, warps);
     cluster.sync();
     // per expert: the pairs of the CTAs before this one, and of all; then of the experts before it
     for (int e0 = warp * 32; e0 < a.E; e0 += warps * 32) {
@@ -425,7 +442,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) moe_sort_kernel(const Sort a)
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         int sum = base[e];
         for (int c = 0; c < e / 32; ++c) sum += chunk[c];
-        for (int w = 0; w < warps; ++w) hist[w * a.E + e] += sum;
+        add_to_all(hist + e, a.E, warps, sum);
     }
     __syncthreads();
     int next = load(begin + lane);
@@ -538,9 +555,9 @@ swiglu_status swiglu_moe_sort(const int32_t* ids, int32_t* counts, int32_t* pos,
     if (rc != SWIGLU_OK) return rc;
     int ctas = 1;
     while (ctas < kSortCtas && pairs > (int64_t)ctas * kSortWarps * 32) ctas *= 2;
-    const int64_t runs = (pairs + 31) / 32, per_cta = (runs + ctas - 1) / ctas;
+    const int64_t runs = std::max<int64_t>(1, (pairs + 31) / 32), per_cta = (runs + ctas - 1) / ctas;
     const int most = E <= 768 ? kSortWarps : 24;           // of 227 KB
-    const int warps = (int)(per_cta < 4 ? 4 : per_cta < most ? per_cta : most);
+    const int warps = (int)std::min<int64_t>((per_cta + 3) / 4 * 4, most);
     const int64_t per_warp = (per_cta + warps - 1) / warps * 32;
     const Sort a{ids, counts, pos, pairs, per_warp, (int)E};
     const size_t smem = ((size_t)(2 * warps + 2) * E + 32) * sizeof(int);
