@@ -12,9 +12,9 @@
 // A thread has a pack of the output, and what hides the latency of the rows, whose places have to be read
 // first, is as many threads as an SM holds: two rows in flight a thread at 32 registers (combine above,
 // 4 in flight at 40 and 48 registers: 28 and 27 us).  Rows off 16-byte boundaries start at another place
-// of a pack each: those are put together from two aligned packs, about 25 instructions for 16 bytes, and
-// these bound them (7 choices of 1021 columns, 4099 tokens: combine bf16 24.5 us for 10.4 of traffic, its
-// gradient fp16 25.1 for 17.1); fp32 rows, which are moved a column a thread instead, 24.9 for 20.8.
+// of a pack each: those are put together from aligned pieces, about 20 instructions for 16 bytes, and
+// these bound them (7 choices of 1021 columns, 4099 tokens: combine bf16 22.5 us for 10.4 of traffic, its
+// gradient fp16 24.5 for 17.1); fp32 rows, which are moved a column a thread instead, 24.9 for 20.8.
 #include <algorithm>
 #include <type_traits>
 
@@ -153,7 +153,7 @@ __device__ __forceinline__ void gather_item(const Gather& a) {
         else gather<T, kElements, DROP, SELF, 1>(a, t, y, c);
     }
 }
-// (Shifted packs take more registers: 6 CTAs an SM would spill them, 39 us instead of 24 for the odd combine.)
+// (Shifted packs take more registers: 5 CTAs an SM.)
 template <class T, Lie LIE, bool DROP>
 __global__ void __launch_bounds__(kThreads, LIE == kShifted ? 5 : 8) moe_gather_kernel(const __grid_constant__ Gather a) {
     after_previous();
@@ -406,7 +406,7 @@ __device__ __forceinline__ float pair_packs(const Scatter& a, uint32_t t, uint32
 }
 
 // Without dropout: `lanes` threads a choice, one warp (four choices a CTA, no barrier) or the CTA.  (A CTA a
-// token with a warp a choice, as below: 34 us instead of 26 for 4099 tokens' 7 choices of 1021 columns.)
+// token with a warp a choice, as below: 34 us where this took 27 for 4099 tokens' 7 choices of 1021 columns.)
 template <class T>
 __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_pairs_kernel(const __grid_constant__ Scatter a, int lanes) {
     after_previous();
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_pairs_kernel(cons
 // With dropout: a CTA a token, `split` warps a choice, kSegment columns at a time, of which it is first
 // computed once for all choices, into shared memory, which ones are dropped: a byte for eight columns.
 // (Computed at each choice's packs, which begin anywhere in those eight, 2048 tokens' 4 choices of 8191
-// bf16 columns took 105 us instead of 73.)
+// bf16 columns took 105 us instead of 71.)
 constexpr int kSegment = 32768;
 template <class T>
 __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_drop_kernel(const __grid_constant__ Scatter a, int split) {
