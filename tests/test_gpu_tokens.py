@@ -105,7 +105,7 @@ def check_all(b, T, E, k, D, dtype, drop=0.2, p=0.0, ld=None, start=(0, 0, 0, 0)
 # more than a CTA's threads; choices past a register block; wide rows
 SHAPES = [(1, 4, 1, 1), (1, 8, 8, 2048), (3, 5, 2, 7), (16, 8, 2, 4096), (37, 6, 3, 8), (33, 40, 7, 1021), (5, 3, 3, 2056),
           (130, 64, 6, 264), (2, 700, 20, 100), (7, 9, 5, 8193), (3, 2, 1, 65536 + 24), (1000, 16, 4, 36),
-          (2, 5, 3, 40001), (3, 4, 2, 32771), (70, 16, 9, 130)]
+          (2, 5, 3, 40001), (3, 4, 2, 32771), (70, 16, 9, 130), (2, 1024, 1024, 40), (2, 1024, 1000, 33)]
 
 
 @pytest.mark.parametrize("dtype", [BF, HF, F32], ids=str)
