@@ -1,10 +1,10 @@
 // moe_gate.cu -- the choice of experts from the router's logits and its gradient, and the (token,
 // choice) pairs sorted by expert (include/swiglu_tokens.h).
 //
-// One GB300, device times: the choice of 8 of 128 experts for 65536 tokens (fp32, 38 MB) 15.3 us, bound by
-// integer instructions (146 a token, two thirds of that pipe busy); its gradient 7.3 us, and 11.7 where it
-// needs all experts' probabilities (75 MB), both near HBM's rate; 40961 tokens of 61 experts, bf16, 5.8 us.
-// The sort of 16384 pairs 4.7 us, of 131072 9.1 us.
+// One GB300, device times: the choice of 8 of 128 experts for 65536 tokens (fp32, 38 MB) 12.6 us (bf16 11.3),
+// bound by integer instructions (about 140 a token, two thirds of that pipe busy); its gradient 7.3 us, and
+// 11.7 where it needs all experts' probabilities (75 MB), both near HBM's rate; 40961 tokens of 61 experts,
+// bf16, 5.8 us.  The sort of 16384 pairs 4.7 us, of 131072 9.1 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -188,19 +188,90 @@ __device__ __noinline__ void choose_by_keys(const Gate& a, int64_t t) {
     for (int j = last - G; j >= 0; j -= G) gates[j] = gates[j] < 0.f ? 0.f : gates[j] / by;
 }
 
-// top_k of more than 32.
+// top_k of more than 32 (4096 tokens, 40 of 512 experts: 34 us, a maximum over the warp and a pass over the
+// lane's keys for each choice).
 template <class T, int OWN>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_fwd_keys_kernel(const __grid_constant__ Gate a) {
     after_previous();
     choose_by_keys<T, OWN, 32>(a, Group<32>::token());
 }
 
+// Order-preserving key of a logit that is no NaN; 0 and -0 have one.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+// A lane's words without the first, where the group's largest is hers.
+template <int KEEP>
+__device__ __forceinline__ void pop(uint32_t* word, uint32_t high) {
+    if (word[0] != high) return;
+#pragma unroll
+    for (int i = 0; i + 1 < KEEP; ++i) word[i] = word[i + 1];
+    word[KEEP - 1] = 0;
+}
+
+// The choices by words, where some are alike in them but not in their logits: among the chosen
+// (their order), or beyond the last one (border: `next`, and who is chosen).  Puts both right; false where
+// too many beyond the last are alike in their words but differ.
+template <int OWN, int G, int KEEP>
+__device__ __forceinline__ bool settle(const Gate& a, int64_t t, uint32_t* word, uint32_t next, bool border, uint32_t mine, int& e, float& value) {
+    constexpr uint32_t kAll = OWN * G, kIndex = 2 * kAll - 1;
+    const int lane = Group<G>::lane();
+    const float* row = static_cast<const float*>(a.logits) + t * a.ld;
+    const uint32_t last = Group<G>::of(mine, a.k - 1);
+    const bool alike = lane < a.k && (mine ^ last) <= kIndex;
+    uint32_t key = order_key(value);
+    // the ones beyond, one by one: in the place of the last of those chosen that are alike, if larger
+    uint32_t least = 0;
+    for (int turn = 0; turn < 4; ++turn) {
+        if (!__any_sync(0xffffffffu, border)) break;
+        const int e2 = (int)(kAll - (next & kIndex));
+        const float v2 = border ? row[e2] : -INFINITY;
+        least = ~Group<G>::max(alike ? ~key : 0u);
+        const int worst = (int)Group<G>::max(alike && key == least ? (uint32_t)e + 1 : 0u) - 1;
+        if (border && alike && e == worst && order_key(v2) > least) e = e2, value = v2, key = order_key(v2);
+        if (border) pop<KEEP>(word, next);
+        next = Group<G>::max(word[0]);
+        border = border && (next ^ last) <= kIndex;
+    }
+    if constexpr (KEEP < OWN) {
+        const uint32_t ran_out = Group<G>::max(word[0] == 0 ? 1u : 0u);        // of a lane's words
+        border = border || ran_out != 0;
+    }
+    bool settled = true;
+    if (__any_sync(0xffffffffu, border)) {                 // more: whether any is larger than the least chosen (equal ones are not)
+        float v[OWN], larger = 0.f;
+        load_logits<float, OWN, G, 1>(v, a, t);
+        least = ~Group<G>::max(alike ? ~key : 0u);
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) larger += expert<G, 1>(i) < a.E && order_key(v[i]) > least;
+        larger = Group<G>::sum(larger - (float)(lane < a.k && key > least));
+        settled = !border || larger == 0.f;
+    }
+    int rank = 0;
+    for (int i = 0; i < a.k; ++i) {
+        const uint32_t k2 = Group<G>::of(key, i);
+        const int e2 = Group<G>::of(e, i);
+        rank += k2 > key || (k2 == key && e2 < e);
+    }
+    const int e0 = e;
+    const float v0 = value;
+    for (int i = 0; i < a.k; ++i) {
+        const int to = Group<G>::of(rank, i), e2 = Group<G>::of(e0, i);
+        const float v2 = Group<G>::of(v0, i);
+        if (lane == to && lane < a.k) e = e2, value = v2;
+    }
+    return settled;
+}
+
 // top_k up to G.  An expert's word has its index in the lowest bits (from all experts down, so that of equal
 // logits the lowest index is the largest word) and as many of the first bits of its key as there is room
 // for: one maximum over the group finds the next choice and who has it, and a lane that keeps its words
 // sorted shows only the first.  These are at least 21 bits, which is all of a 16-bit logit's key.  For fp32
-// the order by words can be wrong only among keys alike in them; where that is among the chosen, or
-// between the last one and the next, the warp chooses by whole keys, and so it does where a logit is NaN.
+// the order by words can be wrong only among keys alike in them, which `settle` puts right (24 bits for 128
+// experts: one token in 600 of normal logits, for which choosing anew by whole keys held up the last warps: 15.3
+// us instead of 12.6); where it cannot, or a logit is NaN, the warp chooses by whole keys.
 template <class T, int OWN, int G>
 __global__ void __launch_bounds__(kGateThreads, OWN > 16 ? 3 : 8) moe_gate_fwd_kernel(const __grid_constant__ Gate a) {
     after_previous();
@@ -213,13 +284,10 @@ __global__ void __launch_bounds__(kGateThreads, OWN > 16 ? 3 : 8) moe_gate_fwd_k
     {
         float v[OWN];
         load_logits<T, OWN, G, 1>(v, a, t);
-        // Places past the row's end, minus infinity too, come after all the row's.
+        // Places past the row's end, minus infinity too, come after all the row's.  The sum makes each NaN
+        // 0x7fffffff, whose key is the largest.
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-            const uint32_t u = __float_as_uint(v[i] + 0.f);            // -0 counts as 0, each NaN is 0x7fffffff
-            const uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-            word[i] = (key & ~kIndex) | (kAll - expert<G, 1>(i));
-        }
+        for (int i = 0; i < OWN; ++i) word[i] = (order_key(v[i]) & ~kIndex) | (kAll - expert<G, 1>(i));
         if (!a.renorm) {
             float top = v[0];
 #pragma unroll
@@ -229,26 +297,24 @@ __global__ void __launch_bounds__(kGateThreads, OWN > 16 ? 3 : 8) moe_gate_fwd_k
         }
     }
     sort_words<0, OWN>(word);
-    bool again = word[0] > (0xffffffffu & ~kIndex);        // a NaN's key is the largest
+    bool again = word[0] > (0xffffffffu & ~kIndex);        // a NaN
     uint32_t mine = 0;
     for (int j = 0; j < a.k; ++j) {
         const uint32_t high = Group<G>::max(word[0]);
         if (lane == j) mine = high;
-        if (word[0] == high) {
-#pragma unroll
-            for (int i = 0; i + 1 < kKeep; ++i) word[i] = word[i + 1];
-            word[kKeep - 1] = 0;
-        }
+        pop<kKeep>(word, high);
     }
     int e = lane < a.k ? (int)(kAll - (mine & kIndex)) : -1;
-    const float value = e < 0 || t >= a.T ? -INFINITY : to_f32(static_cast<const T*>(a.logits)[t * a.ld + e]);
-    const float top = Group<G>::of(value, 0);
+    float value = e < 0 || t >= a.T ? -INFINITY : to_f32(static_cast<const T*>(a.logits)[t * a.ld + e]);
     if constexpr (sizeof(T) == 4) {
         const uint32_t next = Group<G>::max(word[0]), after = Group<G>::of(mine, lane + 1);
         const float other = Group<G>::of(value, lane + 1);
-        again |= lane < a.k - 1 ? (mine ^ after) <= kIndex && value != other : lane == a.k - 1 && (mine ^ next) <= kIndex && value != -INFINITY;
+        const bool inner = lane < a.k - 1 && (mine ^ after) <= kIndex && value != other;
+        const bool border = Group<G>::of((mine ^ next) <= kIndex && value != -INFINITY, a.k - 1);
+        if (__any_sync(0xffffffffu, inner || border)) again |= !settle<OWN, G, kKeep>(a, t, word, next, border, mine, e, value);
     }
     if (__any_sync(0xffffffffu, again)) return choose_by_keys<T, OWN, G>(a, t);
+    const float top = Group<G>::of(value, 0);
     if (value == -INFINITY) e = -1;                        // off
     const float p = e < 0 ? 0.f : expf(value - top);
     if (a.renorm) total = Group<G>::sum(p);
@@ -476,8 +542,8 @@ struct LaunchGate {
             if (a.k > G) return launch_early(moe_gate_fwd_keys_kernel<T, OWN>, grid, kGateThreads, 0, s, a);
         return launch_early(moe_gate_fwd_kernel<T, OWN, G>, grid, kGateThreads, 0, s, a);
     }
-    // Few lanes a token share out its fixed costs best (65536 tokens, 8 of 128 experts, fp32: 15.3 us with 8
-    // lanes, 23.8 with 32): as many as there are choices, each with up to 16 experts.
+    // Few lanes a token share out its fixed costs best (65536 tokens, 8 of 128 experts, fp32: 15.5 us with 8
+    // lanes, 23.8 with 32, when it was measured): as many as there are choices, each with up to 16 experts.
     template <class T>
     cudaError_t run() const {
         if (a.k <= 8 && a.E <= 128) return a.E <= 16 ? go<T, 2, 8>() : a.E <= 32 ? go<T, 4, 8>() : a.E <= 64 ? go<T, 8, 8>() : go<T, 16, 8>();

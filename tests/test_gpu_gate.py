@@ -105,6 +105,30 @@ def test_logits_that_differ_in_their_last_bits(b, E):  # noqa: F811
             check(b, l, n, renormalize, g)
 
 
+@pytest.mark.parametrize("E", [9, 16, 40, 128, 200, 512, 1024])
+def test_many_logits_alike(b, E):  # noqa: F811
+    """All equal (a router that starts at zero); two values a unit of the last place apart, a few of either,
+    or one after all that are equal; a run of neighbours in one lane's experts; the same, some off."""
+    g = torch.Generator().manual_seed(E)
+    up = torch.nextafter(torch.ones(()), torch.tensor(2.0))
+    l = torch.ones(96, E)
+    l[1] = 0
+    for i in range(2, 40):
+        l[i, torch.randperm(E, generator=g)[:1 + i % 7]] = up
+    l[40:50] = torch.where(torch.rand(10, E, generator=g) < 0.5, up, torch.ones(()))
+    for i in range(50, 60):
+        l[i, E - 1 - (i - 50) % E] = up                     # the last ones in order
+        l[i, : (i - 50) % E] = -1.0
+    for i in range(60, 76):                                # every G-th expert, which one lane has
+        l[i, (i % 8)::8 if i < 68 else 16] += torch.randperm(len(l[i, (i % 8)::8 if i < 68 else 16]), generator=g) * 2.0 ** -23
+    l[76:86] = 1 + torch.randint(0, 3, (10, E), generator=g) * 2.0 ** -23
+    l[86:] = torch.where(torch.rand(10, E, generator=g) < 0.3, -math.inf, l[76:86])
+    l = l.cuda()
+    for renormalize in (True, False):
+        for n in (1, 3, min(8, E), min(9, E), min(16, E), min(32, E)):
+            check(b, l, n, renormalize, g)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF, F32], ids=str)
 def test_lowest_values_count_as_values(b, dtype):  # noqa: F811
     low = torch.finfo(dtype).min

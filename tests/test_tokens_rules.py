@@ -24,3 +24,15 @@ def test_every_kernel_that_comes_up_early_waits_first():
 
 def test_only_these_sources_launch_early():
     assert {os.path.basename(p) for p in SOURCES if "launch_early" in open(p).read()} == {"moe_gate.cu", "moe_tokens.cu"}
+
+
+def test_what_a_warp_does_together_stands_in_no_short_circuit():
+    """Shuffles, votes and reductions name every lane of the warp, so none may be the second operand of ||,
+    && or ?:, which some lanes would not reach."""
+    together = r"(?:Group<G>::(?:max|sum|of)|__shfl\w*|__any_sync|__all_sync|__ballot_sync|__reduce_\w+|__match_\w+|warp_sums?)\("
+    for path in SOURCES:
+        if os.path.basename(path) not in ("moe_gate.cu", "moe_tokens.cu"):
+            continue
+        for i, line in enumerate(open(path).read().split("\n"), 1):
+            code = line.split("//")[0]
+            assert not re.search(rf"(?:\|\||&&|\?)[^;)]*{together}", code), f"{os.path.basename(path)}:{i}: {code.strip()}"
