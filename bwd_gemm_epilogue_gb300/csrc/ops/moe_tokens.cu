@@ -518,12 +518,14 @@ struct WithRows {
         if (lie == kWhole) return dropping ? f.template go<T, kWhole, true>() : f.template go<T, kWhole, false>();
         if constexpr (sizeof(T) == 4)
             if (lie == kApart) return f.template go<T, kApart, false>();
-        if (lie == kAlike) return dropping ? f.template go<T, kAlike, true>() : f.template go<T, kAlike, false>();
+        if constexpr (F::kAlikeRows)
+            if (lie == kAlike) return dropping ? f.template go<T, kAlike, true>() : f.template go<T, kAlike, false>();
         return dropping ? f.template go<T, kShifted, true>() : f.template go<T, kShifted, false>();
     }
 };
 
 struct LaunchGather {
+    static constexpr bool kAlikeRows = true;
     const Gather& a;
     cudaStream_t s;
     template <class T, Lie LIE, bool DROP>
@@ -537,28 +539,29 @@ struct LaunchGather {
 
 // A row's place differs from its token's, so no rows are alike below.
 struct LaunchScatter {
+    static constexpr bool kAlikeRows = false;
     const Scatter& a;
     cudaStream_t s;
     template <class T, Lie LIE, bool>
     cudaError_t go() const {
         const uint64_t items = (uint64_t)a.T * a.packs.d;
-        return launch_early(moe_scatter_kernel<T, LIE == kAlike ? kShifted : LIE>, (unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s, a);
+        return launch_early(moe_scatter_kernel<T, LIE>, (unsigned)((items + kThreads - 1) / kThreads), kThreads, 0, s, a);
     }
 };
 
 struct LaunchCombineBwd {
+    static constexpr bool kAlikeRows = false;
     const Scatter& a;
     cudaStream_t s;
     template <class T, Lie LIE, bool DROP>
     cudaError_t go() const {
         const int wide = (int)(a.packs.d + 31) / 32;
-        constexpr bool shifted = LIE == kShifted || LIE == kAlike;
-        if constexpr (shifted && DROP) {   // as many warps a choice as there are for all, and as its packs are for
+        if constexpr (LIE == kShifted && DROP) {   // as many warps a choice as there are for all, and as its packs are for
             int split = 1;
             while (2 * split * a.k <= kThreads / 32 && 2 * split <= wide) split *= 2;
             const int warps = std::min(kThreads / 32, split * a.k);
             return launch_early(moe_combine_bwd_drop_kernel<T>, a.T, warps * 32, (size_t)a.k * split * sizeof(float), s, a, split);
-        } else if constexpr (shifted) {    // a warp for rows of up to 16 packs a lane
+        } else if constexpr (LIE == kShifted) {        // a warp for rows of up to 16 packs a lane
             const uint64_t pairs = (uint64_t)a.T * a.k;
             const int lanes = wide <= 16 ? 32 : kThreads, threads = lanes == 32 ? 128 : kThreads;
             return launch_early(moe_combine_bwd_pairs_kernel<T>, (unsigned)(lanes == 32 ? (pairs + 3) / 4 : pairs), threads, 0, s, a, lanes);
