@@ -213,7 +213,7 @@ __device__ __forceinline__ void pop(uint32_t* word, uint32_t high) {
 
 // The choices by words, where some are alike in them but not in their logits: among the chosen
 // (their order), or beyond the last one (border: `next`, and who is chosen).  Puts both right; false where
-// too many beyond the last are alike in their words but differ.
+// too many beyond the last are alike in their words but differ, or a lane's KEEP words do not show them.
 template <int OWN, int G, int KEEP>
 __device__ __forceinline__ bool settle(const Gate& a, int64_t t, uint32_t* word, uint32_t next, bool border, uint32_t mine, int& e, float& value) {
     constexpr uint32_t kAll = OWN * G, kIndex = 2 * kAll - 1;
@@ -222,25 +222,26 @@ __device__ __forceinline__ bool settle(const Gate& a, int64_t t, uint32_t* word,
     const uint32_t last = Group<G>::of(mine, a.k - 1);
     const bool alike = lane < a.k && (mine ^ last) <= kIndex;
     uint32_t key = order_key(value);
-    // the ones beyond, one by one: in the place of the last of those chosen that are alike, if larger
+    // the ones beyond, one by one: in the place of the last of those chosen that are alike, if larger.  They come
+    // by falling word, so of equal logits by rising index, until a lane has no words left: what it would show
+    // next is not known.
     uint32_t least = 0;
+    bool more = border, ran_out = false;
     for (int turn = 0; turn < 4; ++turn) {
-        if (!__any_sync(0xffffffffu, border)) break;
+        if (!__any_sync(0xffffffffu, more)) break;
         const int e2 = (int)(kAll - (next & kIndex));
-        const float v2 = border ? row[e2] : -INFINITY;
+        const float v2 = more ? row[e2] : -INFINITY;
         least = ~Group<G>::max(alike ? ~key : 0u);
         const int worst = (int)Group<G>::max(alike && key == least ? (uint32_t)e + 1 : 0u) - 1;
-        if (border && alike && e == worst && order_key(v2) > least) e = e2, value = v2, key = order_key(v2);
-        if (border) pop<KEEP>(word, next);
+        if (more && alike && e == worst && order_key(v2) > least) e = e2, value = v2, key = order_key(v2);
+        if (more) pop<KEEP>(word, next);
         next = Group<G>::max(word[0]);
-        border = border && (next ^ last) <= kIndex;
+        if constexpr (KEEP < OWN) ran_out = Group<G>::max(word[0] == 0 ? 1u : 0u) != 0;
+        more = more && !ran_out && (next ^ last) <= kIndex;
     }
-    if constexpr (KEEP < OWN) {
-        const uint32_t ran_out = Group<G>::max(word[0] == 0 ? 1u : 0u);        // of a lane's words
-        border = border || ran_out != 0;
-    }
+    border = more || ran_out;
     bool settled = true;
-    if (__any_sync(0xffffffffu, border)) {                 // more: whether any is larger than the least chosen (equal ones are not)
+    if (__any_sync(0xffffffffu, border)) {                 // the rest: whether any is larger than the least chosen (equal ones come after it)
         float v[OWN], larger = 0.f;
         load_logits<float, OWN, G, 1>(v, a, t);
         least = ~Group<G>::max(alike ? ~key : 0u);
@@ -276,7 +277,7 @@ template <class T, int OWN, int G>
 __global__ void __launch_bounds__(kGateThreads, OWN > 16 ? 3 : 8) moe_gate_fwd_kernel(const __grid_constant__ Gate a) {
     after_previous();
     constexpr uint32_t kAll = OWN * G, kIndex = 2 * kAll - 1;
-    constexpr int kKeep = OWN > G ? G + 1 : OWN;           // no more than top_k + 1 of a lane's words are asked for
+    constexpr int kKeep = OWN > G ? G + 1 : OWN;           // of a lane's words: the choice shows top_k + 1 at most
     const int64_t t = Group<G>::token();
     const int lane = Group<G>::lane();
     uint32_t word[OWN];
