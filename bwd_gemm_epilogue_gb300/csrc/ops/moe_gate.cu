@@ -630,10 +630,8 @@ swiglu_status swiglu_moe_sort(const int32_t* ids, int32_t* counts, int32_t* pos,
     const size_t smem = ((size_t)(2 * warps + 2) * E + 32) * sizeof(int);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return launch_traced(SWIGLU_KERNEL_MOE_SORT, s, [&] {
-        if (smem > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (e != cudaSuccess) return e;
-        }
+        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(moe_sort_kernel), smem);
+        if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -1,0 +1,60 @@
+"""GPU tests of the C entry points called from two threads at once, for launches of one kernel with different
+amounts of shared memory, past what a kernel may have without leave."""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+from test_gpu_tokens import b  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+TURNS = 10000
+
+
+def c(v):
+    """A tensor or a whole number as ctypes has it, made once: the threads shall spend their time in the calls."""
+    return ctypes.c_void_p(v.data_ptr()) if isinstance(v, torch.Tensor) else ctypes.c_int64(v) if isinstance(v, int) else v
+
+
+def at_once(entry, calls):
+    """calls: (arguments, outputs).  Each is made once alone, then all TURNS times, a thread and a stream each."""
+    want = []
+    for args, outs in calls:
+        assert entry(*map(c, args), None) == 0
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+        for t in outs:
+            t.zero_()
+    torch.cuda.synchronize()
+    statuses, go = [{} for _ in calls], threading.Barrier(len(calls))
+
+    def run(i, args):
+        stream = torch.cuda.Stream()
+        args = [*map(c, args), ctypes.c_void_p(stream.cuda_stream)]
+        go.wait()
+        for turn in range(TURNS):
+            st = entry(*args)
+            statuses[i][st] = statuses[i].get(st, 0) + 1
+            if turn % 64 == 63:                            # few launches queued: what is looked for is at the call
+                stream.synchronize()
+        stream.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i, args)) for i, (args, _) in enumerate(calls)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert statuses == [{0: TURNS}] * len(calls)
+    for (_, outs), alone in zip(calls, want):
+        assert all(torch.equal(p, q) for p, q in zip(outs, alone))
+
+
+def test_sorts(b):  # noqa: F811
+    g = torch.Generator().manual_seed(1)
+    calls = []
+    for n, E in ((256, 1024), (1024, 1024)):               # 74 and 205 KB
+        ids = torch.randint(0, E, (n,), generator=g).int().cuda()
+        counts, pos = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty_like(ids)
+        calls.append(((ids, counts, pos, n, E), (counts, pos)))
+    at_once(b.lib().swiglu_moe_sort, calls)
