@@ -216,13 +216,6 @@ struct Rows16 {
     }
 };
 
-// Past 48 KB, of which the kernels' own arrays take less than 1 KB, a launch has to be allowed.
-template <class K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-    return bytes <= 47 * 1024 ? cudaSuccess
-                              : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 inline swiglu_status norm_check(int64_t M, int64_t D, int type, int param_type) {
     if (M < 0 || D <= 0) return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: a size is negative or zero");
     if (M >= (int64_t(1) << 31) || D >= (int64_t(1) << 28))

@@ -539,7 +539,7 @@ struct LaunchBwd {
     cudaError_t go() const {
         auto kern = layer_norm_bwd_kernel<T, NV, SKIP, EDGE>;
         const size_t smem = bwd_smem(p, reach(a.D, (int)sizeof(T), EDGE), SKIP, EDGE);
-        cudaError_t e = allow_smem(kern, smem);
+        cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
         if (e != cudaSuccess) return e;
         kern<<<(unsigned)planes, p.threads(), smem, s>>>(a);
         return cudaGetLastError();
@@ -554,7 +554,7 @@ struct LaunchBwd {
         constexpr int rows = THREADS == 32 ? 4 : 1;
         auto kern = a.skip ? layer_norm_bwd_narrow_kernel<T, true, THREADS> : layer_norm_bwd_narrow_kernel<T, false, THREADS>;
         const size_t smem = (size_t)rows * 2 * (a.skip ? 3 : 2) * narrow_pitch(a.D * (int)sizeof(T));
-        cudaError_t e = allow_smem(kern, smem);
+        cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
         if (e != cudaSuccess) return e;
         kern<<<(unsigned)(planes / rows), THREADS * rows, smem, s>>>(a);
         return cudaGetLastError();

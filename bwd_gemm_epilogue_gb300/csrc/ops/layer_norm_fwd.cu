@@ -363,7 +363,7 @@ struct LaunchFwd {
             else if (p.threads() > 128) kern = layer_norm_fwd_kernel<T, NV, RES, EDGE, 384, 2>;
         }
         const size_t smem = EDGE ? (size_t)p.groups * 2 * padded((int)reach(a.D, (int)sizeof(T), true)) * 4 : 0;
-        cudaError_t e = allow_smem(kern, smem);
+        cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
         if (e != cudaSuccess) return e;
         int64_t grid = (a.M + p.groups - 1) / p.groups;
         if (EDGE) {

@@ -6,7 +6,7 @@ import threading
 import pytest
 import torch
 
-from test_gpu_tokens import b  # noqa: F401
+from test_gpu_tokens import BF, b  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 TURNS = 10000
@@ -58,3 +58,25 @@ def test_sorts(b):  # noqa: F811
         counts, pos = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty_like(ids)
         calls.append(((ids, counts, pos, n, E), (counts, pos)))
     at_once(b.lib().swiglu_moe_sort, calls)
+
+
+def test_layer_norms_forward(b):  # noqa: F811
+    calls = []
+    for D in (7001, 12001):                                # odd rows, whose parameters go through 56 and 96 KB
+        x, y = torch.randn(3, D, device="cuda").to(BF), torch.empty(3, D, dtype=BF, device="cuda")
+        w, stats = torch.randn(2, D, device="cuda").to(BF), torch.empty(2, 3, device="cuda")
+        calls.append(((x, D, None, 0, w[0], w[1], y, D, None, 0, stats[0], stats[1], 3, D, ctypes.c_float(1e-5), ctypes.c_int(0),
+                       ctypes.c_int(0)), (y, stats)))
+    at_once(b.lib().swiglu_mlp_layer_norm_fwd, calls)
+
+
+def test_layer_norms_backward(b):  # noqa: F811
+    calls = []
+    M = 480
+    for D in (2048, 3584):                                 # 74 and 111 KB: rows in flight, and gamma
+        dy, s, dx = (torch.randn(M, D, device="cuda").to(BF) for _ in range(3))
+        w, stats = torch.randn(3, D, device="cuda").to(BF), torch.rand(2, M, device="cuda")
+        need = b.swiglu_mlp_layer_norm_bwd_workspace_size(M, D)
+        calls.append(((dy, D, s, D, w[0], stats[0], stats[1], None, 0, dx, D, w[1], w[2], M, D, ctypes.c_int(0), ctypes.c_int(0),
+                       torch.empty(need, dtype=torch.uint8, device="cuda"), ctypes.c_size_t(need)), (dx, w[1:])))
+    at_once(b.lib().swiglu_mlp_layer_norm_bwd, calls)
