@@ -773,9 +773,7 @@ bool width_ok(int64_t v) { return v > 0 && v % 8 == 0 && v < (int64_t(1) << 24);
 template <class... Args>
 cudaError_t launch_clusters(void (*kernel)(Args...), dim3 clusters, int size, int threads, size_t smem, cudaStream_t s,
                             bool early, Args... args) {
-    cudaError_t e = smem <= 48 * 1024
-                        ? cudaSuccess
-                        : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];

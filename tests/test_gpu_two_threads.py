@@ -80,3 +80,19 @@ def test_layer_norms_backward(b):  # noqa: F811
         calls.append(((dy, D, s, D, w[0], stats[0], stats[1], None, 0, dx, D, w[1], w[2], M, D, ctypes.c_int(0), ctypes.c_int(0),
                        torch.empty(need, dtype=torch.uint8, device="cuda"), ctypes.c_size_t(need)), (dx, w[1:])))
     at_once(b.lib().swiglu_mlp_layer_norm_bwd, calls)
+
+
+@pytest.mark.parametrize("tokens", [(1, 32), (2, 9), (33, 64)])
+def test_routed_layers(b, tokens):  # noqa: F811
+    """The down products' sums take 1 KB of shared memory for each token."""
+    g = torch.Generator().manual_seed(2)
+    E, D, H, k = 4, 64, 64, 1
+    weights = [(torch.randn(s, generator=g) * s[-1] ** -0.5).to(BF).cuda() for s in ((E, D), (E, 2 * H, D), (E, D, H))]
+    calls = []
+    for T in tokens * 2:
+        x, y = torch.randn(T, D, generator=g).to(BF).cuda(), torch.empty(T, D, dtype=BF, device="cuda")
+        ids, gates = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+        need = b.swiglu_moe_routed_fwd_workspace_size(T, H, D, k)
+        calls.append(((x, *weights, None, y, ids, gates, T, E, D, H, D, k, ctypes.c_int(1), ctypes.c_int(0),
+                       torch.empty(need, dtype=torch.uint8, device="cuda"), ctypes.c_size_t(need)), (y, ids, gates)))
+    at_once(b.lib().swiglu_moe_routed_fwd, calls)
