@@ -602,6 +602,8 @@ swiglu_status swiglu_moe_gate_bwd(const void* logits, int64_t ld, const int32_t*
     if ((!renormalize && ld < E) || lddl < E) return fail(SWIGLU_ERR_INVALID_ARG, "gate: a row stride is smaller than E");
     if (misaligned(logits, n) || misaligned(dlogits, n) || misaligned(ids, 4) || misaligned(gates, 4) || misaligned(dgates, 4))
         return fail(SWIGLU_ERR_MISALIGNED, "gate: a pointer is not aligned to its element");
+    if (!renormalize && astride(logits, ld, dlogits, lddl, T))
+        return fail(SWIGLU_ERR_INVALID_ARG, "gate: dlogits is in the logits' place with another row stride");
     int sms;
     rc = device_sms(&sms);
     if (rc != SWIGLU_OK) return rc;

@@ -660,6 +660,8 @@ swiglu_status swiglu_moe_dispatch_bwd(const void* drows, int64_t lddrows, const 
     const size_t n = type_bytes(type);
     if (misaligned(drows, n) || misaligned(dx, n) || (add && misaligned(add, type_bytes(add_type))) || misaligned(pos, 4))
         return fail(SWIGLU_ERR_MISALIGNED, "dispatch: a pointer is not aligned to its element");
+    if (add == dx && (add_type != type || astride(add, ldadd, dx, lddx, T)))
+        return fail(SWIGLU_ERR_INVALID_ARG, "dispatch: dx is in add's place with another type or row stride");
     Gather a{};
     a.rows = drows, a.ldrows = lddrows, a.pos = pos, a.add = add, a.ldadd = ldadd, a.y = dx, a.ldy = lddx;
     a.D = (int)D, a.k = (int)top_k, a.n_rows = (uint32_t)n_rows;
@@ -682,6 +684,7 @@ swiglu_status swiglu_moe_combine_fwd(const void* rows, int64_t ldrows, const int
     if (misaligned(rows, n) || misaligned(y, n) || misaligned(residual, n) || misaligned(pos, 4) || misaligned(gates, 4) ||
         misaligned(step, 8))
         return fail(SWIGLU_ERR_MISALIGNED, "combine: a pointer is not aligned to its element");
+    if (astride(residual, ldr, y, ldy, T)) return fail(SWIGLU_ERR_INVALID_ARG, "combine: y is in the residual's place with another row stride");
     a.rows = rows, a.ldrows = ldrows, a.pos = pos, a.gates = gates, a.add = residual, a.ldadd = ldr, a.y = y, a.ldy = ldy;
     a.D = (int)D, a.k = (int)top_k, a.n_rows = (uint32_t)n_rows;
     return run_gather(a, SWIGLU_KERNEL_MOE_GATHER, T, type, type, a.drop.keep < 65536, static_cast<cudaStream_t>(stream));
@@ -723,6 +726,8 @@ swiglu_status swiglu_mlp_dropout(const void* x, int64_t ldx, const void* residua
     const size_t n = type_bytes(type);
     if (misaligned(x, n) || misaligned(y, n) || misaligned(residual, n) || misaligned(step, 8))
         return fail(SWIGLU_ERR_MISALIGNED, "dropout: a pointer is not aligned to its element");
+    if (astride(x, ldx, y, ldy, M) || astride(residual, ldr, y, ldy, M))
+        return fail(SWIGLU_ERR_INVALID_ARG, "dropout: y is in x's or the residual's place with another row stride");
     a.rows = x, a.ldrows = ldx, a.add = residual, a.ldadd = ldr, a.y = y, a.ldy = ldy;
     a.D = (int)D, a.k = 1;
     return run_gather(a, SWIGLU_KERNEL_DROPOUT, M, type, type, a.drop.keep < 65536, static_cast<cudaStream_t>(stream));

@@ -159,6 +159,11 @@ inline int type_bytes(int type) { return type == SWIGLU_FP32 ? 4 : type == SWIGL
 
 inline bool misaligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
+// Whether `out` begins where `in` does but its rows lie elsewhere: writing it would destroy rows not yet read.
+inline bool astride(const void* in, int64_t ld_in, const void* out, int64_t ld_out, int64_t rows) {
+    return in == out && rows > 1 && ld_in != ld_out;
+}
+
 // f.run<T>() for the run-time type.
 template <class F>
 cudaError_t with_type(int type, const F& f) {

@@ -13,7 +13,8 @@
  * stride; a pointer needs only its element's alignment, and rows on 16-byte boundaries run fastest.
  * No entry point needs a workspace, copies to the host or waits for the device, and each is fit for
  * stream capture.  All sums have a fixed order: the same call returns the same bits on every run.
- * An output may share memory with an input only where it says so.
+ * An output may share memory with an input only where it says so; in its place with another row
+ * stride or type it is refused (SWIGLU_ERR_INVALID_ARG).
  */
 #ifndef SWIGLU_TOKENS_H
 #define SWIGLU_TOKENS_H
@@ -105,6 +106,7 @@ swiglu_status swiglu_moe_dispatch_bwd(const void* drows, int64_t lddrows, const 
  *   y_t = residual_t + dropout(sum_j gates_tj rows[pos_tj])   over pairs with pos in 0 .. n_rows - 1
  * summed in fp32 by rising j, rounded once.  Rows and gates of other pairs are not read.
  *   rows [n_rows, D], residual, y [T, D]   `type`; residual NULL: none; y may be residual itself
+ *                                          (the same stride)
  *   pos [T, top_k] int32, gates [T, top_k] fp32
  */
 swiglu_status swiglu_moe_combine_fwd(const void* rows, int64_t ldrows, const int32_t* pos, const float* gates,
