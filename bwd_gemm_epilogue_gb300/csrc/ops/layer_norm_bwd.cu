@@ -627,6 +627,8 @@ swiglu_status swiglu_mlp_layer_norm_bwd(const void* dy, int64_t lddy, const void
     if (misaligned(dy, n) || misaligned(s, n) || misaligned(dskip, n) || misaligned(dx, n) || misaligned(gamma, np) ||
         misaligned(mean, 4) || misaligned(rstd, 4) || !aligned16(workspace))
         return fail(SWIGLU_ERR_MISALIGNED, "layer norm: a pointer is not aligned to its element, or the workspace to 16 bytes");
+    if (astride(dy, lddy, dx, lddx, M) || astride(s, lds, dx, lddx, M) || astride(dskip, ldskip, dx, lddx, M))
+        return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: dx is in an input's place with another row stride");
     if (workspace_bytes < swiglu_mlp_layer_norm_bwd_workspace_size(M, D))
         return fail(SWIGLU_ERR_WORKSPACE_TOO_SMALL, "layer norm: workspace smaller than the size query returns");
     rc = device_sms(&sms);

@@ -430,6 +430,8 @@ swiglu_status swiglu_mlp_layer_norm_fwd(const void* x, int64_t ldx, const void* 
     if (misaligned(x, n) || misaligned(y, n) || misaligned(residual, n) || misaligned(s, n) || misaligned(gamma, np) ||
         misaligned(beta, np) || misaligned(mean, 4) || misaligned(rstd, 4))
         return fail(SWIGLU_ERR_MISALIGNED, "layer norm: a pointer is not aligned to its element");
+    if (astride(x, ldx, y, ldy, M) || astride(x, ldx, s, lds, M) || astride(residual, ldr, y, ldy, M) || astride(residual, ldr, s, lds, M))
+        return fail(SWIGLU_ERR_INVALID_ARG, "layer norm: an output is in an input's place with another row stride");
     int sms;
     rc = device_sms(&sms);
     if (rc != SWIGLU_OK) return rc;

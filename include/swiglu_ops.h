@@ -36,8 +36,8 @@ typedef enum { SWIGLU_BF16 = 0, SWIGLU_FP16 = 1, SWIGLU_FP32 = 2 } swiglu_dtype;
  * of the sum of magnitudes at every width; each output is rounded once.
  * 1 <= D < 2^28, 0 <= M < 2^31, eps >= 0.
  * In place: s and y may each be x or residual itself (the same pointer and row stride; then
- * that input is overwritten), but not both the same.  No other outputs may overlap inputs or
- * one another.
+ * that input is overwritten; with another row stride the call is refused), but not both the
+ * same.  No other outputs may overlap inputs or one another.
  */
 swiglu_status swiglu_mlp_layer_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                         const void* gamma, const void* beta, void* y, int64_t ldy, void* s,
@@ -63,7 +63,8 @@ size_t swiglu_mlp_layer_norm_bwd_workspace_size(int64_t M, int64_t D);
  * dgamma and dbeta are summed in fp32 in an order that depends on M, D, the type, dskip's
  * presence and the alignment only: the same call returns the same bits on every run.  M = 0
  * zeroes them.
- * In place: dx may be dy, s or dskip itself (the same pointer and row stride).
+ * In place: dx may be dy, s or dskip itself (the same pointer and row stride; with another stride
+ * the call is refused).
  */
 swiglu_status swiglu_mlp_layer_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const void* gamma,
                                         const float* mean, const float* rstd, const void* dskip, int64_t ldskip,
