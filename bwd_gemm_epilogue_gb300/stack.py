@@ -6,7 +6,8 @@ kept) and preact_l -- the drop-h saved-tensor policy applied to every layer
 ("SwiGLU MLP Drop-H technical report", 4-layer stack memory table).  Backward
 walks the layers in reverse; each layer's dx is the next (lower) layer's dy.
 Every product runs in the library's kernels through the C ABI.  With dropout, y_l =
-dropout(block_l(y_{l-1})) in place, and the backward computes each layer's mask again.
+dropout(block_l(y_{l-1})) in place, and the backward computes each layer's mask again.  Every buffer is the
+stack's own, so both directions can be captured into a graph.
 """
 from __future__ import annotations
 
@@ -19,10 +20,11 @@ class SwiGLUStack:
     def __init__(self, layers, M: int, device=None, dropout: float = 0.0, seed: int = 0):
         """layers: list of (W1 [2H,D], W2 [Dout,H]) CUDA bf16 tensors with D == Dout.  dropout:
         probability of dropping an element of a layer's output; the masks follow from seed, the number of the
-        forward call and the layer."""
+        forward call (``calls`` so far, which a resumed run sets) or forward's step, and the layer."""
         if not 0 <= dropout <= 1:
             raise ValueError(f"dropout: {dropout}, expected 0 .. 1")
         self.dropout, self.seed, self.calls = dropout, seed, 0
+        self._masks = None
         self.layers = layers
         self.M = M
         W1, W2 = layers[0]
@@ -43,28 +45,41 @@ class SwiGLUStack:
         self.ws_b = torch.empty(max(16, binding.swiglu_mlp_bwd_workspace_size(M, self.D, self.H, self.Dout)),
                                 dtype=torch.uint8, device=self.dev)
 
-    def forward(self, x):
+    def forward(self, x, step=None):
+        """step: an int64 scalar on the device, 0 .. 2**47 - 1, that takes the place of the number of the call in
+        the masks.  A captured graph has to have one, and its user to advance it from replay to replay; it is
+        left alone between a forward and its backward."""
+        self._masks = self._masks_of(step) if self.dropout else None
+        self._check_capture()
         self.acts[0].copy_(x)
         self.calls += 1
         for l, (W1, W2) in enumerate(self.layers):
             binding.swiglu_mlp_fwd(self.acts[l], W1, W2, self.preacts[l], self.acts[l + 1], self.ws_f)
-            if self.dropout:
-                binding.swiglu_mlp_dropout(self.acts[l + 1], self.dropout, self.seed, self._mask(l), y=self.acts[l + 1])
+            if self._masks:
+                binding.swiglu_mlp_dropout(self.acts[l + 1], y=self.acts[l + 1], **self._masks[l])
         return self.acts[-1]
 
-    def _mask(self, l: int) -> int:
-        return self.calls * len(self.layers) + l
+    def _masks_of(self, step):
+        """The dropout's arguments for each layer.  With a step the masks are far from those of any call's number."""
+        L = len(self.layers)
+        offsets = [(self.calls + 1) * L + l if step is None else (l << 48) + (1 << 47) for l in range(L)]
+        return [dict(p=self.dropout, seed=self.seed, offset=o, step=step) for o in offsets]
+
+    def _check_capture(self):
+        """The number of the call would be a constant of a captured graph."""
+        if self._masks and self._masks[0]["step"] is None and torch.cuda.is_current_stream_capturing():
+            raise ValueError("step: a captured forward with dropout needs one, or every replay drops the same elements")
 
     def backward(self, dy):
         """Returns (dx of the stack input, [(dW1_l, dW2_l) for each layer])."""
+        self._check_capture()
         cur = dy
         for l in range(len(self.layers) - 1, -1, -1):
             W1, W2 = self.layers[l]
             dW1, dW2 = self.grads[l]
             out = self.dacts[l % 2]
-            if self.dropout:       # the caller's dy stays as it is
-                cur = binding.swiglu_mlp_dropout(cur, self.dropout, self.seed, self._mask(l),
-                                                 y=self.dacts[(l + 1) % 2] if cur is dy else cur)
+            if self._masks:        # the caller's dy stays as it is
+                cur = binding.swiglu_mlp_dropout(cur, y=self.dacts[(l + 1) % 2] if cur is dy else cur, **self._masks[l])
             binding.swiglu_mlp_bwd(self.acts[l], W1, W2, self.preacts[l], cur, out, dW1, dW2, self.ws_b)
             cur = out
         return cur, self.grads
