@@ -1259,6 +1259,11 @@ def swiglu_mlp_dropout(x, p: float, seed: int, offset: int = 0, step=None, resid
     return y
 
 
+def draw_seed() -> int:
+    """A seed for masks, from torch's default generator on the host (torch.manual_seed)."""
+    return int(torch.randint(1 << 62, (), device="cpu"))
+
+
 class Dropout(torch.autograd.Function):
     """autograd wrapper: the backward computes the mask again.  Leading dimensions are flattened."""
 

@@ -22,9 +22,12 @@ class PreNormMoE:
     """gamma, beta [D], router [E, D] (fp32 or bf16), W1 [E, 2H, D], W2 [E, D, H] bf16 CUDA tensors or
     Parameters; the block has a backward of its own, and autograd sees nothing of it."""
 
-    def __init__(self, gamma, beta, router, W1, W2, top_k: int, eps: float = 1e-5, dropout: float = 0.0, seed: int = 0):
+    def __init__(self, gamma, beta, router, W1, W2, top_k: int, eps: float = 1e-5, dropout: float = 0.0,
+                 seed: int | None = None, layer: int = 0):
         """dropout: probability of dropping an element of the experts' sum in training (not in
-        decode); the masks follow from seed and the number of the forward call."""
+        decode).  The masks follow from seed, layer (0 .. 65535) and the number of the forward call (``calls``
+        so far, which a resumed run sets, and ``seed``): the blocks of one model need a seed or a layer each.  Without a
+        seed the block draws one of its own with torch's default generator."""
         E, H2, D = W1.shape
         if W2.shape != (E, D, H2 // 2) or router.shape != (E, D) or gamma.shape != (D,) or beta.shape != (D,):
             raise ValueError(f"shape mismatch: gamma {tuple(gamma.shape)}, beta {tuple(beta.shape)}, router "
@@ -33,9 +36,13 @@ class PreNormMoE:
             raise ValueError(f"top_k: {top_k}, expected 1 .. {E}")
         if not 0 <= dropout <= 1:
             raise ValueError(f"dropout: {dropout}, expected 0 .. 1")
+        if not 0 <= layer < 1 << 16:
+            raise ValueError(f"layer: {layer}, expected 0 .. 65535")
+        if dropout and seed is None:
+            seed = binding.draw_seed()
         self.params = [gamma, beta, router, W1, W2]
         self.top_k, self.eps = top_k, eps
-        self.dropout, self.seed, self.calls = dropout, seed, 0
+        self.dropout, self.seed, self.layer, self.calls = dropout, seed, layer, 0
         self.grads = None
         self._saved = None
 
@@ -50,7 +57,9 @@ class PreNormMoE:
         counts = counts.tolist()
         xg = binding.swiglu_moe_dispatch_fwd(xn, pos, sum(counts))
         preact, rows = binding.swiglu_moe_fwd(xg, W1, W2, counts)
-        mask = dict(p=self.dropout, seed=self.seed, offset=self.calls)
+        if self.dropout and self.seed is None:             # dropout set since
+            self.seed = binding.draw_seed()
+        mask = dict(p=self.dropout, seed=self.seed or 0, offset=(self.layer << 48) + self.calls)
         y = binding.swiglu_moe_combine_fwd(rows, pos, gates, residual=x, **mask)
         self.calls += 1
         self._saved = (x, xn, mean, rstd, ids.long(), gates, logits, counts, xg, preact, rows, ids, pos, mask)

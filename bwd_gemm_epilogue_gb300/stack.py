@@ -17,12 +17,15 @@ from . import binding
 
 
 class SwiGLUStack:
-    def __init__(self, layers, M: int, device=None, dropout: float = 0.0, seed: int = 0):
+    def __init__(self, layers, M: int, device=None, dropout: float = 0.0, seed: int | None = None):
         """layers: list of (W1 [2H,D], W2 [Dout,H]) CUDA bf16 tensors with D == Dout.  dropout:
         probability of dropping an element of a layer's output; the masks follow from seed, the number of the
-        forward call (``calls`` so far, which a resumed run sets) or forward's step, and the layer."""
+        forward call (``calls`` so far, which a resumed run sets, and ``seed``) or forward's step, and the
+        layer.  Without a seed the stack draws one of its own with torch's default generator."""
         if not 0 <= dropout <= 1:
             raise ValueError(f"dropout: {dropout}, expected 0 .. 1")
+        if dropout and seed is None:
+            seed = binding.draw_seed()
         self.dropout, self.seed, self.calls = dropout, seed, 0
         self._masks = None
         self.layers = layers
@@ -61,6 +64,8 @@ class SwiGLUStack:
 
     def _masks_of(self, step):
         """The dropout's arguments for each layer.  With a step the masks are far from those of any call's number."""
+        if self.seed is None:      # dropout set since
+            self.seed = binding.draw_seed()
         L = len(self.layers)
         offsets = [(self.calls + 1) * L + l if step is None else (l << 48) + (1 << 47) for l in range(L)]
         return [dict(p=self.dropout, seed=self.seed, offset=o, step=step) for o in offsets]
