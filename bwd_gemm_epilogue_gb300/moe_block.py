@@ -44,7 +44,12 @@ class PreNormMoE:
         self.top_k, self.eps = top_k, eps
         self.dropout, self.seed, self.layer, self.calls = dropout, seed, layer, 0
         self.grads = None
-        self._saved = None
+        self._kept = None
+
+    @property
+    def _saved(self):
+        """What the last forward kept, and after rstd its experts in torch's index type, which no kernel needs."""
+        return (*self._kept[:4], self._kept[-3].long(), *self._kept[4:])
 
     @torch.no_grad()
     def forward(self, x):
@@ -62,14 +67,14 @@ class PreNormMoE:
         mask = dict(p=self.dropout, seed=self.seed or 0, offset=(self.layer << 48) + self.calls)
         y = binding.swiglu_moe_combine_fwd(rows, pos, gates, residual=x, **mask)
         self.calls += 1
-        self._saved = (x, xn, mean, rstd, ids.long(), gates, logits, counts, xg, preact, rows, ids, pos, mask)
+        self._kept = (x, xn, mean, rstd, gates, logits, counts, xg, preact, rows, ids, pos, mask)
         return y
 
     @torch.no_grad()
     def backward(self, dy):
         """dy [T, D] bf16 -> dx; leaves the parameters' gradients in self.grads."""
         gamma, _, router, W1, W2 = self.params
-        x, xn, mean, rstd, _, gates, logits, counts, xg, preact, rows, ids, pos, mask = self._saved
+        x, xn, mean, rstd, gates, logits, counts, xg, preact, rows, ids, pos, mask = self._kept
         drows, dgates = binding.swiglu_moe_combine_bwd(dy, rows, pos, gates, **mask)
         dxg, dW1, dW2 = binding.swiglu_moe_bwd(xg, W1, W2, preact, drows, counts)
         dlogits = binding.swiglu_moe_gate_bwd(logits, ids, gates, dgates)
