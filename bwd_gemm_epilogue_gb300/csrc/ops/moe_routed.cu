@@ -34,8 +34,8 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "../host.h"
 #include "convert.cuh"
+#include "launch.cuh"
 #include "swiglu_moe.h"
 
 namespace swiglu {

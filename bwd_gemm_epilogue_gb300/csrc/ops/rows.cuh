@@ -2,7 +2,7 @@
 // have in common.
 #pragma once
 
-#include "../host.h"
+#include "launch.cuh"
 #include "convert.cuh"
 #include "swiglu_ops.h"
 
