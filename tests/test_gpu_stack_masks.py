@@ -61,6 +61,7 @@ def test_a_captured_call_needs_a_step(stack):
     before = results(st, dy)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
+        dy + x
         for call in (lambda: st.forward(x), lambda: st.backward(dy)):
             with pytest.raises(ValueError, match="step"):
                 call()
