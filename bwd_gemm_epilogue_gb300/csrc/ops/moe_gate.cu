@@ -1,10 +1,12 @@
 // moe_gate.cu -- the choice of experts from the router's logits and its gradient, and the (token,
 // choice) pairs sorted by expert (include/swiglu_tokens.h).
 //
-// One GB300, device times: the choice of 8 of 128 experts for 65536 tokens (fp32, 38 MB) 12.6 us (bf16 11.3),
-// bound by integer instructions (about 140 a token, two thirds of that pipe busy); its gradient 7.3 us, and
-// 11.7 where it needs all experts' probabilities (75 MB), both near HBM's rate; 40961 tokens of 61 experts,
-// bf16, 5.8 us.  The sort of 16384 pairs 4.7 us, of 131072 9.1 us.
+// One GB300, device times: the choice of 8 of 128 experts for 65536 tokens (fp32, 38 MB) 12.8 us (bf16 11.3;
+// 64 experts 8.7, 8.5).  Nothing is saturated: 147 instructions a token keep the integer pipe 66 % and the issue
+// slots 50 % busy, with 41 % of an SM's warps (64 registers) and HBM at 26 %; each round waits for the one
+// before.  Its gradient 7.1 us, and 12 where it needs all experts' probabilities (75 MB), both near HBM's rate;
+// 40961 tokens of 61 experts, bf16, 5.8 us for 2.0 of traffic, 2-byte accesses.  The sort of 16384 pairs 4.7 us, of
+// 131072 9.1, of 1048576 43 to 55 (64 and 682 experts).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -188,7 +190,7 @@ __device__ __noinline__ void choose_by_keys(const Gate& a, int64_t t) {
     for (int j = last - G; j >= 0; j -= G) gates[j] = gates[j] < 0.f ? 0.f : gates[j] / by;
 }
 
-// top_k of more than 32 (4096 tokens, 40 of 512 experts: 34 us, a maximum over the warp and a pass over the
+// top_k of more than 32 (4096 tokens, 40 of 512 experts: 34 us for 1.5 of traffic, a maximum over the warp and a pass over the
 // lane's keys for each choice).
 template <class T, int OWN>
 __global__ void __launch_bounds__(kGateThreads) moe_gate_fwd_keys_kernel(const __grid_constant__ Gate a) {
@@ -543,8 +545,8 @@ struct LaunchGate {
             if (a.k > G) return launch_early(moe_gate_fwd_keys_kernel<T, OWN>, grid, kGateThreads, 0, s, a);
         return launch_early(moe_gate_fwd_kernel<T, OWN, G>, grid, kGateThreads, 0, s, a);
     }
-    // Few lanes a token share out its fixed costs best (65536 tokens, 8 of 128 experts, fp32: 15.5 us with 8
-    // lanes, 23.8 with 32, when it was measured): as many as there are choices, each with up to 16 experts.
+    // Few lanes a token share out its fixed costs best (65536 tokens, 8 of 128 experts, fp32, in L2: 12.0 us with
+    // 8 lanes, 22.1 with 32; of 64 experts 8.7 and 21.9): as many as there are choices, each with up to 16 experts.
     template <class T>
     cudaError_t run() const {
         if (a.k <= 8 && a.E <= 128) return a.E <= 16 ? go<T, 2, 8>() : a.E <= 32 ? go<T, 4, 8>() : a.E <= 64 ? go<T, 8, 8>() : go<T, 16, 8>();

@@ -4,7 +4,7 @@
 // All of them move rows and compute little, so HBM bounds them where rows are whole 16-byte packs; one
 // GB300, copies at 6.7 TB/s, device times without the launch's latency, which runs beside the kernel
 // before (launch_early):
-//   dispatch   8192 tokens to 2 of 8 experts, 4096 bf16 columns      31 us, 6.5 TB/s (with the sort 34)
+//   dispatch   8192 tokens to 2 of 8 experts, 4096 bf16 columns      30 us, 6.7 TB/s (with the sort 35)
 //   combine    4096 tokens of 6 experts, 2048 bf16, dropout          24.8 us, 5.4 TB/s
 //              8192 tokens of 2, 4096 bf16                           41.5 us, 6.5 TB/s
 //   gradient   8192 tokens of 2, 4096 bf16, dropout                  49.6 us, 6.8 TB/s
@@ -13,8 +13,10 @@
 // first, is as many threads as an SM holds: two rows in flight a thread at 32 registers (combine above,
 // 4 in flight at 40 and 48 registers: 28 and 27 us).  Rows off 16-byte boundaries start at another place
 // of a pack each: those are put together from aligned pieces, about 20 instructions for 16 bytes, and
-// these bound them (7 choices of 1021 columns, 4099 tokens: combine bf16 22.5 us for 10.4 of traffic, its
-// gradient fp16 24.5 for 17.1); fp32 rows, which are moved a column a thread instead, 24.9 for 20.8.
+// these bound them (7 choices of 1021 columns, a tenth of them absent, 4099 tokens: combine bf16 with
+// dropout 22.5 us for 10.4 of traffic, its gradient fp16 24.5 to 26.4 from GPU to GPU for 17.1; 2 of 4095 columns,
+// 8192 tokens: combine 64 for 40.2, its gradient 68 for 50.2); fp32 rows, which are moved a column a thread
+// instead: the dispatch's gradient 24.9 for 20.8, the combine's 39 for 34.1.
 #include <algorithm>
 #include <type_traits>
 
@@ -203,8 +205,8 @@ __device__ __forceinline__ void scatter_packs(const Scatter& a, const int* pos, 
 }
 
 // rows[pos_tj] = x_t, a pack of x a thread, read once and written to each of its rows: HBM, 6.5 TB/s;
-// kShifted: a pack of each of the token's rows, whose boundaries differ (8192 tokens to 2 of 4095 bf16 columns 39
-// us for 30 of traffic).
+// kShifted: a pack of each of the token's rows, whose boundaries differ (8192 tokens to 2 of 4095 bf16 columns 41
+// us for 30 of traffic, with the sort 44).
 template <class T, Lie LIE>
 __global__ void __launch_bounds__(kThreads) moe_scatter_kernel(const __grid_constant__ Scatter a) {
     after_previous();
@@ -252,7 +254,7 @@ __device__ __forceinline__ float warp_sums(float v0, float v1) {
 
 // The combine's gradient: with e = drop(dy_t), drows[pos_tj] = g_tj e and dgates_tj = <e, rows[pos_tj]>.
 // A CTA a token.  Up to CHOICES choices: all of them at a time, their sums in registers, so a token's
-// gradient and its dropout are read and computed once (4096 tokens of 6 experts of 2048 bf16, p 0.1: 36.0 us
+// gradient and its dropout are read and computed once (4096 tokens of 6 experts of 2048 bf16, p 0.1: 37 us
 // for 32.7 of traffic, two at a time 38.3; the CTAs an SM as they measured best: 8192 tokens of 2, 51 us at 6,
 // 52 at 5).
 template <class T, Lie LIE, bool DROP, int CHOICES>
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, CHOICES == 2 ? 6 : CHOICES == 4 ? 4 
 }
 
 // More choices: two at a time for each pack of dy_t, so that it and its dropout are computed once; `part`: a
-// sum a warp for each choice (2048 tokens of 16 of 2048 bf16 columns, dropout: 48 us for 41.5 of traffic).
+// sum a warp for each choice (2048 tokens of 16 of 2048 bf16 columns, dropout: 49 us for 41.5 of traffic).
 template <class T, Lie LIE, bool DROP>
 __global__ void __launch_bounds__(kThreads, 6) moe_combine_bwd_kernel(const __grid_constant__ Scatter a) {
     after_previous();
